@@ -275,6 +275,24 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
                             size_t workspace_bytes, void *hip_stream);
 
 /*
+ * msr_layer_step with 4-bit weights (linear_w4 of recurrent.h says how they are
+ * stored): a step of few sequences is bound by reading its weights, a quarter of the
+ * bf16 ones here.  The four projections are one matrix, rows in the order
+ * W_Q, W_K, W_V, W_G.
+ *   in_q [2 H dk + 2 H dv, d_model / 2], in_scale, in_zero [2 H dk + 2 H dv, d_model / in_group]
+ *   o_q [d_model, H dv / 2], o_scale, o_zero [d_model, H dv / o_group]   (zeros or NULL)
+ * Everything else, the step's mathematics included, as msr_layer_step; no library
+ * GEMM is called.
+ */
+size_t msr_layer_step_w4_workspace_bytes(int B, int d_model, int H, int dk, int dv);
+ret_status_t msr_layer_step_w4(const void *x, const void *in_q, const void *in_scale,
+                               const void *in_zero, int in_group, const void *o_q,
+                               const void *o_scale, const void *o_zero, int o_group, void *y,
+                               float *state, int *pos, int advance_pos, int B, int d_model, int H,
+                               int dk, int dv, const float *gamma, const float *theta, float gn_eps,
+                               void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
  * The pre-LN residual block around the gated layer (paper summary, the block
  * equations; FFN(X) = gelu(X W_1) W_2), bf16 in and out:
  *   Y = MSR(LN(X)) + X,   out = FFN(LN(Y)) + Y

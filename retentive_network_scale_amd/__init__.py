@@ -8,6 +8,9 @@ functions raises.
 Functions (same names as the C ABI):
     retention_parallel, retention_chunkwise, retention_chunkwise_workspace_bytes,
     retention_recurrent_step, msr_layer_fwd, msr_layer_fwd_workspace_bytes
+and, declared in include/recurrent.h and bound in recurrent.py,
+    selective_scan, selective_scan_bwd, selective_scan_step, causal_conv1d,
+    causal_conv1d_bwd, causal_conv1d_step, linear_w4
 """
 import ctypes
 import os
@@ -23,6 +26,11 @@ __all__ = [
     "retnet_block_fwd",
     "retnet_block_fwd_workspace_bytes", "LIB_PATH",
     "EXPORTED_SYMBOLS",
+    "msr_layer_step_w4", "msr_layer_step_w4_workspace_bytes",
+    "selective_scan", "selective_scan_workspace_bytes", "selective_scan_bwd", "selective_scan_bwd_workspace_bytes",
+    "selective_scan_step", "SelectiveScanGrads", "causal_conv1d", "causal_conv1d_bwd",
+    "causal_conv1d_bwd_workspace_bytes", "causal_conv1d_step", "CausalConvGrads", "linear_w4", "pack_w4",
+    "RECURRENT_SYMBOLS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretention.so")
@@ -60,8 +68,26 @@ _SIGS = {
                               _fp, _ll, _f, _f, _vp, _sz, _vp]),
     "msr_layer_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _fp, _fp,
                             _f, _vp, _sz, _vp]),
+    "msr_layer_step_w4_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "msr_layer_step_w4": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                               _fp, _fp, _f, _vp, _sz, _vp]),
 }
 EXPORTED_SYMBOLS = tuple(_SIGS)
+
+# the same, mirroring include/recurrent.h
+_RECURRENT_SIGS = {
+    "selective_scan_workspace_bytes": (_sz, [_i] * 5),
+    "selective_scan": (_i, [_vp] * 12 + [_i] * 5 + [_ll] * 5 + [_i] * 3 + [_vp, _sz, _vp]),
+    "selective_scan_bwd_workspace_bytes": (_sz, [_i] * 5),
+    "selective_scan_bwd": (_i, [_vp] * 21 + [_i] * 5 + [_ll] * 5 + [_i] * 3 + [_vp, _sz, _vp]),
+    "selective_scan_step": (_i, [_vp] * 10 + [_i] * 4 + [_ll] * 5 + [_i] * 3 + [_vp]),
+    "causal_conv1d": (_i, [_vp] * 7 + [_i] * 4 + [_ll, _i, _i, _vp]),
+    "causal_conv1d_bwd_workspace_bytes": (_sz, [_i] * 4),
+    "causal_conv1d_bwd": (_i, [_vp] * 11 + [_i] * 4 + [_ll, _i, _i, _vp, _sz, _vp]),
+    "causal_conv1d_step": (_i, [_vp] * 5 + [_i] * 3 + [_ll, _i, _i, _vp]),
+    "linear_w4": (_i, [_vp] * 5 + [_i] * 4 + [_ll, _i, _vp]),
+}
+RECURRENT_SYMBOLS = tuple(_RECURRENT_SIGS)
 
 _lib = None
 
@@ -80,7 +106,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m retentive_network_scale_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGS.items():
+        for name, (res, args) in (*_SIGS.items(), *_RECURRENT_SIGS.items()):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = res, args
         _lib = L
@@ -341,3 +367,9 @@ def retnet_block_fwd(x, w_q, w_k, w_v, w_g, w_o, w_1, w_2, H, dk, dv, chunk, gam
                                   float(gn_eps), float(ln_eps), _dev(workspace, "workspace"),
                                   workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
+
+
+from .recurrent import (  # noqa: E402  (needs the helpers above)
+    CausalConvGrads, SelectiveScanGrads, causal_conv1d, causal_conv1d_bwd, causal_conv1d_bwd_workspace_bytes,
+    causal_conv1d_step, linear_w4, msr_layer_step_w4, msr_layer_step_w4_workspace_bytes, pack_w4, selective_scan,
+    selective_scan_bwd, selective_scan_bwd_workspace_bytes, selective_scan_step, selective_scan_workspace_bytes)

@@ -63,6 +63,14 @@ int resident_chunk_max(int dk);
 hipError_t blaslt_gemm_nt(const uint16_t *X, const uint16_t *W, void *C, int T, int N, int K, int ldc, void *ws,
                           size_t ws_bytes, hipStream_t st, const uint16_t *R = nullptr, bool out_f32 = false);
 
+// Products with 4-bit weights (linear_w4.hip): out [M, N] = x [M, K] W^T, arguments as
+// linear_w4's, already checked (q, scale, N, K and group by w4_refusal: the reason to
+// refuse them, or nullptr).
+constexpr int W4_MAX_ROWS = 65535 * 16;  // M, by the launch grid
+const char *w4_refusal(const void *q, const void *scale, int N, int K, int group, bool *unsupported);
+hipError_t launch_w4(const void *x, const void *q, const void *scale, const void *zero, void *out, int M, int N, int K,
+                     int group, long long x_ld, bool out_bf16, hipStream_t st);
+
 // Row-wise bf16 passes of the residual block (block.hip): LayerNorm without
 // affine (y may alias x) and exact gelu in place.
 hipError_t launch_layernorm_bf16(const uint16_t *x, uint16_t *y, long long rows, int d, float eps, hipStream_t st);

@@ -17,6 +17,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "recurrent.hpp"
 #include "retention.h"
 
 using namespace ret;
@@ -85,9 +86,6 @@ hipError_t projections(bool step, const uint16_t *X, const void *w_q, const void
 }
 
 }  // namespace
-
-// Defined in abi.hip: records the message returned by retention_last_error().
-ret_status_t retention_fail_(ret_status_t s, const char *msg);
 
 // Status of a failed launch sequence: a GEMM shape for which hipBLASLt offers no
 // algorithm is UNSUPPORTED (nothing of the call was enqueued after it), anything
@@ -162,6 +160,82 @@ static ret_status_t msr_forward(const void *x, const void *w_q, const void *w_k,
 }
 
 
+// Sizes, decay and rotation of a decode step, with bf16 or 4-bit weights.
+static ret_status_t check_step_sizes(int B, int d_model, int H, int dk, int dv, const float *gamma, const float *theta,
+                                     float gn_eps) {
+  if (B <= 0 || H <= 0 || d_model <= 0 || dk <= 0 || dv <= 0)
+    return retention_fail_(RET_ERR_INVALID_ARG, "sizes must be positive");
+  if (!gamma) return retention_fail_(RET_ERR_INVALID_ARG, "gamma is NULL");
+  if (H > RETENTION_MAX_HEADS || dk > RETENTION_MAX_DK || dv > RETENTION_MAX_DV)
+    return retention_fail_(RET_ERR_UNSUPPORTED, "too many heads or head size too large");
+  for (int h = 0; h < H; ++h)
+    if (!(gamma[h] >= 0.0f && gamma[h] <= 1.0f)) return retention_fail_(RET_ERR_INVALID_ARG, "gamma outside [0,1]");
+  if (theta) {
+    if (dk % 2) return retention_fail_(RET_ERR_INVALID_ARG, "rotation needs an even dk");
+    for (int i = 0; i < dk / 2; ++i)
+      if (!std::isfinite(theta[i])) return retention_fail_(RET_ERR_INVALID_ARG, "theta not finite");
+  }
+  if (!(gn_eps >= 0.0f) || !std::isfinite(gn_eps))
+    return retention_fail_(RET_ERR_INVALID_ARG, "gn_eps must be finite and >= 0 (the layer always normalises)");
+  if (d_model % 128 || (H * dk) % 128 || (H * dv) % 128 || dk % 8 || dv % 8)
+    return retention_fail_(RET_ERR_UNSUPPORTED, "d_model, H*dk and H*dv must be multiples of 128, dk and dv of 8");
+  if (dv / 4 > 256) return retention_fail_(RET_ERR_UNSUPPORTED, "dv too large for the step kernel");
+  return RET_OK;
+}
+
+static ret_status_t check_step_overlap(const void *x, const void *y, const float *state, const void *workspace,
+                                       size_t need, int B, int d_model, int H, int dk, int dv) {
+  const uintptr_t y0 = (uintptr_t)y, y1 = y0 + (size_t)B * d_model * 2;
+  const uintptr_t s0 = (uintptr_t)state, s1 = s0 + (size_t)B * H * dk * dv * 4;
+  const uintptr_t w0 = (uintptr_t)workspace, w1 = w0 + need, x0 = (uintptr_t)x, x1 = x0 + (size_t)B * d_model * 2;
+  if ((y0 < w1 && w0 < y1) || (y0 < x1 && x0 < y1) || (y0 < s1 && s0 < y1) || (s0 < w1 && w0 < s1) ||
+      (s0 < x1 && x0 < s1))
+    return retention_fail_(RET_ERR_INVALID_ARG, "y, state, x and the workspace must not overlap");
+  return RET_OK;
+}
+
+// The retention step between the projections P[B][NP] (fp32) and Z[B][H*dv]: GroupNorm and the swish gate in it.
+static hipError_t step_retention(const float *proj, uint16_t *z, float *state, const int *pos, int B, int H, int dk,
+                                 int dv, const float *gamma, const float *theta, float gn_eps, hipStream_t st) {
+  const long long NP = 2LL * H * dk + 2LL * H * dv;
+  const long long cq = 0, ck = (long long)H * dk, cv = 2LL * H * dk, cg = cv + (long long)H * dv;
+  RetArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = proj + cq;
+  a.k = proj + ck;
+  a.v = proj + cv;
+  a.o = z;
+  a.gate = (const uint16_t *)(proj + cg);
+  a.gate_swish = 1;
+  a.q_sb = NP;
+  a.q_sh = dk;
+  a.q_sn = dk;
+  a.v_sb = NP;
+  a.v_sh = dv;
+  a.v_sn = dv;
+  a.g_sb = NP;
+  a.g_sh = dv;
+  a.g_sn = dv;
+  a.o_sb = (long long)H * dv;
+  a.o_sh = dv;
+  a.o_sn = dv;
+  a.B = B;
+  a.H = H;
+  a.L = 1;
+  a.dk = dk;
+  a.dv = dv;
+  a.chunk = 1;
+  a.in_bf16 = 0;
+  a.out_bf16 = 1;
+  a.use_theta = theta != nullptr;
+  a.use_gn = 1;
+  a.gn_eps = gn_eps;
+  for (int h = 0; h < H; ++h) a.gamma[h] = gamma[h];
+  if (theta)
+    for (int i = 0; i < dk / 2; ++i) a.theta[i] = theta[i];
+  return launch_vec_step(a, state, pos, st);
+}
+
 extern "C" {
 
 size_t msr_layer_fwd_workspace_bytes(int B, int L, int d_model, int H, int dk, int dv, int chunk) {
@@ -228,23 +302,8 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
                             const void *w_o, void *y, float *state, int *pos, int advance_pos, int B, int d_model,
                             int H, int dk, int dv, const float *gamma, const float *theta, float gn_eps,
                             void *workspace, size_t workspace_bytes, void *hip_stream) {
-  if (B <= 0 || H <= 0 || d_model <= 0 || dk <= 0 || dv <= 0)
-    return retention_fail_(RET_ERR_INVALID_ARG, "sizes must be positive");
-  if (!gamma) return retention_fail_(RET_ERR_INVALID_ARG, "gamma is NULL");
-  if (H > RETENTION_MAX_HEADS || dk > RETENTION_MAX_DK || dv > RETENTION_MAX_DV)
-    return retention_fail_(RET_ERR_UNSUPPORTED, "too many heads or head size too large");
-  for (int h = 0; h < H; ++h)
-    if (!(gamma[h] >= 0.0f && gamma[h] <= 1.0f)) return retention_fail_(RET_ERR_INVALID_ARG, "gamma outside [0,1]");
-  if (theta) {
-    if (dk % 2) return retention_fail_(RET_ERR_INVALID_ARG, "rotation needs an even dk");
-    for (int i = 0; i < dk / 2; ++i)
-      if (!std::isfinite(theta[i])) return retention_fail_(RET_ERR_INVALID_ARG, "theta not finite");
-  }
-  if (!(gn_eps >= 0.0f) || !std::isfinite(gn_eps))
-    return retention_fail_(RET_ERR_INVALID_ARG, "gn_eps must be finite and >= 0 (the layer always normalises)");
-  if (d_model % 128 || (H * dk) % 128 || (H * dv) % 128 || dk % 8 || dv % 8)
-    return retention_fail_(RET_ERR_UNSUPPORTED, "d_model, H*dk and H*dv must be multiples of 128, dk and dv of 8");
-  if (dv / 4 > 256) return retention_fail_(RET_ERR_UNSUPPORTED, "dv too large for the step kernel");
+  const ret_status_t checked = check_step_sizes(B, d_model, H, dk, dv, gamma, theta, gn_eps);
+  if (checked != RET_OK) return checked;
   if (!x || !w_q || !w_k || !w_v || !w_g || !w_o || !y || !state || !pos)
     return retention_fail_(RET_ERR_INVALID_ARG, "NULL pointer");
   const void *ptrs[] = {x, w_q, w_k, w_v, w_g, w_o, y, state, workspace};
@@ -252,14 +311,8 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
     if ((uintptr_t)p & 15u) return retention_fail_(RET_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
   const size_t need = msr_layer_step_workspace_bytes(B, d_model, H, dk, dv);
   if (!workspace || workspace_bytes < need) return retention_fail_(RET_ERR_WORKSPACE, "workspace too small");
-  {
-    const uintptr_t y0 = (uintptr_t)y, y1 = y0 + (size_t)B * d_model * 2;
-    const uintptr_t s0 = (uintptr_t)state, s1 = s0 + (size_t)B * H * dk * dv * 4;
-    const uintptr_t w0 = (uintptr_t)workspace, w1 = w0 + need, x0 = (uintptr_t)x, x1 = x0 + (size_t)B * d_model * 2;
-    if ((y0 < w1 && w0 < y1) || (y0 < x1 && x0 < y1) || (y0 < s1 && s0 < y1) || (s0 < w1 && w0 < s1) ||
-        (s0 < x1 && x0 < s1))
-      return retention_fail_(RET_ERR_INVALID_ARG, "y, state, x and the workspace must not overlap");
-  }
+  const ret_status_t apart = check_step_overlap(x, y, state, workspace, need, B, d_model, H, dk, dv);
+  if (apart != RET_OK) return apart;
   hipStream_t st = (hipStream_t)hip_stream;
   char *ws = (char *)workspace;
   const long long NP = 2LL * H * dk + 2LL * H * dv;
@@ -269,7 +322,6 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
   float *proj = (float *)ws;
   uint16_t *z = (uint16_t *)(ws + align256((size_t)B * NP * 4));
   void *blas = ws + align256((size_t)B * NP * 4) + align256((size_t)B * H * dv * 2);
-  const long long cq = 0, ck = (long long)H * dk, cv = 2LL * H * dk, cg = cv + (long long)H * dv;
 
   // 1. projections of this step's tokens into P[B][NP]
   {
@@ -279,41 +331,7 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
   }
 
   // 2. retention step with GroupNorm and the swish gate -> Z[B][H*dv]
-  RetArgs a;
-  memset(&a, 0, sizeof(a));
-  a.q = proj + cq;
-  a.k = proj + ck;
-  a.v = proj + cv;
-  a.o = z;
-  a.gate = (const uint16_t *)(proj + cg);
-  a.gate_swish = 1;
-  a.q_sb = NP;
-  a.q_sh = dk;
-  a.q_sn = dk;
-  a.v_sb = NP;
-  a.v_sh = dv;
-  a.v_sn = dv;
-  a.g_sb = NP;
-  a.g_sh = dv;
-  a.g_sn = dv;
-  a.o_sb = (long long)H * dv;
-  a.o_sh = dv;
-  a.o_sn = dv;
-  a.B = B;
-  a.H = H;
-  a.L = 1;
-  a.dk = dk;
-  a.dv = dv;
-  a.chunk = 1;
-  a.in_bf16 = 0;
-  a.out_bf16 = 1;
-  a.use_theta = theta != nullptr;
-  a.use_gn = 1;
-  a.gn_eps = gn_eps;
-  for (int h = 0; h < H; ++h) a.gamma[h] = gamma[h];
-  if (theta)
-    for (int i = 0; i < dk / 2; ++i) a.theta[i] = theta[i];
-  hipError_t e = launch_vec_step(a, state, pos, st);
+  hipError_t e = step_retention(proj, z, state, pos, B, H, dk, dv, gamma, theta, gn_eps, st);
   if (e != hipSuccess) return launch_fail(e);
 
   // 3. output projection, 4. positions
@@ -323,6 +341,58 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
     e = launch_advance_pos(pos, B, st);
     if (e != hipSuccess) return launch_fail(e);
   }
+  return retention_fail_(RET_OK, "");
+}
+
+size_t msr_layer_step_w4_workspace_bytes(int B, int d_model, int H, int dk, int dv) {
+  if (B <= 0 || d_model <= 0 || H <= 0 || dk <= 0 || dv <= 0) return 0;
+  const size_t NP = 2 * (size_t)H * dk + 2 * (size_t)H * dv;
+  return align256((size_t)B * NP * 4) + align256((size_t)B * H * dv * 2);
+}
+
+// msr_layer_step with 4-bit weights: both products run in the library's own kernel, so
+// the step needs no library workspace.
+ret_status_t msr_layer_step_w4(const void *x, const void *in_q, const void *in_scale, const void *in_zero, int in_group,
+                               const void *o_q, const void *o_scale, const void *o_zero, int o_group, void *y,
+                               float *state, int *pos, int advance_pos, int B, int d_model, int H, int dk, int dv,
+                               const float *gamma, const float *theta, float gn_eps, void *workspace,
+                               size_t workspace_bytes, void *hip_stream) {
+  const ret_status_t checked = check_step_sizes(B, d_model, H, dk, dv, gamma, theta, gn_eps);
+  if (checked != RET_OK) return checked;
+  if (!x || !y || !state || !pos) return retention_fail_(RET_ERR_INVALID_ARG, "NULL pointer");
+  const void *ptrs[] = {x, y, state, workspace};
+  for (const void *p : ptrs)
+    if ((uintptr_t)p & 15u) return retention_fail_(RET_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+  if ((uintptr_t)pos & 3u) return retention_fail_(RET_ERR_INVALID_ARG, "pos is not aligned to its elements");
+  if ((long long)B * H > RETENTION_MAX_TOKEN_HEADS || B > W4_MAX_ROWS)
+    return retention_fail_(RET_ERR_UNSUPPORTED, "B*H too large");
+  const int NP = 2 * H * dk + 2 * H * dv;
+  bool unsupported = false;
+  const char *msg = w4_refusal(in_q, in_scale, NP, d_model, in_group, &unsupported);
+  if (!msg) msg = w4_refusal(o_q, o_scale, d_model, H * dv, o_group, &unsupported);
+  if (msg) return retention_fail_(unsupported ? RET_ERR_UNSUPPORTED : RET_ERR_INVALID_ARG, msg);
+  const size_t need = msr_layer_step_w4_workspace_bytes(B, d_model, H, dk, dv);
+  if (!workspace || workspace_bytes < need) return retention_fail_(RET_ERR_WORKSPACE, "workspace too small");
+  ret_status_t apart = check_step_overlap(x, y, state, workspace, need, B, d_model, H, dk, dv);
+  if (apart != RET_OK) return apart;
+  const size_t ni = (size_t)NP * (d_model / in_group), no = (size_t)d_model * (H * dv / o_group);
+  const RecSpan ins[] = {{"x", x, (size_t)B * d_model * 2}, {"in_q", in_q, (size_t)NP * (d_model / 2)},
+                         {"in_scale", in_scale, ni * 2}, {"in_zero", in_zero, ni},
+                         {"o_q", o_q, (size_t)d_model * (H * dv / 2)}, {"o_scale", o_scale, no * 2},
+                         {"o_zero", o_zero, no}};
+  const RecSpan outs[] = {{"y", y, (size_t)B * d_model * 2}, {"state", state, (size_t)B * H * dk * dv * 4},
+                          {"pos", pos, (size_t)B * 4}, {"the workspace", workspace, need}};
+  if ((apart = rec_check_overlap(ins, outs)) != RET_OK) return apart;
+  hipStream_t st = (hipStream_t)hip_stream;
+  float *proj = (float *)workspace;
+  uint16_t *z = (uint16_t *)((char *)workspace + align256((size_t)B * NP * 4));
+  hipError_t e = launch_w4(x, in_q, in_scale, in_zero, proj, B, NP, d_model, in_group, d_model, false, st);
+  if (e != hipSuccess) return launch_fail(e);
+  if ((e = step_retention(proj, z, state, pos, B, H, dk, dv, gamma, theta, gn_eps, st)) != hipSuccess)
+    return launch_fail(e);
+  if ((e = launch_w4(z, o_q, o_scale, o_zero, y, B, d_model, H * dv, o_group, (long long)H * dv, true, st)) != hipSuccess)
+    return launch_fail(e);
+  if (advance_pos && (e = launch_advance_pos(pos, B, st)) != hipSuccess) return launch_fail(e);
   return retention_fail_(RET_OK, "");
 }
 

@@ -1,0 +1,117 @@
+// Host and device helpers shared by the recurrent-layer operators (recurrent.h).
+#pragma once
+
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "common.hpp"
+#include "recurrent.h"
+
+// Defined in abi.hip: records the message returned by retention_last_error().
+ret_status_t retention_fail_(ret_status_t s, const char *msg);
+
+namespace ret {
+
+// ------------------------------------------------------------------ host side
+inline ret_status_t rec_fail(ret_status_t s, const char *fmt, ...) {
+  char msg[256];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return retention_fail_(s, msg);
+}
+
+inline ret_status_t rec_status(hipError_t e) {
+  return e == hipSuccess ? retention_fail_(RET_OK, "") : rec_fail(RET_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+}
+
+inline size_t rec_esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
+inline bool rec_dtype_ok(ret_dtype_t t) { return t == RET_F32 || t == RET_BF16; }
+inline size_t rec_align(size_t x) { return (x + 255) & ~(size_t)255; }
+inline long long rec_cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// A tensor of a call: its bytes from p on (rows * ld less the gap behind the last row).
+struct RecSpan {
+  const char *name;
+  const void *p;
+  size_t n;
+};
+inline RecSpan rec_rows(const char *name, const void *p, long long rows, long long ld, long long width, size_t e) {
+  return {name, p, p && rows > 0 ? (size_t)((rows - 1) * ld + width) * e : 0};
+}
+inline bool rec_overlap(const RecSpan &a, const RecSpan &b) {
+  if (!a.p || !b.p || !a.n || !b.n) return false;
+  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+  return a0 < b0 + b.n && b0 < a0 + a.n;
+}
+// The first output that meets an input or another output, as an error; RET_OK if none.
+template <int NI, int NO>
+inline ret_status_t rec_check_overlap(const RecSpan (&ins)[NI], const RecSpan (&outs)[NO]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (rec_overlap(outs[o], ins[i]))
+        return rec_fail(RET_ERR_INVALID_ARG, "%s overlaps %s", outs[o].name, ins[i].name);
+    for (int i = 0; i < o; ++i)
+      if (rec_overlap(outs[o], outs[i]))
+        return rec_fail(RET_ERR_INVALID_ARG, "%s overlaps %s", outs[o].name, outs[i].name);
+  }
+  return RET_OK;
+}
+inline bool rec_aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// ------------------------------------------------------------------ device side
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Four consecutive elements from p (n of them valid, the others 0).  VEC: all four
+// are there and p is aligned to them.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load4(const T *p, int n, float (&r)[4]) {
+  if constexpr (VEC) {
+    if constexpr (sizeof(T) == 2) {
+      const uint2 x = *(const uint2 *)p;
+      r[0] = __uint_as_float(x.x << 16);
+      r[1] = __uint_as_float(x.x & 0xffff0000u);
+      r[2] = __uint_as_float(x.y << 16);
+      r[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else {
+      const float4 x = *(const float4 *)p;
+      r[0] = x.x;
+      r[1] = x.y;
+      r[2] = x.z;
+      r[3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      r[c] = 0.0f;
+      if (c < n) {
+        if constexpr (sizeof(T) == 2)
+          r[c] = bf2f(p[c]);
+        else
+          r[c] = p[c];
+      }
+    }
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store4(void *base, long long off, int n, const float (&r)[4], bool bf16) {
+  if constexpr (VEC) {
+    if (bf16)
+      *(uint2 *)((uint16_t *)base + off) = make_uint2(pack_bf2(r[0], r[1]), pack_bf2(r[2], r[3]));
+    else
+      *(float4 *)((float *)base + off) = make_float4(r[0], r[1], r[2], r[3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) store_elem(base, off + c, r[c], bf16);
+  }
+}
+
+// log(1 + e^x); above 20 the difference from x is below half a step of fp32.
+__device__ __forceinline__ float softplus(float x) { return x > 20.0f ? x : log1pf(expf(x)); }
+
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+}  // namespace ret
