@@ -220,27 +220,6 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
   }
 }
 
-// dw and dbias: the sum over all runs, in their order per column; double, as many come together.
-__global__ __launch_bounds__(NT) void conv_sum_kernel(const float *part, float *dw, float *dbias, int rows, int D,
-                                                      int K) {
-  __shared__ double red[4][64];
-  const long long cols = (long long)D * (K + 1), col = (long long)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
-  double x = 0.0;
-  if (col < cols)
-    for (int r = w; r < rows; r += 4) x += part[r * cols + col];
-  red[w][threadIdx.x & 63] = x;
-  __syncthreads();
-  if (w != 0 || col >= cols) return;
-  const float s = (float)(red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x]);
-  const long long d = col / (K + 1);
-  const int j = (int)(col % (K + 1));
-  if (j < K)
-    dw[d * K + j] = s;
-  else if (dbias)
-    dbias[d] = s;
-}
-
 template <typename T, int K, int VC>
 __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
   const int dv = a.D / VC;
@@ -455,20 +434,14 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
       const int vc = channels(qs, 2, D, 0, e);
       err = launch<FWD>(c, bf, vc, (long long)B * (K - 1) * (D / vc), st);
     }
-    if (err == hipSuccess) {
-      hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)rec_cdiv((long long)D * (K + 1), 64)), dim3(NT), 0, st, nullptr,
-                         dw, dbias, 0, D, K);
-      err = hipGetLastError();
-    }
+    if (err == hipSuccess) err = column_sum(nullptr, dw, dbias, 0, (long long)D * (K + 1), K + 1, st);
     return rec_status(err);
   }
   const int vc = channels(ps, 6, D, x_ld, e);
   set_runs(a, vc, BWD_RUN);
   hipError_t err = launch<BWD>(a, bf, vc, a.main_threads, st);
   if (err != hipSuccess) return rec_status(err);
-  hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)rec_cdiv((long long)D * (K + 1), 64)), dim3(NT), 0, st, a.part, dw,
-                     dbias, B * a.runs, D, K);
-  return rec_status(hipGetLastError());
+  return rec_status(column_sum(a.part, dw, dbias, (long long)B * a.runs, (long long)D * (K + 1), K + 1, st));
 }
 
 ret_status_t causal_conv1d_step(const void *x, const void *w, const void *bias, void *out, void *state, int B, int D,

@@ -1,13 +1,18 @@
 // Selective state space scan (recurrent.h): h_t = exp(dt_t A) h_{t-1} + dt_t u_t B_t,
 // y_t = C_t . h_t + D u_t, gated by silu(z_t); its gradients; its single-token form.
 //
-// Layout of every kernel here: a workgroup of four waves covers 64 channels of one
-// group (of B and C) of one sequence; a wave covers 16 channels, lane & 15, and its four
-// rows of 16 lanes (lane >> 4) hold NS of the states each, N <= 4 NS.  Sums over a
-// channel's states are NS terms in registers and two steps across the rows; the
-// recurrence itself never leaves a lane.  Tokens are staged in tiles of 16: thread
-// (token, four channels) computes the time step, u dt and the gated gradient once, in
-// fp32, into LDS, from where all four rows read them.
+// Layout of the passes: a wave works alone on CW = 16 CJ neighbouring channels of one
+// group (of B and C) of one sequence.  A lane holds CJ channels, those of lane & 15, and
+// NS states, those of its row of 16 lanes (lane >> 4), N <= 4 NS: the recurrence never
+// leaves a lane, a sum over a channel's states is NS terms and two steps across the rows.
+// Tokens come in tiles of 16: a lane reads four channels of CJ tokens, computes the time
+// step, dt u and the gated gradient once, in fp32, and leaves them in the wave's part of
+// LDS, from where all four rows read them back.  The loads of the next tile are in flight
+// meanwhile.
+//
+// What bounds it: the exponential (a quarter-rate instruction) and four fp32 operations per
+// token, channel and state, 8 issue slots; N = 16 of them and some 50 slots of softplus,
+// gate and conversions stand against 8 bytes of a bf16 token and channel.
 //
 // Long sequences are cut into segments, so that few channels still fill the chip: the
 // decay of a state over a segment is exp(A sum dt), so the states entering the
@@ -21,7 +26,6 @@ using namespace ret;
 
 namespace {
 
-constexpr int CH = 64;  // channels per workgroup
 constexpr int TT = 16;  // tokens per staged tile
 constexpr int NT = 256;
 
@@ -32,8 +36,9 @@ struct ScanArgs {
   void *out;
   float *hT;
   long long u_ld, delta_ld, z_ld, b_ld, c_ld;
-  int B, L, D, N, G, Dg, tiles;  // Dg = D / G channels per group, tiles of 64 of them
+  int B, L, D, N, G, Dg, tiles;  // Dg = D / G channels per group, tiles of them per workgroup
   int seg_len, nseg, softplus, out_bf16;
+  int vec, vec_bc, vec_n;  // rows of channels, of B and C, and states may be accessed by fours
   // workspace: segment states [B * nseg][D][N], sums of dt [B * nseg][D]
   float *seg, *sdt;
   // backward
@@ -46,7 +51,17 @@ struct ScanArgs {
   int subs;           // sub-tiles per segment
 };
 
-// What a block works on.
+// Channels per lane of a pass where there are channels enough: 16 elements per lane share
+// what a token costs beside them.
+constexpr int wide_cj(int NS) { return NS <= 4 ? 4 : 16 / NS; }
+
+// Channels per lane and tokens per sub-tile of the backward's main pass: a sub-tile's
+// states and decays, 2 SUB CJ NS fp32, stay in 128 registers.
+constexpr int bwd_cj(int NS) { return NS >= 8 ? 1 : 2; }
+constexpr int bwd_sub(int NS) { return std::min(TT, 64 / (NS * bwd_cj(NS))); }
+constexpr int BWD_WAVES = 4;
+
+// What a workgroup works on.
 struct Where {
   int b, s, g, tile, len, t_lo, t_hi;
 };
@@ -65,15 +80,26 @@ __device__ __forceinline__ Where where(const ScanArgs &a) {
   return w;
 }
 
+// Between a wave's own writes to its LDS and its reads of other lanes' values (and the
+// other way round): the hardware keeps a wave's LDS operations in order, this keeps the
+// compiler's.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // The sum over the four rows of a wave, for four tokens at once: lane row r gets token r.
-__device__ __forceinline__ float row_sums(const float (&y)[4], int row) {
-  float s[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    s[j] = y[j] + __shfl_xor(y[j], 16, 64);
-    s[j] += __shfl_xor(s[j], 32, 64);
-  }
-  return row == 0 ? s[0] : row == 1 ? s[1] : row == 2 ? s[2] : s[3];
+// The swaps exchange the halves (rows) of two registers, so that each addition sums both.
+__device__ __forceinline__ float swap_add32(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float swap_add16(float x, float y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float row_sums(const float (&y)[4]) {
+  return swap_add16(swap_add32(y[0], y[2]), swap_add32(y[1], y[3]));
 }
 
 // Sum over the 16 lanes of a row, in all of them (row rotations by 8, 4, 2, 1).
@@ -89,29 +115,181 @@ __device__ __forceinline__ float row16_sum(float x) {
   return x;
 }
 
+// NS states of a lane from n0 on; vec: N and n0 are multiples of four, p is aligned.
 template <int NS>
-__device__ __forceinline__ void load_state(const float *p, int N, int n0, bool ok, float (&h)[NS]) {
+__device__ __forceinline__ void load_state(const float *p, int N, int n0, bool ok, bool vec, float (&h)[NS]) {
+  if constexpr (NS % 4 == 0) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < NS; i += 4) {
+        const float4 v = ok && n0 + i < N ? *(const float4 *)(p + n0 + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        h[i] = v.x;
+        h[i + 1] = v.y;
+        h[i + 2] = v.z;
+        h[i + 3] = v.w;
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NS; ++i) h[i] = ok && n0 + i < N ? p[n0 + i] : 0.0f;
 }
 template <int NS>
-__device__ __forceinline__ void store_state(float *p, int N, int n0, bool ok, const float (&h)[NS]) {
+__device__ __forceinline__ void store_state(float *p, int N, int n0, bool ok, bool vec, const float (&h)[NS]) {
+  if constexpr (NS % 4 == 0) {
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < NS; i += 4)
+        if (ok && n0 + i < N) *(float4 *)(p + n0 + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+      return;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NS; ++i)
     if (ok && n0 + i < N) p[n0 + i] = h[i];
 }
 
-// B or C of the tile's tokens t0.. into dst[16][4 NS], zero behind N and behind t_hi.
-template <typename T, int NS>
-__device__ __forceinline__ void stage_bc(const void *src, long long ld, const ScanArgs &a, const Where &w, int t0,
-                                         float (*dst)[4 * NS]) {
-  for (int e = threadIdx.x; e < TT * 4 * NS; e += NT) {
-    const int tt = e / (4 * NS), n = e % (4 * NS);
-    float x = 0.0f;
-    if (n < a.N && t0 + tt < w.t_hi)
-      x = load_elem(src, ((long long)w.b * a.L + t0 + tt) * ld + (long long)w.g * a.N + n, sizeof(T) == 2);
-    dst[tt][n] = x;
+// Four neighbouring elements as they come from memory.
+template <typename T>
+struct Quad;
+template <>
+struct Quad<uint16_t> {
+  uint2 v;
+  // n of them are there (the others read as 0); vec: all four or none, aligned.
+  __device__ __forceinline__ void load(const uint16_t *p, int n, bool vec) {
+    v = make_uint2(0u, 0u);
+    if (vec) {
+      if (n > 0) v = *(const uint2 *)p;
+    } else {
+      if (n > 0) v.x = p[0];
+      if (n > 1) v.x |= (uint32_t)p[1] << 16;
+      if (n > 2) v.y = p[2];
+      if (n > 3) v.y |= (uint32_t)p[3] << 16;
+    }
   }
+  __device__ __forceinline__ void get(float (&r)[4]) const {
+    r[0] = __uint_as_float(v.x << 16);
+    r[1] = __uint_as_float(v.x & 0xffff0000u);
+    r[2] = __uint_as_float(v.y << 16);
+    r[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+template <>
+struct Quad<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float *p, int n, bool vec) {
+    v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (vec) {
+      if (n > 0) v = *(const float4 *)p;
+    } else {
+      if (n > 0) v.x = p[0];
+      if (n > 1) v.y = p[1];
+      if (n > 2) v.z = p[2];
+      if (n > 3) v.w = p[3];
+    }
+  }
+  __device__ __forceinline__ void get(float (&r)[4]) const {
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
+  }
+};
+
+__device__ __forceinline__ void put_quad(void *base, long long off, int n, const float (&r)[4], bool bf16, bool vec) {
+  if (vec) {
+    if (n > 0) store4<true>(base, off, n, r, bf16);
+  } else {
+    store4<false>(base, off, n, r, bf16);
+  }
+}
+
+// The CJ neighbouring values of a lane in a row of LDS.
+template <int CJ>
+__device__ __forceinline__ void get_lane(const float *p, float (&r)[CJ]) {
+  if constexpr (CJ == 4) {
+    const float4 v = *(const float4 *)p;
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
+  } else if constexpr (CJ == 2) {
+    const float2 v = *(const float2 *)p;
+    r[0] = v.x;
+    r[1] = v.y;
+  } else {
+    r[0] = p[0];
+  }
+}
+template <int CJ>
+__device__ __forceinline__ void put_lane(float *p, const float (&r)[CJ]) {
+  if constexpr (CJ == 4)
+    *(float4 *)p = make_float4(r[0], r[1], r[2], r[3]);
+  else if constexpr (CJ == 2)
+    *(float2 *)p = make_float2(r[0], r[1]);
+  else
+    p[0] = r[0];
+}
+template <int NS>
+__device__ __forceinline__ void get_states(const float *p, float (&r)[NS]) {
+  if constexpr (NS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      const float4 v = *(const float4 *)(p + i);
+      r[i] = v.x;
+      r[i + 1] = v.y;
+      r[i + 2] = v.z;
+      r[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) r[i] = p[i];
+  }
+}
+
+// A lane's share of a tile of B or C: quads of states, NS of them per token.
+template <typename T, int NS>
+struct StatesIn {
+  static constexpr int NQ = (TT * NS + 63) / 64;
+  Quad<T> q[NQ];
+  __device__ __forceinline__ void load(const void *src, long long ld, const ScanArgs &a, const Where &w, int t0, int lane) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int id = i * 64 + lane, tt = id / NS, n = id % NS * 4;
+      const bool there = id < TT * NS && t0 + tt < w.t_hi && t0 + tt >= w.t_lo;
+      q[i].load((const T *)src + ((long long)w.b * a.L + t0 + tt) * ld + (long long)w.g * a.N + n,
+                there ? min(a.N - n, 4) : 0, a.vec_bc);
+    }
+  }
+  __device__ __forceinline__ void put(float *dst, int lane) const {  // [TT][4 NS]
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int id = i * 64 + lane;
+      float r[4];
+      q[i].get(r);
+      if (TT * NS % 64 == 0 || id < TT * NS) *(float4 *)(dst + id * 4) = make_float4(r[0], r[1], r[2], r[3]);
+    }
+  }
+};
+
+// A lane's share of a tile of channels: CJ quads, of tokens tt(i) and channels cq .. cq + 3.
+template <typename T, int CJ>
+struct ChannelsIn {
+  Quad<T> q[CJ];
+  __device__ __forceinline__ void load(const void *src, long long ld, const ScanArgs &a, const Where &w, int t0, int tt,
+                                       long long d, int nc) {
+#pragma unroll
+    for (int i = 0; i < CJ; ++i) {
+      const int t = t0 + i * (TT / CJ) + tt;
+      q[i].load((const T *)src + ((long long)w.b * a.L + t) * ld + d, t >= w.t_lo && t < w.t_hi ? nc : 0, a.vec);
+    }
+  }
+};
+
+// The n values that a lane's four channels have, the others 0.
+__device__ __forceinline__ void load_channels(const float *p, int n, float (&r)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) r[c] = c < n ? p[c] : 0.0f;
 }
 
 enum { OUTPUT, STATES, CHECKPOINTS };
@@ -121,308 +299,502 @@ enum { OUTPUT, STATES, CHECKPOINTS };
 //     writes the final state.
 //   STATES: from zero, the segment's own final state and its sum of dt.
 //   CHECKPOINTS (backward): as STATES, also the state and the sum of dt before every
-//     SUB tokens, and the gradient that the segment's own outputs send to the state in
+//     sub-tile, and the gradient that the segment's own outputs send to the state in
 //     front of it, sum_t exp(A sum dt) C_t dy_t.
-template <typename T, int NS, bool VEC, int MODE>
-__global__ __launch_bounds__(NT) void scan_pass_kernel(ScanArgs a) {
-  constexpr int NP = 4 * NS, SUB = NS <= 4 ? 16 : 64 / NS;
-  __shared__ float2 dtx[TT][CH];  // (dt, dt u)
-  __shared__ float Bs[TT][NP];
-  __shared__ float Cs[MODE == STATES ? 1 : TT][NP];
-  __shared__ float ys[MODE == STATES ? 1 : TT][CH];  // OUTPUT: y; CHECKPOINTS: dy
+template <typename T, int NS, int CJ, int MODE>
+__global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
+  constexpr int NP = 4 * NS, CW = 16 * CJ, SUB = bwd_sub(NS);
+  __shared__ __align__(16) float dts[TT][CW], dus[TT][CW];  // dt, dt u; OUTPUT: y replaces dt u
+  __shared__ __align__(16) float dys[MODE == CHECKPOINTS ? TT : 1][CW];
+  __shared__ __align__(16) float Bs[TT][NP], Cs[MODE == STATES ? 1 : TT][NP];
   const Where w = where(a);
   const bool last = w.s == a.nseg - 1;
-  const int tid = threadIdx.x, lane = tid & 63, row = lane >> 4, ch = (tid >> 6) * 16 + (lane & 15);
-  const int rel = w.tile * CH + ch, n0 = row * NS;
-  const bool ok = rel < a.Dg;
+  const int lane = threadIdx.x, row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
+  const int rel = w.tile * CW + c0;
   const long long d = (long long)w.g * a.Dg + rel;
   const long long sd = ((long long)w.b * a.nseg + w.s) * a.D + d;
-  float A2[NS], h[NS], gs[NS], pr[NS], sum = 0.0f;
-  load_state(a.A + d * a.N, a.N, n0, ok, A2);
-#pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    A2[i] *= kLog2e;
-    h[i] = 0.0f;
-    gs[i] = 0.0f;
-    pr[i] = 1.0f;
-  }
-  if constexpr (MODE == OUTPUT) {
-    if (a.nseg > 1)
-      load_state(a.seg + sd * a.N, a.N, n0, ok, h);
-    else if (a.h0)
-      load_state(a.h0 + sd * a.N, a.N, n0, ok, h);
-  }
-  // the thread's part of the staging: one token, four channels
-  const int tt = tid >> 4, cq = (tid & 15) * 4, relq = w.tile * CH + cq;
+  // the lane's part of the staging
+  const int tt = lane / (4 * CJ), cq = lane % (4 * CJ) * 4, relq = w.tile * CW + cq;
   const int nc = min(max(a.Dg - relq, 0), 4);
   const long long dq = (long long)w.g * a.Dg + relq;
+  ChannelsIn<T, CJ> un, xn, zn, gn;
+  StatesIn<T, NS> bn, cn;
+  auto fetch = [&](int t0) {
+    un.load(a.u, a.u_ld, a, w, t0, tt, dq, nc);
+    xn.load(a.delta, a.delta_ld, a, w, t0, tt, dq, nc);
+    bn.load(a.Bm, a.b_ld, a, w, t0, lane);
+    if constexpr (MODE != STATES) {
+      if (a.z) zn.load(a.z, a.z_ld, a, w, t0, tt, dq, nc);
+      cn.load(a.Cm, a.c_ld, a, w, t0, lane);
+    }
+    if constexpr (MODE == CHECKPOINTS) gn.load(a.d_o, a.D, a, w, t0, tt, dq, nc);
+  };
+  fetch(w.t_lo);
+  float A2[CJ][NS], h[CJ][NS], gs[CJ][NS], pr[CJ][NS], sum[CJ];
+#pragma unroll
+  for (int j = 0; j < CJ; ++j) {
+    load_state(a.A + (d + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, A2[j]);
+    sum[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      A2[j][i] *= kLog2e;
+      h[j][i] = 0.0f;
+      gs[j][i] = 0.0f;
+      pr[j][i] = 1.0f;
+    }
+    if constexpr (MODE == OUTPUT) {
+      if (a.nseg > 1)
+        load_state(a.seg + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+      else if (a.h0)
+        load_state(a.h0 + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+    }
+  }
   float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (c < nc) {
-      if (a.bias) bias[c] = a.bias[dq + c];
-      if (a.Dskip) Dsk[c] = a.Dskip[dq + c];
-    }
+  if (a.bias) load_channels(a.bias + dq, nc, bias);
+  if (MODE == OUTPUT && a.Dskip) load_channels(a.Dskip + dq, nc, Dsk);
   for (int t0 = w.t_lo; t0 < w.t_hi; t0 += TT) {
-    const long long r = (long long)w.b * a.L + t0 + tt;
-    const bool live = t0 + tt < w.t_hi && nc > 0;
-    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (live) {
-      load4<T, VEC>((const T *)a.u + r * a.u_ld + dq, nc, u);
-      load4<T, VEC>((const T *)a.delta + r * a.delta_ld + dq, nc, x);
-      if (MODE != STATES && a.z) load4<T, VEC>((const T *)a.z + r * a.z_ld + dq, nc, z);
-    }
-    __syncthreads();
+    ChannelsIn<T, CJ> uc, zc;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float v = x[c] + bias[c], dt = !live || c >= nc ? 0.0f : a.softplus ? softplus(v) : v;
-      dtx[tt][cq + c] = make_float2(dt, live && c < nc ? dt * u[c] : 0.0f);
-    }
-    stage_bc<T, NS>(a.Bm, a.b_ld, a, w, t0, Bs);
-    if constexpr (MODE != STATES) stage_bc<T, NS>(a.Cm, a.c_ld, a, w, t0, Cs);
-    if constexpr (MODE == CHECKPOINTS) {
-      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (live) load4<T, VEC>((const T *)a.d_o + r * a.D + dq, nc, g);
+    for (int i = 0; i < CJ; ++i) {
+      const int k = i * (TT / CJ) + tt;
+      const bool live = t0 + k < w.t_hi;
+      float u[4], x[4], z[4], g[4], dt[4], dtu[4];
+      un.q[i].get(u);
+      xn.q[i].get(x);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) ys[tt][cq + c] = a.z ? g[c] * z[c] * sigmoid(z[c]) : g[c];
+      for (int c = 0; c < 4; ++c) {
+        const float v = x[c] + bias[c];
+        dt[c] = !live || c >= nc ? 0.0f : a.softplus ? softplus(v) : v;
+        dtu[c] = dt[c] * u[c];
+      }
+      *(float4 *)&dts[k][cq] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+      *(float4 *)&dus[k][cq] = make_float4(dtu[0], dtu[1], dtu[2], dtu[3]);
+      if constexpr (MODE == CHECKPOINTS) {
+        gn.q[i].get(g);
+        if (a.z) {
+          zn.q[i].get(z);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) g[c] *= z[c] * sigmoid(z[c]);
+        }
+        *(float4 *)&dys[k][cq] = make_float4(g[0], g[1], g[2], g[3]);
+      }
+      uc.q[i] = un.q[i];
+      if (MODE == OUTPUT && a.z) zc.q[i] = zn.q[i];
     }
-    __syncthreads();
+    bn.put(&Bs[0][0], lane);
+    if constexpr (MODE != STATES) cn.put(&Cs[0][0], lane);
+    fetch(t0 + TT);
+    wave_sync();
     const int nt = min(TT, w.t_hi - t0);
     for (int t4 = 0; t4 < nt; t4 += 4) {
       if constexpr (MODE == CHECKPOINTS) {
         if (t4 % SUB == 0) {
           const long long k = ((long long)w.b * a.nseg + w.s) * a.subs + (t0 - w.t_lo + t4) / SUB;
-          store_state(a.ck + (k * a.D + d) * a.N, a.N, n0, ok, h);
-          if (ok && row == 0) a.ckdt[k * a.D + d] = sum;
-        }
-      }
-      float y[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 v = dtx[t4 + j][ch];
-        float acc = 0.0f;
-        const float dy = MODE == CHECKPOINTS ? ys[t4 + j][ch] : 0.0f;
-        if constexpr (MODE != OUTPUT) sum += v.x;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          const float e = __builtin_amdgcn_exp2f(v.x * A2[i]);
-          h[i] = e * h[i] + v.y * Bs[t4 + j][n0 + i];
-          if constexpr (MODE == OUTPUT) acc += h[i] * Cs[t4 + j][n0 + i];
-          if constexpr (MODE == CHECKPOINTS) {
-            pr[i] *= e;
-            gs[i] += pr[i] * (dy * Cs[t4 + j][n0 + i]);
+          for (int j = 0; j < CJ; ++j) {
+            store_state(a.ck + (k * a.D + d + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+            if (rel + j < a.Dg && row == 0) a.ckdt[k * a.D + d + j] = sum[j];
           }
         }
-        y[j] = acc;
+      }
+      float y[CJ][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS];
+        get_lane(&dts[t4 + k][c0], dt);
+        get_lane(&dus[t4 + k][c0], dtu);
+        get_states(&Bs[t4 + k][n0], Bv);
+        if constexpr (MODE != STATES) get_states(&Cs[t4 + k][n0], Cv);
+        if constexpr (MODE == CHECKPOINTS) get_lane(&dys[t4 + k][c0], dy);
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+          float acc = 0.0f;
+          if constexpr (MODE != OUTPUT) sum[j] += dt[j];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            const float e = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
+            h[j][i] = e * h[j][i] + dtu[j] * Bv[i];
+            if constexpr (MODE == OUTPUT) acc += h[j][i] * Cv[i];
+            if constexpr (MODE == CHECKPOINTS) {
+              pr[j][i] *= e;
+              gs[j][i] += pr[j][i] * (dy[j] * Cv[i]);
+            }
+          }
+          y[j][k] = acc;
+        }
       }
       if constexpr (MODE == OUTPUT) {
-        const float v = row_sums(y, row);
-        ys[t4 + row][ch] = v;
+        float v[CJ];
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) v[j] = row_sums(y[j]);
+        put_lane(&dus[t4 + row][c0], v);  // the wave is past these tokens' dt u
       }
     }
+    wave_sync();
     if constexpr (MODE == OUTPUT) {
-      __syncthreads();
-      if (live) {
-        float o[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          o[c] = ys[tt][cq + c] + Dsk[c] * u[c];
-          if (a.z) o[c] *= z[c] * sigmoid(z[c]);
+      for (int i = 0; i < CJ; ++i) {
+        const int k = i * (TT / CJ) + tt;
+        float u[4], z[4], o[4];
+        const float4 y = *(const float4 *)&dus[k][cq];
+        uc.q[i].get(u);
+        o[0] = y.x + Dsk[0] * u[0];
+        o[1] = y.y + Dsk[1] * u[1];
+        o[2] = y.z + Dsk[2] * u[2];
+        o[3] = y.w + Dsk[3] * u[3];
+        if (a.z) {
+          zc.q[i].get(z);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] *= z[c] * sigmoid(z[c]);
         }
-        store4<VEC>(a.out, r * a.D + dq, nc, o, a.out_bf16);
+        if (t0 + k < w.t_hi)
+          put_quad(a.out, ((long long)w.b * a.L + t0 + k) * a.D + dq, nc, o, a.out_bf16, a.vec);
       }
+      wave_sync();
     }
   }
-  if constexpr (MODE == OUTPUT) {
-    if (last && a.hT) store_state(a.hT + ((long long)w.b * a.D + d) * a.N, a.N, n0, ok, h);
-  } else {
-    store_state(a.seg + sd * a.N, a.N, n0, ok, h);
-    if (ok && row == 0) a.sdt[sd] = sum;
-    if constexpr (MODE == CHECKPOINTS) store_state(a.gseg + sd * a.N, a.N, n0, ok, gs);
+#pragma unroll
+  for (int j = 0; j < CJ; ++j) {
+    const bool ok = rel + j < a.Dg;
+    if constexpr (MODE == OUTPUT) {
+      if (last && a.hT) store_state(a.hT + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
+    } else {
+      store_state(a.seg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
+      if (ok && row == 0) a.sdt[sd + j] = sum[j];
+      if constexpr (MODE == CHECKPOINTS) store_state(a.gseg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, gs[j]);
+    }
   }
 }
 
 // Segment states -> states entering the segments, in place; with gseg also the
-// gradients entering them from behind.  One thread per (sequence, channel, state).
+// gradients entering them from behind.  One thread per (sequence, channel, state); the
+// chain over segments is short next to its loads, which go ahead by eight.
 __global__ __launch_bounds__(NT) void scan_combine_kernel(ScanArgs a) {
   const long long DN = (long long)a.D * a.N, id = (long long)blockIdx.x * NT + threadIdx.x;
   if (id >= a.B * DN) return;
+  constexpr int U = 8;
   const long long b = id / DN, e = id % DN, d = e / a.N;
   const float A2 = a.A[e] * kLog2e;
+  const float *sdt = a.sdt + b * a.nseg * a.D + d;
+  float own[U], dt[U];
   float carry = a.h0 ? a.h0[id] : 0.0f;
   float *S = a.seg + b * a.nseg * DN + e;
-  const float *sdt = a.sdt + b * a.nseg * a.D + d;
-  for (int s = 0; s < a.nseg; ++s) {
-    const float own = S[s * DN];
-    S[s * DN] = carry;
-    carry = __builtin_amdgcn_exp2f(A2 * sdt[(long long)s * a.D]) * carry + own;
+  for (int s0 = 0; s0 < a.nseg; s0 += U) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int s = min(s0 + k, a.nseg - 1);
+      own[k] = S[s * DN];
+      dt[k] = sdt[(long long)s * a.D];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (s0 + k < a.nseg) {
+        S[(s0 + k) * DN] = carry;
+        carry = __builtin_amdgcn_exp2f(A2 * dt[k]) * carry + own[k];
+      }
   }
   if (!a.gseg) return;
   float *Gs = a.gseg + b * a.nseg * DN + e;
   carry = a.dhT ? a.dhT[id] : 0.0f;
-  for (int s = a.nseg - 1; s >= 0; --s) {
-    const float own = Gs[s * DN];
-    Gs[s * DN] = carry;
-    carry = __builtin_amdgcn_exp2f(A2 * sdt[(long long)s * a.D]) * carry + own;
+  for (int s0 = a.nseg - 1; s0 >= 0; s0 -= U) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int s = max(s0 - k, 0);
+      own[k] = Gs[s * DN];
+      dt[k] = sdt[(long long)s * a.D];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (s0 - k >= 0) {
+        Gs[(s0 - k) * DN] = carry;
+        carry = __builtin_amdgcn_exp2f(A2 * dt[k]) * carry + own[k];
+      }
+  }
+}
+
+// The backward's sums over a wave's channels, for one token: the products of a lane, NS of
+// dB and NS of dC, are summed over the row's 16 lanes.  Four states of both together: the
+// first two steps halve the number of registers as well, since the bank mask of a row
+// operation lets two sums share one (lanes 0-7 keep the first, 8-15 the second; then banks
+// of four): 16 additions for eight sums instead of 32.  out: [2][4 NS] of the token.
+template <int NS>
+__device__ __forceinline__ void channel_sums(const float (&pB)[NS], const float (&pC)[NS], int lane, float *out) {
+  const int row = lane >> 4;
+  if constexpr (NS % 4 == 0) {
+    const int bank = (lane >> 2) & 3, state = (bank & 1) * 2 + (bank >> 1);
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      float b, c, t0, t1, t2, t3;
+      // two instructions, or that many idle slots, between a register's write and its use by a row operation
+      asm("s_nop 1\n"
+          "v_add_f32_dpp %2, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+          "v_add_f32_dpp %2, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+          "v_add_f32_dpp %3, %8, %8 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+          "v_add_f32_dpp %3, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+          "v_add_f32_dpp %4, %10, %10 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+          "v_add_f32_dpp %4, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+          "v_add_f32_dpp %5, %12, %12 row_ror:8 row_mask:0xf bank_mask:0x3\n"
+          "v_add_f32_dpp %5, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xc\n"
+          "v_add_f32_dpp %0, %2, %2 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+          "v_add_f32_dpp %0, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+          "v_add_f32_dpp %1, %4, %4 row_half_mirror row_mask:0xf bank_mask:0x5\n"
+          "v_add_f32_dpp %1, %5, %5 row_half_mirror row_mask:0xf bank_mask:0xa\n"
+          "v_add_f32_dpp %0, %0, %0 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n"
+          "s_nop 0\n"
+          "v_add_f32_dpp %1, %1, %1 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n"
+          "v_add_f32_dpp %0, %0, %0 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n"
+          "s_nop 0\n"
+          "v_add_f32_dpp %1, %1, %1 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n"
+          : "=&v"(b), "=&v"(c), "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3)
+          : "v"(pB[i]), "v"(pB[i + 1]), "v"(pB[i + 2]), "v"(pB[i + 3]), "v"(pC[i]), "v"(pC[i + 1]), "v"(pC[i + 2]),
+            "v"(pC[i + 3]));
+      out[(lane & 1) * 4 * NS + row * NS + i + state] = lane & 1 ? c : b;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const float b = row16_sum(pB[i]), c = row16_sum(pC[i]);
+      out[(lane & 1) * 4 * NS + row * NS + i] = lane & 1 ? c : b;
+    }
   }
 }
 
 // The backward's main pass over a segment, tiles and sub-tiles from the last to the
 // first: each sub-tile's states are computed again from its checkpoint and kept in
-// registers with their decays; then the gradient of the state runs against time.
-template <typename T, int NS, bool VEC>
-__global__ __launch_bounds__(NT) void scan_bwd_kernel(ScanArgs a) {
-  constexpr int NP = 4 * NS, SUB = NS <= 4 ? 16 : 64 / NS;
-  __shared__ float2 dtx[TT][CH];       // (dt, dt u), then (sum g B, sum A w)
-  __shared__ float dys[TT][CH];        // dy, then C . h
-  __shared__ float Bs[TT][NP], Cs[TT][NP];
-  __shared__ float part[4][TT][2][NP];  // each wave's sums over its channels
+// registers with their decays; then the gradient of the state runs against time.  The
+// waves of a workgroup work on neighbouring channels and meet once per tile, to add up
+// their sums for dB and dC.
+template <typename T, int NS>
+__global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_kernel(ScanArgs a) {
+  constexpr int NP = 4 * NS, CJ = bwd_cj(NS), CW = 16 * CJ, SUB = bwd_sub(NS);
+  struct WaveLds {
+    float dt[TT][CW];
+    float du[TT][CW];  // dt u, then sum_n g B
+    float dy[TT][CW];  // dy, then sum_n A w
+    float y[TT][CW];   // C . h
+    float B[TT][NP], C[TT][NP];
+  };
+  __shared__ __align__(16) WaveLds lds[BWD_WAVES];
+  __shared__ float part[2][BWD_WAVES][TT][2][NP];  // each wave's sums over its channels
   const Where w = where(a);
-  const int tid = threadIdx.x, lane = tid & 63, row = lane >> 4, wave = tid >> 6, ch = wave * 16 + (lane & 15);
-  const int rel = w.tile * CH + ch, n0 = row * NS;
-  const bool ok = rel < a.Dg;
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
+  const int base = (w.tile * waves + wave) * CW, rel = base + c0;
   const long long d = (long long)w.g * a.Dg + rel;
   const long long bs = (long long)w.b * a.nseg + w.s, sd = bs * a.D + d;
-  float A1[NS], hin[NS], carry[NS], dA[NS];
-  load_state(a.A + d * a.N, a.N, n0, ok, A1);
-  load_state(a.seg + sd * a.N, a.N, n0, ok, hin);
-  load_state(a.gseg + sd * a.N, a.N, n0, ok, carry);
-#pragma unroll
-  for (int i = 0; i < NS; ++i) dA[i] = 0.0f;
-  const int tt = tid >> 4, cq = (tid & 15) * 4, relq = w.tile * CH + cq;
+  WaveLds &s = lds[wave];
+  const int tt = lane / (4 * CJ), cq = lane % (4 * CJ) * 4, relq = base + cq;
   const int nc = min(max(a.Dg - relq, 0), 4);
   const long long dq = (long long)w.g * a.Dg + relq;
-  float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float sD[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (c < nc) {
-      if (a.bias) bias[c] = a.bias[dq + c];
-      if (a.Dskip) Dsk[c] = a.Dskip[dq + c];
-    }
+  ChannelsIn<T, CJ> un, xn, zn, gn;
+  StatesIn<T, NS> bn, cn;
+  auto fetch = [&](int t0) {
+    un.load(a.u, a.u_ld, a, w, t0, tt, dq, nc);
+    xn.load(a.delta, a.delta_ld, a, w, t0, tt, dq, nc);
+    if (a.z) zn.load(a.z, a.z_ld, a, w, t0, tt, dq, nc);
+    gn.load(a.d_o, a.D, a, w, t0, tt, dq, nc);
+    bn.load(a.Bm, a.b_ld, a, w, t0, lane);
+    cn.load(a.Cm, a.c_ld, a, w, t0, lane);
+  };
   const int ntile = (w.t_hi - w.t_lo + TT - 1) / TT;
+  fetch(w.t_lo + (ntile - 1) * TT);
+  float A2[CJ][NS], carry[CJ][NS], dA[CJ][NS];
+#pragma unroll
+  for (int j = 0; j < CJ; ++j) {
+    const bool ok = rel + j < a.Dg;
+    load_state(a.A + (d + j) * a.N, a.N, n0, ok, a.vec_n, A2[j]);
+    load_state(a.gseg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, carry[j]);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      A2[j][i] *= kLog2e;
+      dA[j][i] = 0.0f;
+    }
+  }
+  float sD[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int tile = ntile - 1; tile >= 0; --tile) {
     const int t0 = w.t_lo + tile * TT;
-    const long long r = (long long)w.b * a.L + t0 + tt;
-    const bool live = t0 + tt < w.t_hi && nc > 0;
-    float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float go[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dt[4], dy[4];
-    if (live) {
-      load4<T, VEC>((const T *)a.u + r * a.u_ld + dq, nc, u);
-      load4<T, VEC>((const T *)a.delta + r * a.delta_ld + dq, nc, x);
-      load4<T, VEC>((const T *)a.d_o + r * a.D + dq, nc, go);
-      if (a.z) load4<T, VEC>((const T *)a.z + r * a.z_ld + dq, nc, z);
-    }
-    __syncthreads();
+    float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.bias) load_channels(a.bias + dq, nc, bias);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      x[c] += bias[c];
-      dt[c] = !live || c >= nc ? 0.0f : a.softplus ? softplus(x[c]) : x[c];
-      dy[c] = a.z ? go[c] * z[c] * sigmoid(z[c]) : go[c];
-      dtx[tt][cq + c] = make_float2(dt[c], live && c < nc ? dt[c] * u[c] : 0.0f);
-      dys[tt][cq + c] = dy[c];
-    }
-    stage_bc<T, NS>(a.Bm, a.b_ld, a, w, t0, Bs);
-    stage_bc<T, NS>(a.Cm, a.c_ld, a, w, t0, Cs);
-    __syncthreads();
-    const int nt = min(TT, w.t_hi - t0);
-    for (int t1 = (nt - 1) / SUB * SUB; t1 >= 0; t1 -= SUB) {
-      float h[NS], hh[SUB][NS], aa[SUB][NS], y[4];
-      const long long k = bs * a.subs + (tile * TT + t1) / SUB;
-      load_state(a.ck + (k * a.D + d) * a.N, a.N, n0, ok, h);
-      const float before = ok ? a.ckdt[k * a.D + d] : 0.0f;
-      float hstart[NS];
+    for (int i = 0; i < CJ; ++i) {
+      const int k = i * (TT / CJ) + tt;
+      const bool live = t0 + k < w.t_hi;
+      float u[4], x[4], z[4], g[4], dt[4];
+      un.q[i].get(u);
+      xn.q[i].get(x);
+      gn.q[i].get(g);
 #pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        h[i] += __builtin_amdgcn_exp2f(A1[i] * kLog2e * before) * hin[i];
-        hstart[i] = h[i];
+      for (int c = 0; c < 4; ++c) {
+        const float v = x[c] + bias[c];
+        dt[c] = !live || c >= nc ? 0.0f : a.softplus ? softplus(v) : v;
       }
-      float ysum[SUB / 4];
+      if (a.z) {
+        zn.q[i].get(z);
 #pragma unroll
-      for (int t = 0; t < SUB; ++t) {
-        const float2 v = dtx[t1 + t][ch];
-        float acc = 0.0f;
+        for (int c = 0; c < 4; ++c) g[c] *= z[c] * sigmoid(z[c]);
+      }
+      *(float4 *)&s.dt[k][cq] = make_float4(dt[0], dt[1], dt[2], dt[3]);
+      *(float4 *)&s.du[k][cq] = make_float4(dt[0] * u[0], dt[1] * u[1], dt[2] * u[2], dt[3] * u[3]);
+      *(float4 *)&s.dy[k][cq] = make_float4(g[0], g[1], g[2], g[3]);
+    }
+    bn.put(&s.B[0][0], lane);
+    cn.put(&s.C[0][0], lane);
+    wave_sync();
+    const int nt = min(TT, w.t_hi - t0);
+    float(*ps)[2][NP] = part[tile & 1][wave];
+    for (int t1 = (nt - 1) / SUB * SUB; t1 >= 0; t1 -= SUB) {
+      float h[CJ][NS], hh[SUB][CJ][NS], aa[SUB][CJ][NS], y[CJ][4];
+      const long long k = bs * a.subs + (tile * TT + t1) / SUB;
+      float hstart[CJ][NS];
+#pragma unroll
+      for (int j = 0; j < CJ; ++j) {
+        const bool ok = rel + j < a.Dg;
+        float hin[NS];
+        load_state(a.ck + (k * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
+        load_state(a.seg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, hin);
+        const float before = ok ? a.ckdt[k * a.D + d + j] : 0.0f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          aa[t][i] = __builtin_amdgcn_exp2f(v.x * (A1[i] * kLog2e));
-          h[i] = aa[t][i] * h[i] + v.y * Bs[t1 + t][n0 + i];
-          hh[t][i] = h[i];
-          acc += h[i] * Cs[t1 + t][n0 + i];
+          h[j][i] += __builtin_amdgcn_exp2f(A2[j][i] * before) * hin[i];
+          hstart[j][i] = h[j][i];
         }
-        y[t & 3] = acc;
-        if ((t & 3) == 3) ysum[t >> 2] = row_sums(y, row);
+      }
+#pragma unroll
+      for (int t = 0; t < SUB; ++t) {
+        float dt[CJ], dtu[CJ], Bv[NS], Cv[NS];
+        get_lane(&s.dt[t1 + t][c0], dt);
+        get_lane(&s.du[t1 + t][c0], dtu);
+        get_states(&s.B[t1 + t][n0], Bv);
+        get_states(&s.C[t1 + t][n0], Cv);
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+          float acc = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            aa[t][j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
+            h[j][i] = aa[t][j][i] * h[j][i] + dtu[j] * Bv[i];
+            hh[t][j][i] = h[j][i];
+            acc += h[j][i] * Cv[i];
+          }
+          y[j][t & 3] = acc;
+        }
+        if ((t & 3) == 3) {
+          float v[CJ];
+#pragma unroll
+          for (int j = 0; j < CJ; ++j) v[j] = row_sums(y[j]);
+          put_lane(&s.y[t1 + (t & ~3) + row][c0], v);
+        }
       }
 #pragma unroll
       for (int t4 = SUB - 4; t4 >= 0; t4 -= 4) {
-        float gB[4], sA[4];
+        float gB[CJ][4], sA[CJ][4];
 #pragma unroll
-        for (int j = 3; j >= 0; --j) {
-          const int t = t4 + j;
-          const float2 v = dtx[t1 + t][ch];
-          const float dyv = dys[t1 + t][ch];
-          gB[j] = sA[j] = 0.0f;
+        for (int q = 3; q >= 0; --q) {
+          const int t = t4 + q;
+          float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS], pB[NS], pC[NS];
+          get_lane(&s.dt[t1 + t][c0], dt);
+          get_lane(&s.du[t1 + t][c0], dtu);
+          get_lane(&s.dy[t1 + t][c0], dy);
+          get_states(&s.B[t1 + t][n0], Bv);
+          get_states(&s.C[t1 + t][n0], Cv);
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            const float Bv = Bs[t1 + t][n0 + i], Cv = Cs[t1 + t][n0 + i];
-            const float g = Cv * dyv + carry[i];
-            carry[i] = aa[t][i] * g;
-            const float wv = carry[i] * (t > 0 ? hh[t - 1][i] : hstart[i]);
-            sA[j] += A1[i] * wv;
-            dA[i] += v.x * wv;
-            gB[j] += g * Bv;
-            const float pB = row16_sum(g * v.y), pC = row16_sum(dyv * hh[t][i]);
-            if ((lane & 15) == 0) {
-              part[wave][t1 + t][0][n0 + i] = pB;
-              part[wave][t1 + t][1][n0 + i] = pC;
+          for (int j = 0; j < CJ; ++j) {
+            gB[j][q] = sA[j][q] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+              const float g = Cv[i] * dy[j] + carry[j][i];
+              carry[j][i] = aa[t][j][i] * g;
+              const float wv = carry[j][i] * (t > 0 ? hh[t > 0 ? t - 1 : 0][j][i] : hstart[j][i]);
+              sA[j][q] += A2[j][i] * wv;  // times log2 e; taken out below
+              dA[j][i] += dt[j] * wv;
+              gB[j][q] += g * Bv[i];
+              pB[i] = j ? pB[i] + g * dtu[j] : g * dtu[j];
+              pC[i] = j ? pC[i] + dy[j] * hh[t][j][i] : dy[j] * hh[t][j][i];
             }
           }
+          channel_sums(pB, pC, lane, &ps[t1 + t][0][0]);
         }
-        const float vB = row_sums(gB, row), vA = row_sums(sA, row);
-        // only this wave reads these channels' entries, and it is past these tokens
-        dtx[t1 + t4 + row][ch] = make_float2(vB, vA);
-        dys[t1 + t4 + row][ch] = ysum[t4 >> 2];
+        float vB[CJ], vA[CJ];
+#pragma unroll
+        for (int j = 0; j < CJ; ++j) {
+          vB[j] = row_sums(gB[j]);
+          vA[j] = kLn2 * row_sums(sA[j]);
+        }
+        // the wave is past these tokens
+        put_lane(&s.du[t1 + t4 + row][c0], vB);
+        put_lane(&s.dy[t1 + t4 + row][c0], vA);
+      }
+    }
+    wave_sync();
+    // the inputs stayed in registers; the next tile's take their place as they are used
+    const ChannelsIn<T, CJ> uc = un, xc = xn, zc = zn, gc = gn;
+    fetch(t0 - TT);
+    if (a.bias) load_channels(a.bias + dq, nc, bias);
+    if (a.Dskip) load_channels(a.Dskip + dq, nc, Dsk);
+#pragma unroll
+    for (int i = 0; i < CJ; ++i) {
+      const int k = i * (TT / CJ) + tt;
+      float u[4], x[4], z[4], g[4], dt[4], gB[4], sA[4], y[4], du[4], dd[4], dz[4];
+      uc.q[i].get(u);
+      xc.q[i].get(x);
+      gc.q[i].get(g);
+      get_lane(&s.dt[k][cq], dt);
+      get_lane(&s.du[k][cq], gB);
+      get_lane(&s.dy[k][cq], sA);
+      get_lane(&s.y[k][cq], y);
+      if (a.z) zc.q[i].get(z);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float dy = g[c];
+        if (a.z) {
+          const float sg = sigmoid(z[c]), gate = z[c] * sg;
+          dy *= gate;
+          dz[c] = g[c] * (y[c] + Dsk[c] * u[c]) * (sg + gate * (1.0f - sg));
+        }
+        du[c] = gB[c] * dt[c] + dy * Dsk[c];
+        dd[c] = sA[c] + gB[c] * u[c];
+        if (a.softplus) dd[c] *= sigmoid(x[c] + bias[c]);
+        const bool live = t0 + k < w.t_hi && c < nc;
+        sD[c] += live ? dy * u[c] : 0.0f;
+        sb[c] += live ? dd[c] : 0.0f;
+      }
+      if (t0 + k < w.t_hi) {
+        const long long o = ((long long)w.b * a.L + t0 + k) * a.D + dq;
+        put_quad(a.du, o, nc, du, a.out_bf16, a.vec);
+        put_quad(a.ddelta, o, nc, dd, a.out_bf16, a.vec);
+        if (a.z) put_quad(a.dz, o, nc, dz, a.out_bf16, a.vec);
       }
     }
     __syncthreads();
-    if (live) {
-      float gu[4], gd[4], gz[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float2 v = dtx[tt][cq + c];
-        gu[c] = v.x * dt[c] + dy[c] * Dsk[c];
-        gd[c] = v.y + v.x * u[c];
-        if (a.softplus) gd[c] *= sigmoid(x[c]);
-        const float y = dys[tt][cq + c] + Dsk[c] * u[c], sg = sigmoid(z[c]);
-        gz[c] = go[c] * y * sg * (1.0f + z[c] * (1.0f - sg));
-        sD[c] += dy[c] * u[c];
-        sb[c] += gd[c];
-      }
-      store4<VEC>(a.du, r * a.D + dq, nc, gu, a.out_bf16);
-      store4<VEC>(a.ddelta, r * a.D + dq, nc, gd, a.out_bf16);
-      if (a.z) store4<VEC>(a.dz, r * a.D + dq, nc, gz, a.out_bf16);
-    }
-    for (int e = tid; e < nt * 2 * a.N; e += NT) {
+    // the other half of part is written before the next barrier, this one behind it
+    for (int e = threadIdx.x; e < nt * 2 * a.N; e += blockDim.x) {
       const int t = e / (2 * a.N), k = e / a.N % 2, n = e % a.N;
-      a.bcpart[((((long long)w.tile * a.B + w.b) * a.L + t0 + t) * a.G + w.g) * 2 * a.N + k * a.N + n] =
-          part[0][t][k][n] + part[1][t][k][n] + part[2][t][k][n] + part[3][t][k][n];
+      float x = part[tile & 1][0][t][k][n];
+      for (int v = 1; v < waves; ++v) x += part[tile & 1][v][t][k][n];
+      a.bcpart[((((long long)w.tile * a.B + w.b) * a.L + t0 + t) * a.G + w.g) * 2 * a.N + k * a.N + n] = x;
     }
   }
-  store_state(a.dApart + sd * a.N, a.N, n0, ok, dA);
-  if (w.s == 0 && a.dh0) store_state(a.dh0 + ((long long)w.b * a.D + d) * a.N, a.N, n0, ok, carry);
-  // dD and the bias's gradient: the 16 token threads of each channel
-  __syncthreads();
 #pragma unroll
-  for (int c = 0; c < 4; ++c) dtx[tt][cq + c] = make_float2(sD[c], sb[c]);
-  __syncthreads();
-  if (tid < CH && w.tile * CH + tid < a.Dg) {
-    float2 t = make_float2(0.0f, 0.0f);
-    for (int k = 0; k < TT; ++k) {
-      t.x += dtx[k][tid].x;
-      t.y += dtx[k][tid].y;
+  for (int j = 0; j < CJ; ++j) {
+    const bool ok = rel + j < a.Dg;
+    store_state(a.dApart + (sd + j) * a.N, a.N, n0, ok, a.vec_n, dA[j]);
+    if (w.s == 0 && a.dh0) store_state(a.dh0 + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, carry[j]);
+  }
+  // dD and the bias's gradient: the lanes that staged a channel's tokens
+  wave_sync();
+  *(float4 *)&s.dt[tt][cq] = make_float4(sD[0], sD[1], sD[2], sD[3]);
+  *(float4 *)&s.du[tt][cq] = make_float4(sb[0], sb[1], sb[2], sb[3]);
+  wave_sync();
+  if (lane < CW && base + lane < a.Dg) {
+    float x = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < TT / CJ; ++k) {
+      x += s.dt[k][lane];
+      y += s.du[k][lane];
     }
-    const long long e = bs * a.D + (long long)w.g * a.Dg + w.tile * CH + tid;
-    a.dDpart[e] = t.x;
-    a.dbpart[e] = t.y;
+    const long long e = bs * a.D + (long long)w.g * a.Dg + base + lane;
+    a.dDpart[e] = x;
+    a.dbpart[e] = y;
   }
 }
 
@@ -449,20 +821,6 @@ __global__ __launch_bounds__(NT) void scan_reduce_bc_kernel(ScanArgs a, void *dB
   store_elem(k ? dC : dB, rg * a.N + n, x, a.out_bf16);
 }
 
-// Column sums of part[rows][cols]; double, as thousands of rows may come together.
-__global__ __launch_bounds__(NT) void column_sum_kernel(const float *part, float *out, int rows, long long cols) {
-  __shared__ double red[4][64];
-  const long long col = (long long)blockIdx.x * 64 + (threadIdx.x & 63);
-  const int w = threadIdx.x >> 6;
-  double x = 0.0;
-  if (col < cols)
-    for (int r = w; r < rows; r += 4) x += part[r * cols + col];
-  red[w][threadIdx.x & 63] = x;
-  __syncthreads();
-  if (w == 0 && col < cols)
-    out[col] = (float)(red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x]);
-}
-
 __global__ __launch_bounds__(NT) void state_copy_kernel(float *dst, const float *src, long long n) {
   for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < n; i += (long long)gridDim.x * NT)
     dst[i] = src ? src[i] : 0.0f;
@@ -474,48 +832,64 @@ hipError_t state_copy(float *dst, const float *src, long long n, hipStream_t st)
   return hipGetLastError();
 }
 
-// One token: a wave's lanes as in the passes above, the state read and written once.
-template <typename T, int NS>
+constexpr int STEP_CH = 64;  // channels of a workgroup's four waves
+
+// One token: a wave's lanes as in the passes above with one channel each; bound by reading
+// and writing the states once.
+// SQ sequences share their channels' A and have their loads in flight together.
+template <typename T, int NS, int SQ>
 __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, row = lane >> 4, ch = (tid >> 6) * 16 + (lane & 15);
   int id = blockIdx.x;
   const int tile = id % a.tiles;
   id /= a.tiles;
   const int g = id % a.G;
-  const long long b = id / a.G;
-  const int rel = tile * CH + ch, n0 = row * NS;
+  const int b0 = id / a.G * SQ;
+  const int rel = tile * STEP_CH + ch, n0 = row * NS;
   const bool ok = rel < a.Dg;
   const long long d = (long long)g * a.Dg + rel;
-  float A[NS], h[NS];
-  float *S = a.hT + (b * a.D + d) * a.N;
-  load_state(a.A + d * a.N, a.N, n0, ok, A);
-  load_state(S, a.N, n0, ok, h);
   constexpr int bf = sizeof(T) == 2;
-  float u = 0.0f, dt = 0.0f;
-  if (ok) {
-    u = load_elem(a.u, b * a.u_ld + d, bf);
-    dt = load_elem(a.delta, b * a.delta_ld + d, bf) + (a.bias ? a.bias[d] : 0.0f);
-    if (a.softplus) dt = softplus(dt);
-  }
-  float y = 0.0f;
+  float A[NS], h[SQ][NS], u[SQ], x[SQ], z[SQ], y[SQ];
+  Quad<T> Bq[SQ][(NS + 3) / 4], Cq[SQ][(NS + 3) / 4];
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const int n = n0 + i;
-    const float Bv = n < a.N ? load_elem(a.Bm, b * a.b_ld + (long long)g * a.N + n, bf) : 0.0f;
-    const float Cv = n < a.N ? load_elem(a.Cm, b * a.c_ld + (long long)g * a.N + n, bf) : 0.0f;
-    h[i] = __builtin_amdgcn_exp2f(dt * (A[i] * kLog2e)) * h[i] + dt * u * Bv;
-    y += h[i] * Cv;
-  }
-  store_state(S, a.N, n0, ok, h);
-  y += __shfl_xor(y, 16, 64);
-  y += __shfl_xor(y, 32, 64);
-  if (ok && row == 0) {
-    if (a.Dskip) y += a.Dskip[d] * u;
-    if (a.z) {
-      const float z = load_elem(a.z, b * a.z_ld + d, bf);
-      y *= z * sigmoid(z);
+  for (int q = 0; q < SQ; ++q) {
+    const long long b = min(b0 + q, a.B - 1);
+    load_state(a.hT + (b * a.D + d) * a.N, a.N, n0, ok, a.vec_n, h[q]);
+    u[q] = ok ? load_elem(a.u, b * a.u_ld + d, bf) : 0.0f;
+    x[q] = ok ? load_elem(a.delta, b * a.delta_ld + d, bf) : 0.0f;
+    z[q] = ok && a.z ? load_elem(a.z, b * a.z_ld + d, bf) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      const int n = min(min(a.N - n0 - i, 4), NS - i);
+      Bq[q][i / 4].load((const T *)a.Bm + b * a.b_ld + (long long)g * a.N + n0 + i, n, NS % 4 == 0 && a.vec_bc);
+      Cq[q][i / 4].load((const T *)a.Cm + b * a.c_ld + (long long)g * a.N + n0 + i, n, NS % 4 == 0 && a.vec_bc);
     }
-    store_elem(a.out, b * a.D + d, y, a.out_bf16);
+  }
+  load_state(a.A + d * a.N, a.N, n0, ok, a.vec_n, A);
+  const float bias = ok && a.bias ? a.bias[d] : 0.0f, skip = ok && a.Dskip ? a.Dskip[d] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
+#pragma unroll
+  for (int q = 0; q < SQ; ++q) {
+    const float dt = a.softplus ? softplus(x[q] + bias) : x[q] + bias, dtu = dt * u[q];
+    y[q] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      float Bv[4], Cv[4];
+      Bq[q][i / 4].get(Bv);
+      Cq[q][i / 4].get(Cv);
+      h[q][i] = __builtin_amdgcn_exp2f(dt * A[i]) * h[q][i] + dtu * Bv[i % 4];
+      y[q] += h[q][i] * Cv[i % 4];
+    }
+    if (b0 + q < a.B) store_state(a.hT + ((long long)(b0 + q) * a.D + d) * a.N, a.N, n0, ok, a.vec_n, h[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < SQ; ++q) {
+    y[q] += __shfl_xor(y[q], 16, 64);
+    y[q] += __shfl_xor(y[q], 32, 64);
+    y[q] += skip * u[q];
+    if (a.z) y[q] *= z[q] * sigmoid(z[q]);
+    if (ok && row == q % 4 && b0 + q < a.B) store_elem(a.out, (long long)(b0 + q) * a.D + d, y[q], a.out_bf16);
   }
 }
 
@@ -523,20 +897,39 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
 int state_regs(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 struct ScanPlan {
-  int tiles, seg_len, nseg, subs;
+  int cj, seg_len, nseg, subs;
+  int bwd_waves, bwd_tiles;
   size_t seg, sdt, gseg, ck, ckdt, bcpart, dApart, dDpart, dbpart, total;
 };
 
-// Segments: about `want` workgroups in all, of at least a tile each.
+// How a call is cut.  Waves of 16 wide_cj channels share a token's LDS reads and sums
+// among 16 elements per lane, waves of 16 channels are up to four times as many.  A sequence is
+// cut into segments only where its channels give less than a wave per SIMD (1024), since
+// that computes every exponential twice.
 ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   ScanPlan p;
-  p.tiles = (int)rec_cdiv(D / G, CH);
-  const long long blocks = (long long)B * G * p.tiles, want = 1024;
-  long long nseg = std::min<long long>(rec_cdiv(want, blocks), rec_cdiv(L, 4 * TT));
-  if (!bwd && 2 * blocks >= want) nseg = 1;
-  p.seg_len = (int)(rec_cdiv(rec_cdiv(L, std::max<long long>(nseg, 1)), TT) * TT);
+  const int NS = state_regs(N), SUB = bwd_sub(NS), Dg = D / G;
+  const int wide = wide_cj(NS);
+  const long long groups = (long long)B * G, ww = groups * rec_cdiv(Dg, 16 * wide), w16 = groups * rec_cdiv(Dg, 16);
+  const long long most = rec_cdiv(L, 4 * TT);  // segments of at least four tiles
+  long long nseg = 1;
+  if (bwd) {
+    // the main pass has workgroups of up to four waves of bwd_cj * 16 channels, two per SIMD at most
+    const int cw = 16 * bwd_cj(NS);
+    p.bwd_waves = (int)std::min<long long>(BWD_WAVES, rec_cdiv(Dg, cw));
+    p.bwd_tiles = (int)rec_cdiv(Dg, (long long)cw * p.bwd_waves);
+    nseg = std::min(rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves), rec_cdiv(L, 2 * TT));
+    p.cj = ww * nseg >= 1024 ? wide : 1;
+  } else {
+    p.bwd_waves = p.bwd_tiles = 0;
+    p.cj = ww >= 1024 ? wide : 1;
+    if (w16 < 1024 && most > 1) {
+      p.cj = ww * most >= 1024 ? wide : 1;
+      nseg = std::min(most, rec_cdiv(3072, p.cj == 1 ? w16 : ww));
+    }
+  }
+  p.seg_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
   p.nseg = (int)rec_cdiv(L, p.seg_len);
-  const int NS = state_regs(N), SUB = NS <= 4 ? 16 : 64 / NS;
   p.subs = p.seg_len / SUB;
   size_t off = 0;
   auto take = [&off](size_t floats) {
@@ -554,7 +947,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.gseg = take(bs * DN);
     p.ck = take(bs * p.subs * DN);
     p.ckdt = take(bs * p.subs * D);
-    p.bcpart = take((size_t)p.tiles * B * L * G * 2 * N);
+    p.bcpart = take((size_t)p.bwd_tiles * B * L * G * 2 * N);
     p.dApart = take(bs * DN);
     p.dDpart = take(bs * D);
     p.dbpart = take(bs * D);
@@ -567,7 +960,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
 bool plan_ok(int B, int L, int D, int N, int G) {
   return B > 0 && L > 0 && D > 0 && N > 0 && G > 0 && D % G == 0 && N <= RECURRENT_MAX_STATE &&
          (long long)B * L <= RECURRENT_MAX_TOKENS && (double)B * L * D <= RECURRENT_MAX_ELEMENTS &&
-         (double)B * D * N <= RECURRENT_MAX_ELEMENTS && (double)B * G * rec_cdiv(D / G, CH) < 2e9 &&
+         (double)B * D * N <= RECURRENT_MAX_ELEMENTS && (double)B * G * rec_cdiv(D / G, 16) < 2e9 &&
          (double)B * L * G * N <= RECURRENT_MAX_ELEMENTS;
 }
 
@@ -587,70 +980,75 @@ ret_status_t check_sizes(int B, int L, int D, int N, int G, ret_dtype_t in_dtype
 bool wide(const void *p, long long ld, size_t e) { return !p || (ld % 4 == 0 && rec_aligned(p, 4 * e)); }
 
 template <typename K>
-hipError_t launch(K kernel, long long blocks, hipStream_t st, const ScanArgs &a) {
+hipError_t launch(K kernel, long long blocks, int threads, hipStream_t st, const ScanArgs &a) {
   if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(NT), 0, st, a);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
   return hipGetLastError();
 }
 
-template <typename T, bool VEC, int MODE>
-hipError_t launch_pass(const ScanArgs &a, hipStream_t st) {
+template <typename T, int NS, int MODE>
+hipError_t launch_pass(ScanArgs a, int cj, hipStream_t st) {
+  a.tiles = (int)rec_cdiv(a.Dg, 16 * cj);
   const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
+  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE>, blocks, 64, st, a)
+                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE>, blocks, 64, st, a);
+}
+template <typename T, int MODE>
+hipError_t launch_pass(const ScanArgs &a, int cj, hipStream_t st) {
   switch (state_regs(a.N)) {
-    case 1: return launch(scan_pass_kernel<T, 1, VEC, MODE>, blocks, st, a);
-    case 2: return launch(scan_pass_kernel<T, 2, VEC, MODE>, blocks, st, a);
-    case 4: return launch(scan_pass_kernel<T, 4, VEC, MODE>, blocks, st, a);
-    case 8: return launch(scan_pass_kernel<T, 8, VEC, MODE>, blocks, st, a);
-    default: return launch(scan_pass_kernel<T, 16, VEC, MODE>, blocks, st, a);
+    case 1: return launch_pass<T, 1, MODE>(a, cj, st);
+    case 2: return launch_pass<T, 2, MODE>(a, cj, st);
+    case 4: return launch_pass<T, 4, MODE>(a, cj, st);
+    case 8: return launch_pass<T, 8, MODE>(a, cj, st);
+    default: return launch_pass<T, 16, MODE>(a, cj, st);
   }
 }
 template <int MODE>
-hipError_t launch_pass(const ScanArgs &a, bool bf, bool vec, hipStream_t st) {
-  if (bf) return vec ? launch_pass<uint16_t, true, MODE>(a, st) : launch_pass<uint16_t, false, MODE>(a, st);
-  return vec ? launch_pass<float, true, MODE>(a, st) : launch_pass<float, false, MODE>(a, st);
-}
-
-template <typename T, bool VEC>
-hipError_t launch_bwd(const ScanArgs &a, hipStream_t st) {
-  const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
-  switch (state_regs(a.N)) {
-    case 1: return launch(scan_bwd_kernel<T, 1, VEC>, blocks, st, a);
-    case 2: return launch(scan_bwd_kernel<T, 2, VEC>, blocks, st, a);
-    case 4: return launch(scan_bwd_kernel<T, 4, VEC>, blocks, st, a);
-    case 8: return launch(scan_bwd_kernel<T, 8, VEC>, blocks, st, a);
-    default: return launch(scan_bwd_kernel<T, 16, VEC>, blocks, st, a);
-  }
-}
-hipError_t launch_bwd(const ScanArgs &a, bool bf, bool vec, hipStream_t st) {
-  if (bf) return vec ? launch_bwd<uint16_t, true>(a, st) : launch_bwd<uint16_t, false>(a, st);
-  return vec ? launch_bwd<float, true>(a, st) : launch_bwd<float, false>(a, st);
+hipError_t launch_pass(const ScanArgs &a, bool bf, int cj, hipStream_t st) {
+  return bf ? launch_pass<uint16_t, MODE>(a, cj, st) : launch_pass<float, MODE>(a, cj, st);
 }
 
 template <typename T>
-hipError_t launch_step(const ScanArgs &a, hipStream_t st) {
-  const long long blocks = (long long)a.B * a.G * a.tiles;
+hipError_t launch_bwd(ScanArgs a, const ScanPlan &p, hipStream_t st) {
+  a.tiles = p.bwd_tiles;
+  const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
+  const int threads = 64 * p.bwd_waves;
   switch (state_regs(a.N)) {
-    case 1: return launch(scan_step_kernel<T, 1>, blocks, st, a);
-    case 2: return launch(scan_step_kernel<T, 2>, blocks, st, a);
-    case 4: return launch(scan_step_kernel<T, 4>, blocks, st, a);
-    case 8: return launch(scan_step_kernel<T, 8>, blocks, st, a);
-    default: return launch(scan_step_kernel<T, 16>, blocks, st, a);
+    case 1: return launch(scan_bwd_kernel<T, 1>, blocks, threads, st, a);
+    case 2: return launch(scan_bwd_kernel<T, 2>, blocks, threads, st, a);
+    case 4: return launch(scan_bwd_kernel<T, 4>, blocks, threads, st, a);
+    case 8: return launch(scan_bwd_kernel<T, 8>, blocks, threads, st, a);
+    default: return launch(scan_bwd_kernel<T, 16>, blocks, threads, st, a);
   }
 }
 
-hipError_t launch_combine(const ScanArgs &a, hipStream_t st) {
-  return launch(scan_combine_kernel, rec_cdiv((long long)a.B * a.D * a.N, NT), st, a);
+template <typename T, int SQ>
+hipError_t launch_step(ScanArgs a, hipStream_t st) {
+  a.tiles = (int)rec_cdiv(a.Dg, STEP_CH);
+  const long long blocks = rec_cdiv(a.B, SQ) * a.G * a.tiles;
+  switch (state_regs(a.N)) {
+    case 1: return launch(scan_step_kernel<T, 1, SQ>, blocks, NT, st, a);
+    case 2: return launch(scan_step_kernel<T, 2, SQ>, blocks, NT, st, a);
+    case 4: return launch(scan_step_kernel<T, 4, SQ>, blocks, NT, st, a);
+    case 8: return launch(scan_step_kernel<T, 8, SQ>, blocks, NT, st, a);
+    default: return launch(scan_step_kernel<T, 16, SQ>, blocks, NT, st, a);
+  }
+}
+// Four sequences a workgroup where that still leaves four workgroups a CU.
+template <typename T>
+hipError_t launch_step(const ScanArgs &a, hipStream_t st) {
+  const bool many = (long long)a.B * a.G * rec_cdiv(a.Dg, STEP_CH) >= 4096;
+  return many ? launch_step<T, 4>(a, st) : launch_step<T, 1>(a, st);
 }
 
-hipError_t column_sum(const float *part, float *out, int rows, long long cols, hipStream_t st) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)rec_cdiv(cols, 64)), dim3(NT), 0, st, part, out, rows, cols);
-  return hipGetLastError();
+hipError_t launch_combine(const ScanArgs &a, hipStream_t st) {
+  return launch(scan_combine_kernel, rec_cdiv((long long)a.B * a.D * a.N, NT), NT, st, a);
 }
 
 ScanArgs scan_args(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
                    const float *D_skip, const void *z, const float *bias, const int *lengths, int B, int L, int D,
                    int N, int G, long long u_ld, long long delta_ld, long long z_ld, long long b_ld, long long c_ld,
-                   int softplus, ret_dtype_t out_dtype) {
+                   int softplus, ret_dtype_t in_dtype, ret_dtype_t out_dtype) {
   ScanArgs a = {};
   a.u = u;
   a.delta = delta;
@@ -672,10 +1070,21 @@ ScanArgs scan_args(const void *u, const void *delta, const float *A, const void 
   a.N = N;
   a.G = G;
   a.Dg = D / G;
-  a.tiles = (int)rec_cdiv(a.Dg, CH);
   a.softplus = softplus != 0;
   a.out_bf16 = out_dtype == RET_BF16;
+  const size_t e = rec_esize(in_dtype);
+  a.vec = a.Dg % 4 == 0 && wide(u, u_ld, e) && wide(delta, delta_ld, e) && wide(z, z_ld, e);
+  a.vec_bc = N % 4 == 0 && wide(Bm, b_ld, e) && wide(Cm, c_ld, e);
   return a;
+}
+
+// States may be accessed by fours: the caller's, A, and the workspace's.
+bool wide_states(const ScanArgs &a) {
+  const void *ps[] = {a.A, a.h0, a.hT, a.dhT, a.dh0, a.seg};
+  if (a.N % 4) return false;
+  for (const void *p : ps)
+    if (!rec_aligned(p, 16)) return false;
+  return true;
 }
 
 // Pointers, strides and alignment of the inputs that all three calls share.
@@ -719,7 +1128,7 @@ ret_status_t selective_scan(const void *u, const void *delta, const float *A, co
   const size_t e = rec_esize(in_dtype), oe = rec_esize(out_dtype), ns = (size_t)B * D * N * 4;
   const long long rows = (long long)B * L;
   ScanArgs a = scan_args(u, delta, A, Bm, Cm, D_skip, z, delta_bias, lengths, B, L, D, N, G, u_ld, delta_ld, z_ld, b_ld,
-                         c_ld, delta_softplus, out_dtype);
+                         c_ld, delta_softplus, in_dtype, out_dtype);
   a.h0 = state_in;
   a.hT = state_out;
   a.out = out;
@@ -753,14 +1162,14 @@ ret_status_t selective_scan(const void *u, const void *delta, const float *A, co
   a.seg = (float *)((char *)workspace + p.seg);
   a.sdt = (float *)((char *)workspace + p.sdt);
   const bool bf = in_dtype == RET_BF16;
-  const bool vec = a.Dg % 4 == 0 && wide(u, u_ld, e) && wide(delta, delta_ld, e) && wide(z, z_ld, e) &&
-                   wide(out, D, oe);
+  a.vec = a.vec && wide(out, D, oe);
+  a.vec_n = wide_states(a);
   hipError_t err = hipSuccess;
   if (p.nseg > 1) {
-    if ((err = launch_pass<STATES>(a, bf, vec, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess)
+    if ((err = launch_pass<STATES>(a, bf, p.cj, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess)
       return rec_status(err);
   }
-  return rec_status(launch_pass<OUTPUT>(a, bf, vec, st));
+  return rec_status(launch_pass<OUTPUT>(a, bf, p.cj, st));
 }
 
 ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
@@ -777,7 +1186,7 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   const long long rows = (long long)B * L, bc = (long long)G * N;
   hipStream_t st = (hipStream_t)hip_stream;
   ScanArgs a = scan_args(u, delta, A, Bm, Cm, D_skip, z, delta_bias, lengths, B, L, D, N, G, u_ld, delta_ld, z_ld, b_ld,
-                         c_ld, delta_softplus, out_dtype);
+                         c_ld, delta_softplus, in_dtype, out_dtype);
   a.h0 = state_in;
   a.dhT = d_state_out;
   a.d_o = d_o;
@@ -835,19 +1244,20 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   a.dDpart = (float *)(ws + p.dDpart);
   a.dbpart = (float *)(ws + p.dbpart);
   const bool bf = in_dtype == RET_BF16;
-  const bool vec = a.Dg % 4 == 0 && wide(u, u_ld, e) && wide(delta, delta_ld, e) && wide(z, z_ld, e) &&
-                   wide(d_o, D, e) && wide(du, D, oe) && wide(ddelta, D, oe) && wide(dz, D, oe);
+  a.vec = a.vec && wide(d_o, D, e) && wide(du, D, oe) && wide(ddelta, D, oe) && wide(dz, D, oe);
+  a.vec_n = wide_states(a);
   hipError_t err;
-  if ((err = launch_pass<CHECKPOINTS>(a, bf, vec, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess ||
-      (err = launch_bwd(a, bf, vec, st)) != hipSuccess)
+  if ((err = launch_pass<CHECKPOINTS>(a, bf, p.cj, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess ||
+      (err = bf ? launch_bwd<uint16_t>(a, p, st) : launch_bwd<float>(a, p, st)) != hipSuccess)
     return rec_status(err);
-  if (lengths && (err = launch(scan_bwd_tail_kernel, rows, st, a)) != hipSuccess) return rec_status(err);
+  if (lengths && (err = launch(scan_bwd_tail_kernel, rows, NT, st, a)) != hipSuccess) return rec_status(err);
+  a.tiles = p.bwd_tiles;
   hipLaunchKernelGGL(scan_reduce_bc_kernel, dim3((unsigned)rec_cdiv(rows * 2 * bc, NT)), dim3(NT), 0, st, a, dB, dC);
   if ((err = hipGetLastError()) != hipSuccess) return rec_status(err);
   const int parts = B * p.nseg;
-  if ((err = column_sum(a.dApart, dA, parts, (long long)D * N, st)) != hipSuccess) return rec_status(err);
-  if (dD && (err = column_sum(a.dDpart, dD, parts, D, st)) != hipSuccess) return rec_status(err);
-  if (ddelta_bias && (err = column_sum(a.dbpart, ddelta_bias, parts, D, st)) != hipSuccess) return rec_status(err);
+  if ((err = column_sum(a.dApart, dA, nullptr, parts, (long long)D * N, 0, st)) != hipSuccess) return rec_status(err);
+  if (dD && (err = column_sum(a.dDpart, dD, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
+  if (ddelta_bias && (err = column_sum(a.dbpart, ddelta_bias, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
   return rec_status(hipSuccess);
 }
 
@@ -860,7 +1270,7 @@ ret_status_t selective_scan_step(const void *u, const void *delta, const float *
   if (s != RET_OK) return s;
   const size_t e = rec_esize(in_dtype), oe = rec_esize(out_dtype);
   ScanArgs a = scan_args(u, delta, A, Bm, Cm, D_skip, z, delta_bias, nullptr, B, 1, D, N, G, u_ld, delta_ld, z_ld, b_ld,
-                         c_ld, delta_softplus, out_dtype);
+                         c_ld, delta_softplus, in_dtype, out_dtype);
   a.out = out;
   a.hT = state;
   if ((s = check_inputs(a, e)) != RET_OK) return s;
@@ -873,6 +1283,7 @@ ret_status_t selective_scan_step(const void *u, const void *delta, const float *
                          {"D_skip", D_skip, (size_t)D * 4}, {"delta_bias", delta_bias, (size_t)D * 4}};
   const RecSpan outs[] = {{"out", out, (size_t)B * D * oe}, {"state", state, (size_t)B * D * N * 4}};
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
+  a.vec_n = wide_states(a);
   hipStream_t st = (hipStream_t)hip_stream;
   return rec_status(in_dtype == RET_BF16 ? launch_step<uint16_t>(a, st) : launch_step<float>(a, st));
 }
