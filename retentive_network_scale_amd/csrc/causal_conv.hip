@@ -1,9 +1,10 @@
 // Short causal depthwise convolution (recurrent.h): c_t = act(bias + sum_j w_j x_{t-K+1+j}),
 // its gradients and its single-token form.
 //
-// Every kernel streams: a thread keeps VC neighbouring channels (16 bytes of them where
-// rows are aligned), their taps and a window of the last K inputs in registers and walks
-// a run of tokens, so each input is read once but for the K - 1 in front of a run.
+// Every kernel streams: a thread keeps VC neighbouring channels (four, where rows are
+// aligned to them), their taps and a window of the last K inputs in registers and walks
+// a run of tokens, so each input is read once but for the K - 1 in front of a run.  The
+// loads of a step's tokens go out together.
 #include <algorithm>
 
 #include "recurrent.hpp"
@@ -13,13 +14,14 @@ using namespace ret;
 namespace {
 
 constexpr int NT = 256;
-constexpr int STEP = 8;  // tokens whose loads are issued together
+constexpr int STEP = 8;    // tokens whose loads the forward issues together
+constexpr int WAVES = NT / 64;
 
 struct ConvArgs {
   const void *x, *w, *bias, *h0, *d_o, *dhT;
   const int *lengths;
   void *out, *hT, *dx, *dh0;
-  float *part;  // [B * runs][D][K + 1]: dw, dbias
+  float *part;  // [B * runs / WAVES][D][K + 1]: dw, dbias
   long long x_ld;
   int B, L, D, K, run, runs, silu;
   long long main_threads, state_at;  // runs' threads; the first of the state's, a workgroup's start behind them
@@ -27,33 +29,27 @@ struct ConvArgs {
 
 template <typename T, int VC>
 __device__ __forceinline__ void loadc(const T *p, float (&r)[VC]) {
-  if constexpr (VC == 8) {
-    const uint4 v = *(const uint4 *)p;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r[2 * i] = __uint_as_float(w[i] << 16);
-      r[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  if constexpr (VC == 4 && sizeof(T) == 2) {
+    const uint2 v = *(const uint2 *)p;
+    r[0] = __uint_as_float(v.x << 16);
+    r[1] = __uint_as_float(v.x & 0xffff0000u);
+    r[2] = __uint_as_float(v.y << 16);
+    r[3] = __uint_as_float(v.y & 0xffff0000u);
   } else if constexpr (VC == 4) {
     const float4 v = *(const float4 *)p;
     r[0] = v.x;
     r[1] = v.y;
     r[2] = v.z;
     r[3] = v.w;
-  } else if constexpr (sizeof(T) == 2) {
-    r[0] = bf2f(p[0]);
   } else {
-    r[0] = p[0];
+    r[0] = load_elem(p, 0, sizeof(T) == 2);
   }
 }
 
 template <typename T, int VC>
 __device__ __forceinline__ void storec(T *p, const float (&r)[VC]) {
-  if constexpr (VC == 8)
-    *(uint4 *)p = make_uint4(pack_bf2(r[0], r[1]), pack_bf2(r[2], r[3]), pack_bf2(r[4], r[5]), pack_bf2(r[6], r[7]));
-  else if constexpr (VC == 4)
-    *(float4 *)p = make_float4(r[0], r[1], r[2], r[3]);
+  if constexpr (VC == 4)
+    store4<true>(p, 0, 4, r, sizeof(T) == 2);
   else
     store_elem(p, 0, r[0], sizeof(T) == 2);
 }
@@ -134,89 +130,116 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
 // Gradients.  With g_t = d_o_t act'(pre_t): dx_s = sum_j w_j g_{s+K-1-j}, dw_j = sum_t g_t
 // x_{t-K+1+j}, dbias = sum_t g_t.  A thread walks its run's tokens and K - 1 more, whose
 // g the last inputs of the run need; the first run also covers the K - 1 inputs of the
-// state in front.
+// state in front.  The workgroup's waves take neighbouring runs of the same channels and
+// add up their dw and dbias.
 template <typename T, int K, int VC>
 __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
-  const int dv = a.D / VC;
-  const long long id = (long long)blockIdx.x * NT + threadIdx.x;
-  if (id >= a.main_threads) return;
-  const int d = (int)(id % dv) * VC, k = (int)(id / dv % a.runs);
-  const long long b = id / dv / a.runs;
+  constexpr int S = 4;
+  __shared__ float red[WAVES][VC * (K + 1)][64];
+  const int dv = a.D / VC, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int chunks = (dv + 63) / 64, groups = (a.runs + WAVES - 1) / WAVES;
+  const int chunk = (int)(blockIdx.x % chunks) * 64 + lane, rg = (int)(blockIdx.x / chunks % groups);
+  const long long b = blockIdx.x / chunks / groups;
+  const int k = rg * WAVES + wave, d = min(chunk, dv - 1) * VC;
   const int len = length_of(a, b), t0 = k * a.run, t1 = min(t0 + a.run, len);
-  float w[K][VC], bias[VC], x[K][VC], g[K][VC], dw[K][VC], db[VC];
-  load_taps<T, K, VC>(a, d, w, bias);
+  float dw[K][VC], db[VC];
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
     db[c] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < K; ++j) x[j][c] = g[j][c] = dw[j][c] = 0.0f;
+    for (int j = 0; j < K; ++j) dw[j][c] = 0.0f;
   }
-  if (t0 < t1 || k == 0) {
+  if (chunk < dv && k < a.runs) {
+    if (t0 < t1 || k == 0) {
+      float w[K][VC], bias[VC], x[K - 1 + S][VC], g[K - 1 + S][VC];
+      load_taps<T, K, VC>(a, d, w, bias);
 #pragma unroll
-    for (int j = 1; j < K; ++j) input_at<T, K, VC>(a, b, t0 - K + j, d, x[j]);  // x[j]: input t0 - K + j
-    // the loop's token t closes input s = t - (K - 1); the first run starts with s = -(K - 1)
-    for (int t = t0; t < max(t1, t0) + K - 1; ++t) {
+      for (int j = 0; j < K - 1; ++j) {
+        input_at<T, K, VC>(a, b, t0 - (K - 1) + j, d, x[j]);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j)
+        for (int c = 0; c < VC; ++c) g[j][c] = 0.0f;
+      }
+      // token t closes input s = t - (K - 1); the first run starts with s = -(K - 1)
+      const int end = max(t1, t0) + K - 1;
+      for (int t = t0; t < end; t += S) {
+        float go[S][VC];
 #pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          x[j][c] = x[j + 1][c];
-          g[j][c] = g[j + 1][c];
-        }
-      if (t < len) {
-        float go[VC];
-        input_at<T, K, VC>(a, b, t, d, x[K - 1]);
-        loadc<T, VC>((const T *)a.d_o + (b * a.L + t) * a.D + d, go);
-#pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          float s = bias[c];
-#pragma unroll
-          for (int j = 0; j < K; ++j) s += w[j][c] * x[j][c];
-          const float sg = sigmoid(s);
-          g[K - 1][c] = a.silu ? go[c] * sg * (1.0f + s * (1.0f - sg)) : go[c];
-          if (t < t1) {
-            db[c] += g[K - 1][c];
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][c] += g[K - 1][c] * x[j][c];
+        for (int i = 0; i < S; ++i) {  // tokens behind the end: any inside, and no g
+          const int r = min(t + i, len - 1);
+          if (len > 0) {
+            loadc<T, VC>((const T *)a.x + (b * a.L + r) * a.x_ld + d, x[K - 1 + i]);
+            loadc<T, VC>((const T *)a.d_o + (b * a.L + r) * a.D + d, go[i]);
           }
         }
-      } else {
 #pragma unroll
-        for (int c = 0; c < VC; ++c) x[K - 1][c] = g[K - 1][c] = 0.0f;
+        for (int i = 0; i < S; ++i) {
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            float s = bias[c];
+#pragma unroll
+            for (int j = 0; j < K; ++j) s += w[j][c] * x[i + j][c];
+            const float sg = sigmoid(s), v = a.silu ? go[i][c] * sg * (1.0f + s * (1.0f - sg)) : go[i][c];
+            g[K - 1 + i][c] = t + i < len ? v : 0.0f;
+            if (t + i < t1) {
+              db[c] += g[K - 1 + i][c];
+#pragma unroll
+              for (int j = 0; j < K; ++j) dw[j][c] += g[K - 1 + i][c] * x[i + j][c];
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int s = t + i - (K - 1);
+          if (t + i >= end || (s < t0 && k > 0)) continue;  // the run in front closes the latter
+          float dx[VC];
+          const int q = s - (len - (K - 1));  // its place in the final state
+          if (a.dhT && q >= 0 && q < K - 1) {
+            loadc<T, VC>((const T *)a.dhT + (b * (K - 1) + q) * a.D + d, dx);
+          } else {
+#pragma unroll
+            for (int c = 0; c < VC; ++c) dx[c] = 0.0f;
+          }
+#pragma unroll
+          for (int c = 0; c < VC; ++c)
+#pragma unroll
+            for (int j = 0; j < K; ++j) dx[c] += w[j][c] * g[K - 1 + i - j][c];
+          if (s >= 0)
+            storec<T, VC>((T *)a.dx + (b * a.L + s) * a.D + d, dx);
+          else if (a.dh0)
+            storec<T, VC>((T *)a.dh0 + (b * (K - 1) + s + K - 1) * a.D + d, dx);
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            x[j][c] = x[S + j][c];
+            g[j][c] = g[S + j][c];
+          }
       }
-      const int s = t - (K - 1);
-      if (s < t0 && k > 0) continue;  // the run in front closes these
-      float dx[VC];
-      const int q = s - (len - (K - 1));  // its place in the final state
-      if (a.dhT && q >= 0 && q < K - 1) {
-        loadc<T, VC>((const T *)a.dhT + (b * (K - 1) + q) * a.D + d, dx);
-      } else {
+    }
+    // rows behind the end
+    for (int t = max(t0, len); t < min(t0 + a.run, a.L); ++t) {
+      float zero[VC];
 #pragma unroll
-        for (int c = 0; c < VC; ++c) dx[c] = 0.0f;
-      }
-#pragma unroll
-      for (int c = 0; c < VC; ++c)
-#pragma unroll
-        for (int j = 0; j < K; ++j) dx[c] += w[j][c] * g[K - 1 - j][c];
-      if (s >= 0)
-        storec<T, VC>((T *)a.dx + (b * a.L + s) * a.D + d, dx);
-      else if (a.dh0)
-        storec<T, VC>((T *)a.dh0 + (b * (K - 1) + s + K - 1) * a.D + d, dx);
+      for (int c = 0; c < VC; ++c) zero[c] = 0.0f;
+      storec<T, VC>((T *)a.dx + (b * a.L + t) * a.D + d, zero);
     }
   }
-  // rows behind the end
-  for (int t = max(t0, len); t < min(t0 + a.run, a.L); ++t) {
-    float zero[VC];
-#pragma unroll
-    for (int c = 0; c < VC; ++c) zero[c] = 0.0f;
-    storec<T, VC>((T *)a.dx + (b * a.L + t) * a.D + d, zero);
-  }
-  float *p = a.part + ((b * a.runs + k) * a.D + d) * (K + 1);
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) p[c * (K + 1) + j] = dw[j][c];
-    p[c * (K + 1) + K] = db[c];
+    for (int j = 0; j < K; ++j) red[wave][c * (K + 1) + j][lane] = dw[j][c];
+    red[wave][c * (K + 1) + K][lane] = db[c];
+  }
+  __syncthreads();
+  float *p = a.part + (b * groups + rg) * a.D * (K + 1) + (long long)(blockIdx.x % chunks) * 64 * VC * (K + 1);
+  const int have = min(dv - (int)(blockIdx.x % chunks) * 64, 64) * VC * (K + 1);
+  for (int e = threadIdx.x; e < have; e += NT) {
+    const int l = e / (VC * (K + 1)), i = e % (VC * (K + 1));
+    float s = red[0][i][l];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) s += red[v][i][l];
+    p[e] = s;
   }
 }
 
@@ -250,7 +273,8 @@ enum { FWD, BWD, ONE };
 
 template <int WHAT, typename T, int K, int VC>
 hipError_t launch_k(const ConvArgs &a, long long threads, hipStream_t st) {
-  const dim3 grid((unsigned)rec_cdiv(threads, NT));
+  dim3 grid((unsigned)rec_cdiv(threads, NT));
+  if (WHAT == BWD) grid.x = (unsigned)(rec_cdiv(a.D / VC, 64) * rec_cdiv(a.runs, WAVES) * a.B);
   if constexpr (WHAT == FWD)
     hipLaunchKernelGGL((conv_fwd_kernel<T, K, VC>), grid, dim3(NT), 0, st, a);
   else if constexpr (WHAT == BWD)
@@ -273,7 +297,7 @@ hipError_t launch_vc(const ConvArgs &a, long long threads, hipStream_t st) {
 }
 template <int WHAT>
 hipError_t launch(const ConvArgs &a, bool bf, int vc, long long threads, hipStream_t st) {
-  if (bf) return vc > 1 ? launch_vc<WHAT, uint16_t, 8>(a, threads, st) : launch_vc<WHAT, uint16_t, 1>(a, threads, st);
+  if (bf) return vc > 1 ? launch_vc<WHAT, uint16_t, 4>(a, threads, st) : launch_vc<WHAT, uint16_t, 1>(a, threads, st);
   return vc > 1 ? launch_vc<WHAT, float, 4>(a, threads, st) : launch_vc<WHAT, float, 1>(a, threads, st);
 }
 
@@ -290,13 +314,12 @@ ret_status_t check_sizes(int B, int L, int D, int K, long long x_ld, ret_dtype_t
   return RET_OK;
 }
 
-// Channels a thread takes: 16 bytes of them where every tensor of the call allows it.
+// Channels a thread takes: four where every tensor of the call allows it.
 int channels(const void *const *ps, int n, int D, long long x_ld, size_t e) {
-  const int vc = 16 / (int)e;
-  if (D % vc || x_ld % vc) return 1;
+  if (D % 4 || x_ld % 4) return 1;
   for (int i = 0; i < n; ++i)
-    if (!rec_aligned(ps[i], 16)) return 1;
-  return vc;
+    if (!rec_aligned(ps[i], 4 * e)) return 1;
+  return 4;
 }
 
 // Tokens a thread walks: long runs reread fewer of the K - 1 tokens in front, short
@@ -309,19 +332,19 @@ void set_runs(ConvArgs &a, int vc, int most) {
   a.runs = (int)rec_cdiv(a.L, run);
   a.main_threads = per * a.runs;
 }
-constexpr int FWD_RUN = 64, BWD_RUN = 128;
+constexpr int FWD_RUN = 64, BWD_RUN = 64;
 
-// Runs of the backward for the workspace: those of the narrowest kernel, the most.
-int bwd_runs(int B, int L, int D) {
+// Partial sums of the backward: workgroups along the tokens, of the kernel that has the most.
+long long bwd_parts(int B, int L, int D) {
   ConvArgs a = {};
   a.B = B;
   a.L = L;
   a.D = D;
-  int most = 0;
-  for (int vc : {1, 4, 8})
+  long long most = 0;
+  for (int vc : {1, 4})
     if (D % vc == 0) {
       set_runs(a, vc, BWD_RUN);
-      most = std::max(most, a.runs);
+      most = std::max(most, B * rec_cdiv(a.runs, WAVES));
     }
   return most;
 }
@@ -373,7 +396,7 @@ ret_status_t causal_conv1d(const void *x, const void *w, const void *bias, void 
 size_t causal_conv1d_bwd_workspace_bytes(int B, int L, int D, int K) {
   if (B <= 0 || L <= 0 || D <= 0 || K < 2 || K > RECURRENT_MAX_TAPS) return 0;
   if ((long long)B * L > RECURRENT_MAX_TOKENS || (double)B * L * D > RECURRENT_MAX_ELEMENTS) return 0;
-  return rec_align((size_t)B * bwd_runs(B, L, D) * D * (K + 1) * 4);
+  return rec_align((size_t)bwd_parts(B, L, D) * D * (K + 1) * 4);
 }
 
 ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, const void *d_o, const int *lengths,
@@ -441,7 +464,7 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
   set_runs(a, vc, BWD_RUN);
   hipError_t err = launch<BWD>(a, bf, vc, a.main_threads, st);
   if (err != hipSuccess) return rec_status(err);
-  return rec_status(column_sum(a.part, dw, dbias, (long long)B * a.runs, (long long)D * (K + 1), K + 1, st));
+  return rec_status(column_sum(a.part, dw, dbias, B * rec_cdiv(a.runs, WAVES), (long long)D * (K + 1), K + 1, st));
 }
 
 ret_status_t causal_conv1d_step(const void *x, const void *w, const void *bias, void *out, void *state, int B, int D,

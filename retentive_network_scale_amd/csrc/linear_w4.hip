@@ -36,16 +36,16 @@ struct W4Args {
   int M, N, K, group, out_bf16;
 };
 
-// Eight elements of x in the order 0 4 1 5 2 6 3 7.
+// Eight elements of x, as loaded and in the order 0 4 1 5 2 6 3 7.
 template <bool VEC>
-__device__ __forceinline__ bf16x8 load_x(const uint16_t *p) {
+__device__ __forceinline__ u32x4 load_x(const uint16_t *p) {
+  if constexpr (VEC) return *(const u32x4 *)p;
   u32x4 v;
-  if constexpr (VEC) {
-    v = *(const u32x4 *)p;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-  }
+  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+  return v;
+}
+__device__ __forceinline__ bf16x8 permuted(u32x4 v) {
   u32x4 r;
   r[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
   r[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
@@ -71,6 +71,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4_kernel(W4Args a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, kq = lane >> 4;
   const int n = blockIdx.x * 16 + col, nr = min(n, a.N - 1), m0 = blockIdx.y * MT * 16;
   constexpr int KB = WORDS * 32;  // k per block
+  constexpr int U = 16 / (WORDS * MT) < 1 ? 1 : 16 / (WORDS * MT) > 4 ? 4 : 16 / (WORDS * MT);
   const int groups = a.K / a.group;
   const uint32_t *q = a.q + (long long)nr * (a.K / 8) + kq * WORDS;
   const uint16_t *scale = a.scale + (long long)nr * groups;
@@ -81,34 +82,51 @@ __global__ __launch_bounds__(WAVES * 64) void w4_kernel(W4Args a) {
   f32x4 tot[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) tot[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = wave; kb < a.K / KB; kb += WAVES) {
-    uint32_t w[WORDS];
-    if constexpr (WORDS == 4) {
-      const u32x4 v = *(const u32x4 *)(q + (long long)kb * 16);
+  const int blocks = a.K / KB;
+  for (int kb0 = wave; kb0 < blocks; kb0 += WAVES * U) {
+    // everything that U blocks need is requested before the first is used: a wave has few
+    // blocks, and their latency is most of its time.  Blocks behind the end: the last one
+    // again, with scale 0.
+    uint32_t w[U][WORDS], z[U];
+    u32x4 xv[U][MT][WORDS];
+    float s[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = v[i];
-    } else if constexpr (WORDS == 2) {
-      const uint2 v = *(const uint2 *)(q + (long long)kb * 8);
-      w[0] = v.x;
-      w[1] = v.y;
-    } else {
-      w[0] = q[(long long)kb * 4];
-    }
-    const int g = (int)((long long)kb * KB / a.group);
-    const uint32_t off = (0xC180u | (zero ? zero[g] & 15u : 8u) << 3) * 0x10001u;
-    const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
-    const float s = bf2f(scale[g]);
+    for (int u = 0; u < U; ++u) {
+      const int kb = min(kb0 + u * WAVES, blocks - 1), g = (int)((long long)kb * KB / a.group);
+      if constexpr (WORDS == 4) {
+        const u32x4 v = *(const u32x4 *)(q + (long long)kb * 16);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i) {
-        const bf16x8 xv = load_x<VEC>(x[m] + (long long)kb * KB + i * 8);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, unpack(w[i]), acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, minus, acc, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) w[u][i] = v[i];
+      } else if constexpr (WORDS == 2) {
+        const uint2 v = *(const uint2 *)(q + (long long)kb * 8);
+        w[u][0] = v.x;
+        w[u][1] = v.y;
+      } else {
+        w[u][0] = q[(long long)kb * 4];
       }
+      z[u] = zero ? zero[g] & 15u : 8u;
+      s[u] = kb0 + u * WAVES < blocks ? bf2f(scale[g]) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tot[m][i] += s * acc[i];
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) xv[u][m][i] = load_x<VEC>(x[m] + (long long)kb * KB + i * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t off = (0xC180u | z[u] << 3) * 0x10001u;
+      const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+          const bf16x8 xp = permuted(xv[u][m][i]);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp, unpack(w[u][i]), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp, minus, acc, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[m][i] += s[u] * acc[i];
+      }
     }
   }
 #pragma unroll
@@ -136,10 +154,13 @@ hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
     hipLaunchKernelGGL((w4_kernel<MT, WORDS, WAVES, false>), grid, dim3(WAVES * 64), 0, st, a);
   return hipGetLastError();
 }
+// Sixteen waves a workgroup where the grid alone does not give every CU eight.
 template <int MT>
-hipError_t launch_words(const W4Args &a, bool vec, hipStream_t st) {
-  if (a.group % 128 == 0) return launch_w<MT, 4, 8>(a, vec, st);
-  return a.group == 64 ? launch_w<MT, 2, 8>(a, vec, st) : launch_w<MT, 1, 8>(a, vec, st);
+hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
+  const bool few = rec_cdiv(a.N, 16) * rec_cdiv(a.M, MT * 16) <= 256;
+  if (a.group % 128 == 0) return few ? launch_w<MT, 4, 16>(a, vec, st) : launch_w<MT, 4, 8>(a, vec, st);
+  if (a.group == 64) return few ? launch_w<MT, 2, 16>(a, vec, st) : launch_w<MT, 2, 8>(a, vec, st);
+  return few ? launch_w<MT, 1, 16>(a, vec, st) : launch_w<MT, 1, 8>(a, vec, st);
 }
 
 }  // namespace
@@ -174,7 +195,13 @@ hipError_t launch_w4(const void *x, const void *q, const void *scale, const void
   a.group = group;
   a.out_bf16 = out_bf16;
   const bool vec = x_ld % 8 == 0 && rec_aligned(x, 16);
-  return M <= 16 ? launch_words<1>(a, vec, st) : M <= 32 ? launch_words<2>(a, vec, st) : launch_words<4>(a, vec, st);
+  // Tokens per workgroup: 64 read a weight once; where that leaves CUs idle, fewer tokens
+  // and more workgroups, whose weights then come from L2 (N / 16 workgroups apart, a
+  // multiple of the eight dies in the usual case).
+  const long long rows = rec_cdiv(N, 16);
+  if (M > 32 && rows * rec_cdiv(M, 64) >= 512) return launch_mt<4>(a, vec, st);
+  if (M > 16 && rows * rec_cdiv(M, 32) >= 512) return launch_mt<2>(a, vec, st);
+  return launch_mt<1>(a, vec, st);
 }
 
 }  // namespace ret

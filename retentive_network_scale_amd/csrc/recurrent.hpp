@@ -71,38 +71,7 @@ hipError_t column_sum(const float *part, float *out, float *last, long long rows
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)1.4426950408889634f);
 
-// Four consecutive elements from p (n of them valid, the others 0).  VEC: all four
-// are there and p is aligned to them.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T *p, int n, float (&r)[4]) {
-  if constexpr (VEC) {
-    if constexpr (sizeof(T) == 2) {
-      const uint2 x = *(const uint2 *)p;
-      r[0] = __uint_as_float(x.x << 16);
-      r[1] = __uint_as_float(x.x & 0xffff0000u);
-      r[2] = __uint_as_float(x.y << 16);
-      r[3] = __uint_as_float(x.y & 0xffff0000u);
-    } else {
-      const float4 x = *(const float4 *)p;
-      r[0] = x.x;
-      r[1] = x.y;
-      r[2] = x.z;
-      r[3] = x.w;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      r[c] = 0.0f;
-      if (c < n) {
-        if constexpr (sizeof(T) == 2)
-          r[c] = bf2f(p[c]);
-        else
-          r[c] = p[c];
-      }
-    }
-  }
-}
-
+// Four consecutive elements to base + off: the first n of them, or all, aligned (VEC).
 template <bool VEC>
 __device__ __forceinline__ void store4(void *base, long long off, int n, const float (&r)[4], bool bf16) {
   if constexpr (VEC) {

@@ -38,7 +38,8 @@ struct ScanArgs {
   long long u_ld, delta_ld, z_ld, b_ld, c_ld;
   int B, L, D, N, G, Dg, tiles;  // Dg = D / G channels per group, tiles of them per workgroup
   int seg_len, nseg, softplus, out_bf16;
-  int vec, vec_bc, vec_n;  // rows of channels, of B and C, and states may be accessed by fours
+  int span, nspan;  // segments that a workgroup of the backward's main pass walks, and how many such spans
+  int vec;  // everything may be accessed by fours: channels, states, B and C
   // workspace: segment states [B * nseg][D][N], sums of dt [B * nseg][D]
   float *seg, *sdt;
   // backward
@@ -46,7 +47,7 @@ struct ScanArgs {
   float *gseg;        // gradients entering the segments from behind, [B * nseg][D][N]
   float *ck, *ckdt;   // per sub-tile: state relative to the segment, sum of dt before it
   float *bcpart;      // [tiles][B * L][G][2][N]
-  float *dApart, *dDpart, *dbpart;  // [B * nseg][D][N], [B * nseg][D]
+  float *dApart, *dDpart, *dbpart;  // [B * nspan][D][N], [B * nspan][D]
   float *dh0;
   int subs;           // sub-tiles per segment
 };
@@ -56,15 +57,16 @@ struct ScanArgs {
 constexpr int wide_cj(int NS) { return NS <= 4 ? 4 : 16 / NS; }
 
 // Channels per lane and tokens per sub-tile of the backward's main pass: a sub-tile's
-// states and decays, 2 SUB CJ NS fp32, stay in 128 registers.
+// states, SUB CJ NS fp32, stay in 64 registers.
 constexpr int bwd_cj(int NS) { return NS >= 8 ? 1 : 2; }
 constexpr int bwd_sub(int NS) { return std::min(TT, 64 / (NS * bwd_cj(NS))); }
 constexpr int BWD_WAVES = 4;
 
-// What a workgroup works on.
+// What a workgroup works on: a segment, or a span of them.
 struct Where {
   int b, s, g, tile, len, t_lo, t_hi;
 };
+template <bool SPANS>
 __device__ __forceinline__ Where where(const ScanArgs &a) {
   Where w;
   int id = blockIdx.x;
@@ -72,11 +74,12 @@ __device__ __forceinline__ Where where(const ScanArgs &a) {
   id /= a.tiles;
   w.g = id % a.G;
   id /= a.G;
-  w.s = id % a.nseg;
-  w.b = id / a.nseg;
+  const int parts = SPANS ? a.nspan : a.nseg, tokens = SPANS ? a.span * a.seg_len : a.seg_len;
+  w.s = id % parts;
+  w.b = id / parts;
   w.len = a.lengths ? min(max(a.lengths[w.b], 0), a.L) : a.L;
-  w.t_lo = min(w.s * a.seg_len, w.len);
-  w.t_hi = min(w.t_lo + a.seg_len, w.len);
+  w.t_lo = (int)min((long long)w.s * tokens, (long long)w.len);
+  w.t_hi = (int)min((long long)w.t_lo + tokens, (long long)w.len);
   return w;
 }
 
@@ -115,52 +118,49 @@ __device__ __forceinline__ float row16_sum(float x) {
   return x;
 }
 
-// NS states of a lane from n0 on; vec: N and n0 are multiples of four, p is aligned.
-template <int NS>
-__device__ __forceinline__ void load_state(const float *p, int N, int n0, bool ok, bool vec, float (&h)[NS]) {
-  if constexpr (NS % 4 == 0) {
-    if (vec) {
+// NS states of a lane from n0 on.  VEC: N and n0 are multiples of four, p is aligned.
+template <int NS, bool VEC>
+__device__ __forceinline__ void load_state(const float *p, int N, int n0, bool ok, float (&h)[NS]) {
+  if constexpr (VEC && NS % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < NS; i += 4) {
-        const float4 v = ok && n0 + i < N ? *(const float4 *)(p + n0 + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        h[i] = v.x;
-        h[i + 1] = v.y;
-        h[i + 2] = v.z;
-        h[i + 3] = v.w;
-      }
-      return;
+    for (int i = 0; i < NS; i += 4) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (ok && n0 + i < N) v = *(const float4 *)(p + n0 + i);
+      h[i] = v.x;
+      h[i + 1] = v.y;
+      h[i + 2] = v.z;
+      h[i + 3] = v.w;
     }
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < NS; ++i) h[i] = ok && n0 + i < N ? p[n0 + i] : 0.0f;
+    for (int i = 0; i < NS; ++i) h[i] = ok && n0 + i < N ? p[n0 + i] : 0.0f;
+  }
 }
-template <int NS>
-__device__ __forceinline__ void store_state(float *p, int N, int n0, bool ok, bool vec, const float (&h)[NS]) {
-  if constexpr (NS % 4 == 0) {
-    if (vec) {
+template <int NS, bool VEC>
+__device__ __forceinline__ void store_state(float *p, int N, int n0, bool ok, const float (&h)[NS]) {
+  if constexpr (VEC && NS % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < NS; i += 4)
-        if (ok && n0 + i < N) *(float4 *)(p + n0 + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-      return;
-    }
+    for (int i = 0; i < NS; i += 4)
+      if (ok && n0 + i < N) *(float4 *)(p + n0 + i) = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (ok && n0 + i < N) p[n0 + i] = h[i];
   }
-#pragma unroll
-  for (int i = 0; i < NS; ++i)
-    if (ok && n0 + i < N) p[n0 + i] = h[i];
 }
 
-// Four neighbouring elements as they come from memory.
-template <typename T>
+// Four neighbouring elements as they come from memory.  VEC: all four are there, p is
+// aligned to them; otherwise n of them are, and the others read as 0.
+template <typename T, bool VEC>
 struct Quad;
-template <>
-struct Quad<uint16_t> {
+template <bool VEC>
+struct Quad<uint16_t, VEC> {
   uint2 v;
-  // n of them are there (the others read as 0); vec: all four or none, aligned.
-  __device__ __forceinline__ void load(const uint16_t *p, int n, bool vec) {
-    v = make_uint2(0u, 0u);
-    if (vec) {
-      if (n > 0) v = *(const uint2 *)p;
+  __device__ __forceinline__ void load(const uint16_t *p, int n) {
+    if constexpr (VEC) {
+      v = *(const uint2 *)p;
     } else {
+      v = make_uint2(0u, 0u);
       if (n > 0) v.x = p[0];
       if (n > 1) v.x |= (uint32_t)p[1] << 16;
       if (n > 2) v.y = p[2];
@@ -174,14 +174,14 @@ struct Quad<uint16_t> {
     r[3] = __uint_as_float(v.y & 0xffff0000u);
   }
 };
-template <>
-struct Quad<float> {
+template <bool VEC>
+struct Quad<float, VEC> {
   float4 v;
-  __device__ __forceinline__ void load(const float *p, int n, bool vec) {
-    v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (vec) {
-      if (n > 0) v = *(const float4 *)p;
+  __device__ __forceinline__ void load(const float *p, int n) {
+    if constexpr (VEC) {
+      v = *(const float4 *)p;
     } else {
+      v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (n > 0) v.x = p[0];
       if (n > 1) v.y = p[1];
       if (n > 2) v.z = p[2];
@@ -195,14 +195,6 @@ struct Quad<float> {
     r[3] = v.w;
   }
 };
-
-__device__ __forceinline__ void put_quad(void *base, long long off, int n, const float (&r)[4], bool bf16, bool vec) {
-  if (vec) {
-    if (n > 0) store4<true>(base, off, n, r, bf16);
-  } else {
-    store4<false>(base, off, n, r, bf16);
-  }
-}
 
 // The CJ neighbouring values of a lane in a row of LDS.
 template <int CJ>
@@ -247,49 +239,71 @@ __device__ __forceinline__ void get_states(const float *p, float (&r)[NS]) {
   }
 }
 
-// A lane's share of a tile of B or C: quads of states, NS of them per token.
-template <typename T, int NS>
+// A lane's share of a tile of B or C: quads of states, NS of them per token.  Wide loads
+// are not predicated: tokens and states outside read the nearest ones inside, and put()
+// zeroes them.
+template <typename T, int NS, bool VEC>
 struct StatesIn {
   static constexpr int NQ = (TT * NS + 63) / 64;
-  Quad<T> q[NQ];
+  Quad<T, VEC> q[NQ];
   __device__ __forceinline__ void load(const void *src, long long ld, const ScanArgs &a, const Where &w, int t0, int lane) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int id = i * 64 + lane, tt = id / NS, n = id % NS * 4;
-      const bool there = id < TT * NS && t0 + tt < w.t_hi && t0 + tt >= w.t_lo;
-      q[i].load((const T *)src + ((long long)w.b * a.L + t0 + tt) * ld + (long long)w.g * a.N + n,
-                there ? min(a.N - n, 4) : 0, a.vec_bc);
+      const int id = i * 64 + lane, t = t0 + id / NS, n = id % NS * 4;
+      const T *p = (const T *)src + (long long)w.b * a.L * ld + (long long)w.g * a.N;
+      if constexpr (VEC)
+        q[i].load(p + (long long)min(max(t, w.t_lo), w.t_hi - 1) * ld + min(n, a.N - 4), 4);
+      else
+        q[i].load(p + (long long)t * ld + n, id < TT * NS && t >= w.t_lo && t < w.t_hi ? a.N - n : 0);
     }
   }
-  __device__ __forceinline__ void put(float *dst, int lane) const {  // [TT][4 NS]
+  __device__ __forceinline__ void put(float *dst, const ScanArgs &a, const Where &w, int t0, int lane) const {  // [TT][4 NS]
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int id = i * 64 + lane;
+      const bool there = t0 + id / NS < w.t_hi && id % NS * 4 < a.N;
       float r[4];
       q[i].get(r);
-      if (TT * NS % 64 == 0 || id < TT * NS) *(float4 *)(dst + id * 4) = make_float4(r[0], r[1], r[2], r[3]);
+      if (TT * NS % 64 == 0 || id < TT * NS)
+        *(float4 *)(dst + id * 4) = make_float4(there ? r[0] : 0.0f, there ? r[1] : 0.0f, there ? r[2] : 0.0f,
+                                                there ? r[3] : 0.0f);
     }
   }
 };
 
-// A lane's share of a tile of channels: CJ quads, of tokens tt(i) and channels cq .. cq + 3.
-template <typename T, int CJ>
+// A lane's share of a tile of channels: CJ quads, of tokens TT / CJ apart and channels
+// d .. d + 3 (of which nc are the lane's own: none, if the group ends before them; the wide
+// load then reads the group's last four).  Its users zero what is outside.
+template <typename T, int CJ, bool VEC>
 struct ChannelsIn {
-  Quad<T> q[CJ];
+  Quad<T, VEC> q[CJ];
   __device__ __forceinline__ void load(const void *src, long long ld, const ScanArgs &a, const Where &w, int t0, int tt,
                                        long long d, int nc) {
+    const T *p = (const T *)src + (long long)w.b * a.L * ld + d;
 #pragma unroll
     for (int i = 0; i < CJ; ++i) {
       const int t = t0 + i * (TT / CJ) + tt;
-      q[i].load((const T *)src + ((long long)w.b * a.L + t) * ld + d, t >= w.t_lo && t < w.t_hi ? nc : 0, a.vec);
+      if constexpr (VEC)
+        q[i].load(p + (long long)min(max(t, w.t_lo), w.t_hi - 1) * ld, 4);
+      else
+        q[i].load(p + (long long)t * ld, t >= w.t_lo && t < w.t_hi ? nc : 0);
     }
   }
 };
 
-// The n values that a lane's four channels have, the others 0.
+// The n values that a lane's four channels have, the others 0 (or anything, where n is 0).
+template <bool VEC>
 __device__ __forceinline__ void load_channels(const float *p, int n, float (&r)[4]) {
+  if constexpr (VEC) {
+    const float4 v = *(const float4 *)p;
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
+  } else {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) r[c] = c < n ? p[c] : 0.0f;
+    for (int c = 0; c < 4; ++c) r[c] = c < n ? p[c] : 0.0f;
+  }
 }
 
 enum { OUTPUT, STATES, CHECKPOINTS };
@@ -301,13 +315,13 @@ enum { OUTPUT, STATES, CHECKPOINTS };
 //   CHECKPOINTS (backward): as STATES, also the state and the sum of dt before every
 //     sub-tile, and the gradient that the segment's own outputs send to the state in
 //     front of it, sum_t exp(A sum dt) C_t dy_t.
-template <typename T, int NS, int CJ, int MODE>
+template <typename T, int NS, int CJ, int MODE, bool VEC>
 __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
   constexpr int NP = 4 * NS, CW = 16 * CJ, SUB = bwd_sub(NS);
   __shared__ __align__(16) float dts[TT][CW], dus[TT][CW];  // dt, dt u; OUTPUT: y replaces dt u
   __shared__ __align__(16) float dys[MODE == CHECKPOINTS ? TT : 1][CW];
   __shared__ __align__(16) float Bs[TT][NP], Cs[MODE == STATES ? 1 : TT][NP];
-  const Where w = where(a);
+  const Where w = where<false>(a);
   const bool last = w.s == a.nseg - 1;
   const int lane = threadIdx.x, row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
   const int rel = w.tile * CW + c0;
@@ -316,9 +330,9 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
   // the lane's part of the staging
   const int tt = lane / (4 * CJ), cq = lane % (4 * CJ) * 4, relq = w.tile * CW + cq;
   const int nc = min(max(a.Dg - relq, 0), 4);
-  const long long dq = (long long)w.g * a.Dg + relq;
-  ChannelsIn<T, CJ> un, xn, zn, gn;
-  StatesIn<T, NS> bn, cn;
+  const long long dq = (long long)w.g * a.Dg + (VEC ? min(relq, a.Dg - 4) : relq);
+  ChannelsIn<T, CJ, VEC> un, xn, zn, gn;
+  StatesIn<T, NS, VEC> bn, cn;
   auto fetch = [&](int t0) {
     un.load(a.u, a.u_ld, a, w, t0, tt, dq, nc);
     xn.load(a.delta, a.delta_ld, a, w, t0, tt, dq, nc);
@@ -329,11 +343,11 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
     }
     if constexpr (MODE == CHECKPOINTS) gn.load(a.d_o, a.D, a, w, t0, tt, dq, nc);
   };
-  fetch(w.t_lo);
+  if (w.t_lo < w.t_hi) fetch(w.t_lo);
   float A2[CJ][NS], h[CJ][NS], gs[CJ][NS], pr[CJ][NS], sum[CJ];
 #pragma unroll
   for (int j = 0; j < CJ; ++j) {
-    load_state(a.A + (d + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, A2[j]);
+    load_state<NS, VEC>(a.A + (d + j) * a.N, a.N, n0, rel + j < a.Dg, A2[j]);
     sum[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -344,28 +358,29 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
     }
     if constexpr (MODE == OUTPUT) {
       if (a.nseg > 1)
-        load_state(a.seg + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+        load_state<NS, VEC>(a.seg + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, h[j]);
       else if (a.h0)
-        load_state(a.h0 + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+        load_state<NS, VEC>(a.h0 + (sd + j) * a.N, a.N, n0, rel + j < a.Dg, h[j]);
     }
   }
   float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (a.bias) load_channels(a.bias + dq, nc, bias);
-  if (MODE == OUTPUT && a.Dskip) load_channels(a.Dskip + dq, nc, Dsk);
+  if (a.bias) load_channels<VEC>(a.bias + dq, nc, bias);
+  if (MODE == OUTPUT && a.Dskip) load_channels<VEC>(a.Dskip + dq, nc, Dsk);
   for (int t0 = w.t_lo; t0 < w.t_hi; t0 += TT) {
-    ChannelsIn<T, CJ> uc, zc;
+    ChannelsIn<T, CJ, VEC> uc, zc;
 #pragma unroll
     for (int i = 0; i < CJ; ++i) {
       const int k = i * (TT / CJ) + tt;
-      const bool live = t0 + k < w.t_hi;
+      const bool live = t0 + k < w.t_hi && nc > 0;
       float u[4], x[4], z[4], g[4], dt[4], dtu[4];
       un.q[i].get(u);
       xn.q[i].get(x);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float v = x[c] + bias[c];
-        dt[c] = !live || c >= nc ? 0.0f : a.softplus ? softplus(v) : v;
-        dtu[c] = dt[c] * u[c];
+        const bool there = VEC ? live : live && c < nc;
+        dt[c] = there ? a.softplus ? softplus(v) : v : 0.0f;
+        dtu[c] = there ? dt[c] * u[c] : 0.0f;
       }
       *(float4 *)&dts[k][cq] = make_float4(dt[0], dt[1], dt[2], dt[3]);
       *(float4 *)&dus[k][cq] = make_float4(dtu[0], dtu[1], dtu[2], dtu[3]);
@@ -376,13 +391,15 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) g[c] *= z[c] * sigmoid(z[c]);
         }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) g[c] = (VEC ? live : live && c < nc) ? g[c] : 0.0f;
         *(float4 *)&dys[k][cq] = make_float4(g[0], g[1], g[2], g[3]);
       }
       uc.q[i] = un.q[i];
       if (MODE == OUTPUT && a.z) zc.q[i] = zn.q[i];
     }
-    bn.put(&Bs[0][0], lane);
-    if constexpr (MODE != STATES) cn.put(&Cs[0][0], lane);
+    bn.put(&Bs[0][0], a, w, t0, lane);
+    if constexpr (MODE != STATES) cn.put(&Cs[0][0], a, w, t0, lane);
     fetch(t0 + TT);
     wave_sync();
     const int nt = min(TT, w.t_hi - t0);
@@ -392,7 +409,7 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
           const long long k = ((long long)w.b * a.nseg + w.s) * a.subs + (t0 - w.t_lo + t4) / SUB;
 #pragma unroll
           for (int j = 0; j < CJ; ++j) {
-            store_state(a.ck + (k * a.D + d + j) * a.N, a.N, n0, rel + j < a.Dg, a.vec_n, h[j]);
+            store_state<NS, VEC>(a.ck + (k * a.D + d + j) * a.N, a.N, n0, rel + j < a.Dg, h[j]);
             if (rel + j < a.Dg && row == 0) a.ckdt[k * a.D + d + j] = sum[j];
           }
         }
@@ -447,8 +464,8 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) o[c] *= z[c] * sigmoid(z[c]);
         }
-        if (t0 + k < w.t_hi)
-          put_quad(a.out, ((long long)w.b * a.L + t0 + k) * a.D + dq, nc, o, a.out_bf16, a.vec);
+        if (t0 + k < w.t_hi && nc > 0)
+          store4<VEC>(a.out, ((long long)w.b * a.L + t0 + k) * a.D + dq, nc, o, a.out_bf16);
       }
       wave_sync();
     }
@@ -457,11 +474,11 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
   for (int j = 0; j < CJ; ++j) {
     const bool ok = rel + j < a.Dg;
     if constexpr (MODE == OUTPUT) {
-      if (last && a.hT) store_state(a.hT + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
+      if (last && a.hT) store_state<NS, VEC>(a.hT + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, h[j]);
     } else {
-      store_state(a.seg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
+      store_state<NS, VEC>(a.seg + (sd + j) * a.N, a.N, n0, ok, h[j]);
       if (ok && row == 0) a.sdt[sd + j] = sum[j];
-      if constexpr (MODE == CHECKPOINTS) store_state(a.gseg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, gs[j]);
+      if constexpr (MODE == CHECKPOINTS) store_state<NS, VEC>(a.gseg + (sd + j) * a.N, a.N, n0, ok, gs[j]);
     }
   }
 }
@@ -559,12 +576,13 @@ __device__ __forceinline__ void channel_sums(const float (&pB)[NS], const float 
   }
 }
 
-// The backward's main pass over a segment, tiles and sub-tiles from the last to the
-// first: each sub-tile's states are computed again from its checkpoint and kept in
-// registers with their decays; then the gradient of the state runs against time.  The
+// The backward's main pass over a span of segments, tiles and sub-tiles from the last to
+// the first: each sub-tile's states are computed again from its checkpoint and kept in
+// registers; then the gradient of the state runs against time, computing the decays once
+// more (keeping them too took the registers that hold the next checkpoint's loads).  The
 // waves of a workgroup work on neighbouring channels and meet once per tile, to add up
 // their sums for dB and dC.
-template <typename T, int NS>
+template <typename T, int NS, bool VEC>
 __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_kernel(ScanArgs a) {
   constexpr int NP = 4 * NS, CJ = bwd_cj(NS), CW = 16 * CJ, SUB = bwd_sub(NS);
   struct WaveLds {
@@ -576,18 +594,18 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
   };
   __shared__ __align__(16) WaveLds lds[BWD_WAVES];
   __shared__ float part[2][BWD_WAVES][TT][2][NP];  // each wave's sums over its channels
-  const Where w = where(a);
+  const Where w = where<true>(a);
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
   const int base = (w.tile * waves + wave) * CW, rel = base + c0;
   const long long d = (long long)w.g * a.Dg + rel;
-  const long long bs = (long long)w.b * a.nseg + w.s, sd = bs * a.D + d;
+  const long long bs = (long long)w.b * a.nspan + w.s;
   WaveLds &s = lds[wave];
   const int tt = lane / (4 * CJ), cq = lane % (4 * CJ) * 4, relq = base + cq;
   const int nc = min(max(a.Dg - relq, 0), 4);
-  const long long dq = (long long)w.g * a.Dg + relq;
-  ChannelsIn<T, CJ> un, xn, zn, gn;
-  StatesIn<T, NS> bn, cn;
+  const long long dq = (long long)w.g * a.Dg + (VEC ? min(relq, a.Dg - 4) : relq);
+  ChannelsIn<T, CJ, VEC> un, xn, zn, gn;
+  StatesIn<T, NS, VEC> bn, cn;
   auto fetch = [&](int t0) {
     un.load(a.u, a.u_ld, a, w, t0, tt, dq, nc);
     xn.load(a.delta, a.delta_ld, a, w, t0, tt, dq, nc);
@@ -597,68 +615,85 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
     cn.load(a.Cm, a.c_ld, a, w, t0, lane);
   };
   const int ntile = (w.t_hi - w.t_lo + TT - 1) / TT;
-  fetch(w.t_lo + (ntile - 1) * TT);
+  if (ntile > 0) fetch(w.t_lo + (ntile - 1) * TT);
   float A2[CJ][NS], carry[CJ][NS], dA[CJ][NS];
 #pragma unroll
   for (int j = 0; j < CJ; ++j) {
     const bool ok = rel + j < a.Dg;
-    load_state(a.A + (d + j) * a.N, a.N, n0, ok, a.vec_n, A2[j]);
-    load_state(a.gseg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, carry[j]);
+    load_state<NS, VEC>(a.A + (d + j) * a.N, a.N, n0, ok, A2[j]);
+    const int end = min((w.s + 1) * a.span, a.nseg) - 1;  // the span's last segment
+    load_state<NS, VEC>(a.gseg + (((long long)w.b * a.nseg + end) * a.D + d + j) * a.N, a.N, n0, ok, carry[j]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       A2[j][i] *= kLog2e;
       dA[j][i] = 0.0f;
     }
   }
+  float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   float sD[4] = {0.0f, 0.0f, 0.0f, 0.0f}, sb[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.bias) load_channels<VEC>(a.bias + dq, nc, bias);
+  if (a.Dskip) load_channels<VEC>(a.Dskip + dq, nc, Dsk);
+  // the state in front of a sub-tile: its checkpoint, and what the segment's entering
+  // state has become; loaded one sub-tile ahead
+  float hck[CJ][NS], hin[CJ][NS], before[CJ];
+  const int last = w.t_hi - w.t_lo - 1;  // of the span's tokens
+  int ck_seg = max(last, 0) / a.seg_len, ck_sub = max(last, 0) % a.seg_len / SUB;
+  auto checkpoint = [&]() {  // the next one towards the span's start, and then the one before it
+    const long long seg = (long long)w.b * a.nseg + w.s * a.span + ck_seg, k = seg * a.subs + ck_sub;
+#pragma unroll
+    for (int j = 0; j < CJ; ++j) {
+      const bool ok = rel + j < a.Dg && ck_seg >= 0;
+      load_state<NS, VEC>(a.ck + (k * a.D + d + j) * a.N, a.N, n0, ok, hck[j]);
+      load_state<NS, VEC>(a.seg + (seg * a.D + d + j) * a.N, a.N, n0, ok, hin[j]);
+      before[j] = ok ? a.ckdt[k * a.D + d + j] : 0.0f;
+    }
+    if (--ck_sub < 0) {
+      --ck_seg;
+      ck_sub = a.subs - 1;
+    }
+  };
+  if (ntile > 0) checkpoint();
   for (int tile = ntile - 1; tile >= 0; --tile) {
     const int t0 = w.t_lo + tile * TT;
-    float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f}, Dsk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (a.bias) load_channels(a.bias + dq, nc, bias);
 #pragma unroll
     for (int i = 0; i < CJ; ++i) {
       const int k = i * (TT / CJ) + tt;
-      const bool live = t0 + k < w.t_hi;
-      float u[4], x[4], z[4], g[4], dt[4];
+      const bool live = t0 + k < w.t_hi && nc > 0;
+      float u[4], x[4], z[4], g[4], dt[4], dtu[4];
       un.q[i].get(u);
       xn.q[i].get(x);
       gn.q[i].get(g);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float v = x[c] + bias[c];
-        dt[c] = !live || c >= nc ? 0.0f : a.softplus ? softplus(v) : v;
+        const bool there = VEC ? live : live && c < nc;
+        dt[c] = there ? a.softplus ? softplus(v) : v : 0.0f;
+        dtu[c] = there ? dt[c] * u[c] : 0.0f;
       }
       if (a.z) {
         zn.q[i].get(z);
 #pragma unroll
         for (int c = 0; c < 4; ++c) g[c] *= z[c] * sigmoid(z[c]);
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) g[c] = (VEC ? live : live && c < nc) ? g[c] : 0.0f;
       *(float4 *)&s.dt[k][cq] = make_float4(dt[0], dt[1], dt[2], dt[3]);
-      *(float4 *)&s.du[k][cq] = make_float4(dt[0] * u[0], dt[1] * u[1], dt[2] * u[2], dt[3] * u[3]);
+      *(float4 *)&s.du[k][cq] = make_float4(dtu[0], dtu[1], dtu[2], dtu[3]);
       *(float4 *)&s.dy[k][cq] = make_float4(g[0], g[1], g[2], g[3]);
     }
-    bn.put(&s.B[0][0], lane);
-    cn.put(&s.C[0][0], lane);
+    bn.put(&s.B[0][0], a, w, t0, lane);
+    cn.put(&s.C[0][0], a, w, t0, lane);
     wave_sync();
     const int nt = min(TT, w.t_hi - t0);
     float(*ps)[2][NP] = part[tile & 1][wave];
     for (int t1 = (nt - 1) / SUB * SUB; t1 >= 0; t1 -= SUB) {
-      float h[CJ][NS], hh[SUB][CJ][NS], aa[SUB][CJ][NS], y[CJ][4];
-      const long long k = bs * a.subs + (tile * TT + t1) / SUB;
-      float hstart[CJ][NS];
+      float h[CJ][NS], hstart[CJ][NS], hh[SUB][CJ][NS], y[CJ][4];
 #pragma unroll
-      for (int j = 0; j < CJ; ++j) {
-        const bool ok = rel + j < a.Dg;
-        float hin[NS];
-        load_state(a.ck + (k * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, h[j]);
-        load_state(a.seg + (sd + j) * a.N, a.N, n0, ok, a.vec_n, hin);
-        const float before = ok ? a.ckdt[k * a.D + d + j] : 0.0f;
+      for (int j = 0; j < CJ; ++j)
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          h[j][i] += __builtin_amdgcn_exp2f(A2[j][i] * before) * hin[i];
-          hstart[j][i] = h[j][i];
-        }
-      }
+        for (int i = 0; i < NS; ++i)
+          h[j][i] = hstart[j][i] = hck[j][i] + __builtin_amdgcn_exp2f(A2[j][i] * before[j]) * hin[j][i];
+      checkpoint();
 #pragma unroll
       for (int t = 0; t < SUB; ++t) {
         float dt[CJ], dtu[CJ], Bv[NS], Cv[NS];
@@ -671,8 +706,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
           float acc = 0.0f;
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            aa[t][j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
-            h[j][i] = aa[t][j][i] * h[j][i] + dtu[j] * Bv[i];
+            h[j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]) * h[j][i] + dtu[j] * Bv[i];
             hh[t][j][i] = h[j][i];
             acc += h[j][i] * Cv[i];
           }
@@ -703,7 +737,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
               const float g = Cv[i] * dy[j] + carry[j][i];
-              carry[j][i] = aa[t][j][i] * g;
+              carry[j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]) * g;
               const float wv = carry[j][i] * (t > 0 ? hh[t > 0 ? t - 1 : 0][j][i] : hstart[j][i]);
               sA[j][q] += A2[j][i] * wv;  // times log2 e; taken out below
               dA[j][i] += dt[j] * wv;
@@ -727,10 +761,8 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
     }
     wave_sync();
     // the inputs stayed in registers; the next tile's take their place as they are used
-    const ChannelsIn<T, CJ> uc = un, xc = xn, zc = zn, gc = gn;
+    const ChannelsIn<T, CJ, VEC> uc = un, xc = xn, zc = zn, gc = gn;
     fetch(t0 - TT);
-    if (a.bias) load_channels(a.bias + dq, nc, bias);
-    if (a.Dskip) load_channels(a.Dskip + dq, nc, Dsk);
 #pragma unroll
     for (int i = 0; i < CJ; ++i) {
       const int k = i * (TT / CJ) + tt;
@@ -758,17 +790,18 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
         sD[c] += live ? dy * u[c] : 0.0f;
         sb[c] += live ? dd[c] : 0.0f;
       }
-      if (t0 + k < w.t_hi) {
+      if (t0 + k < w.t_hi && nc > 0) {
         const long long o = ((long long)w.b * a.L + t0 + k) * a.D + dq;
-        put_quad(a.du, o, nc, du, a.out_bf16, a.vec);
-        put_quad(a.ddelta, o, nc, dd, a.out_bf16, a.vec);
-        if (a.z) put_quad(a.dz, o, nc, dz, a.out_bf16, a.vec);
+        store4<VEC>(a.du, o, nc, du, a.out_bf16);
+        store4<VEC>(a.ddelta, o, nc, dd, a.out_bf16);
+        if (a.z) store4<VEC>(a.dz, o, nc, dz, a.out_bf16);
       }
     }
     __syncthreads();
     // the other half of part is written before the next barrier, this one behind it
-    for (int e = threadIdx.x; e < nt * 2 * a.N; e += blockDim.x) {
-      const int t = e / (2 * a.N), k = e / a.N % 2, n = e % a.N;
+    for (int e = threadIdx.x; e < nt * 2 * NP; e += blockDim.x) {
+      const int t = e / (2 * NP), k = e / NP % 2, n = e % NP;
+      if (n >= a.N) continue;
       float x = part[tile & 1][0][t][k][n];
       for (int v = 1; v < waves; ++v) x += part[tile & 1][v][t][k][n];
       a.bcpart[((((long long)w.tile * a.B + w.b) * a.L + t0 + t) * a.G + w.g) * 2 * a.N + k * a.N + n] = x;
@@ -777,8 +810,8 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
 #pragma unroll
   for (int j = 0; j < CJ; ++j) {
     const bool ok = rel + j < a.Dg;
-    store_state(a.dApart + (sd + j) * a.N, a.N, n0, ok, a.vec_n, dA[j]);
-    if (w.s == 0 && a.dh0) store_state(a.dh0 + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, a.vec_n, carry[j]);
+    store_state<NS, VEC>(a.dApart + (bs * a.D + d + j) * a.N, a.N, n0, ok, dA[j]);
+    if (w.s == 0 && a.dh0) store_state<NS, VEC>(a.dh0 + ((long long)w.b * a.D + d + j) * a.N, a.N, n0, ok, carry[j]);
   }
   // dD and the bias's gradient: the lanes that staged a channel's tokens
   wave_sync();
@@ -837,7 +870,7 @@ constexpr int STEP_CH = 64;  // channels of a workgroup's four waves
 // One token: a wave's lanes as in the passes above with one channel each; bound by reading
 // and writing the states once.
 // SQ sequences share their channels' A and have their loads in flight together.
-template <typename T, int NS, int SQ>
+template <typename T, int NS, int SQ, bool VEC>
 __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, row = lane >> 4, ch = (tid >> 6) * 16 + (lane & 15);
   int id = blockIdx.x;
@@ -850,22 +883,24 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
   const long long d = (long long)g * a.Dg + rel;
   constexpr int bf = sizeof(T) == 2;
   float A[NS], h[SQ][NS], u[SQ], x[SQ], z[SQ], y[SQ];
-  Quad<T> Bq[SQ][(NS + 3) / 4], Cq[SQ][(NS + 3) / 4];
+  constexpr bool VQ = VEC && NS % 4 == 0;  // a lane's states come in whole quads
+  Quad<T, VQ> Bq[SQ][(NS + 3) / 4], Cq[SQ][(NS + 3) / 4];
 #pragma unroll
   for (int q = 0; q < SQ; ++q) {
     const long long b = min(b0 + q, a.B - 1);
-    load_state(a.hT + (b * a.D + d) * a.N, a.N, n0, ok, a.vec_n, h[q]);
+    load_state<NS, VEC>(a.hT + (b * a.D + d) * a.N, a.N, n0, ok, h[q]);
     u[q] = ok ? load_elem(a.u, b * a.u_ld + d, bf) : 0.0f;
     x[q] = ok ? load_elem(a.delta, b * a.delta_ld + d, bf) : 0.0f;
     z[q] = ok && a.z ? load_elem(a.z, b * a.z_ld + d, bf) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NS; i += 4) {
-      const int n = min(min(a.N - n0 - i, 4), NS - i);
-      Bq[q][i / 4].load((const T *)a.Bm + b * a.b_ld + (long long)g * a.N + n0 + i, n, NS % 4 == 0 && a.vec_bc);
-      Cq[q][i / 4].load((const T *)a.Cm + b * a.c_ld + (long long)g * a.N + n0 + i, n, NS % 4 == 0 && a.vec_bc);
+      // states behind N (their A, and so their state, is 0 and stays unwritten): any quad inside
+      const int at = VQ ? min(n0 + i, a.N - 4) : n0 + i, n = min(a.N - n0 - i, NS - i);
+      Bq[q][i / 4].load((const T *)a.Bm + b * a.b_ld + (long long)g * a.N + at, n);
+      Cq[q][i / 4].load((const T *)a.Cm + b * a.c_ld + (long long)g * a.N + at, n);
     }
   }
-  load_state(a.A + d * a.N, a.N, n0, ok, a.vec_n, A);
+  load_state<NS, VEC>(a.A + d * a.N, a.N, n0, ok, A);
   const float bias = ok && a.bias ? a.bias[d] : 0.0f, skip = ok && a.Dskip ? a.Dskip[d] : 0.0f;
 #pragma unroll
   for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
@@ -879,9 +914,9 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
       Bq[q][i / 4].get(Bv);
       Cq[q][i / 4].get(Cv);
       h[q][i] = __builtin_amdgcn_exp2f(dt * A[i]) * h[q][i] + dtu * Bv[i % 4];
-      y[q] += h[q][i] * Cv[i % 4];
+      y[q] += !VQ || n0 + i < a.N ? h[q][i] * Cv[i % 4] : 0.0f;
     }
-    if (b0 + q < a.B) store_state(a.hT + ((long long)(b0 + q) * a.D + d) * a.N, a.N, n0, ok, a.vec_n, h[q]);
+    if (b0 + q < a.B) store_state<NS, VEC>(a.hT + ((long long)(b0 + q) * a.D + d) * a.N, a.N, n0, ok, h[q]);
   }
 #pragma unroll
   for (int q = 0; q < SQ; ++q) {
@@ -897,7 +932,7 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
 int state_regs(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 struct ScanPlan {
-  int cj, seg_len, nseg, subs;
+  int cj, seg_len, nseg, subs, span, nspan;
   int bwd_waves, bwd_tiles;
   size_t seg, sdt, gseg, ck, ckdt, bcpart, dApart, dDpart, dbpart, total;
 };
@@ -914,12 +949,13 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   const long long most = rec_cdiv(L, 4 * TT);  // segments of at least four tiles
   long long nseg = 1;
   if (bwd) {
-    // the main pass has workgroups of up to four waves of bwd_cj * 16 channels, two per SIMD at most
+    // The checkpoints' pass wants three waves per SIMD; the main pass, at two, few long
+    // spans: each starts with loads that nothing hides.
     const int cw = 16 * bwd_cj(NS);
     p.bwd_waves = (int)std::min<long long>(BWD_WAVES, rec_cdiv(Dg, cw));
     p.bwd_tiles = (int)rec_cdiv(Dg, (long long)cw * p.bwd_waves);
-    nseg = std::min(rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves), rec_cdiv(L, 2 * TT));
-    p.cj = ww * nseg >= 1024 ? wide : 1;
+    p.cj = ww * rec_cdiv(L, 2 * TT) >= 1024 ? wide : 1;
+    nseg = std::min(rec_cdiv(4096, p.cj == 1 ? w16 : ww), rec_cdiv(L, 2 * TT));
   } else {
     p.bwd_waves = p.bwd_tiles = 0;
     p.cj = ww >= 1024 ? wide : 1;
@@ -931,6 +967,12 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   p.seg_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
   p.nseg = (int)rec_cdiv(L, p.seg_len);
   p.subs = p.seg_len / SUB;
+  p.span = p.nspan = 1;
+  if (bwd) {
+    const long long spans = std::min<long long>(p.nseg, rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves));
+    p.span = (int)rec_cdiv(p.nseg, spans);
+    p.nspan = (int)rec_cdiv(p.nseg, p.span);
+  }
   size_t off = 0;
   auto take = [&off](size_t floats) {
     const size_t at = off;
@@ -948,9 +990,9 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.ck = take(bs * p.subs * DN);
     p.ckdt = take(bs * p.subs * D);
     p.bcpart = take((size_t)p.bwd_tiles * B * L * G * 2 * N);
-    p.dApart = take(bs * DN);
-    p.dDpart = take(bs * D);
-    p.dbpart = take(bs * D);
+    p.dApart = take((size_t)B * p.nspan * DN);
+    p.dDpart = take((size_t)B * p.nspan * D);
+    p.dbpart = take((size_t)B * p.nspan * D);
   }
   p.total = off;
   return p;
@@ -986,12 +1028,16 @@ hipError_t launch(K kernel, long long blocks, int threads, hipStream_t st, const
   return hipGetLastError();
 }
 
+// Where rows or states cannot be accessed by fours, one kernel per type and NS will do:
+// the narrow one.
 template <typename T, int NS, int MODE>
 hipError_t launch_pass(ScanArgs a, int cj, hipStream_t st) {
+  if (!a.vec) cj = 1;
   a.tiles = (int)rec_cdiv(a.Dg, 16 * cj);
   const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
-  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE>, blocks, 64, st, a)
-                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE>, blocks, 64, st, a);
+  if (!a.vec) return launch(scan_pass_kernel<T, NS, 1, MODE, false>, blocks, 64, st, a);
+  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE, true>, blocks, 64, st, a)
+                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE, true>, blocks, 64, st, a);
 }
 template <typename T, int MODE>
 hipError_t launch_pass(const ScanArgs &a, int cj, hipStream_t st) {
@@ -1008,37 +1054,42 @@ hipError_t launch_pass(const ScanArgs &a, bool bf, int cj, hipStream_t st) {
   return bf ? launch_pass<uint16_t, MODE>(a, cj, st) : launch_pass<float, MODE>(a, cj, st);
 }
 
-template <typename T>
+template <typename T, bool VEC>
 hipError_t launch_bwd(ScanArgs a, const ScanPlan &p, hipStream_t st) {
   a.tiles = p.bwd_tiles;
-  const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
+  const long long blocks = (long long)a.B * a.nspan * a.G * a.tiles;
   const int threads = 64 * p.bwd_waves;
   switch (state_regs(a.N)) {
-    case 1: return launch(scan_bwd_kernel<T, 1>, blocks, threads, st, a);
-    case 2: return launch(scan_bwd_kernel<T, 2>, blocks, threads, st, a);
-    case 4: return launch(scan_bwd_kernel<T, 4>, blocks, threads, st, a);
-    case 8: return launch(scan_bwd_kernel<T, 8>, blocks, threads, st, a);
-    default: return launch(scan_bwd_kernel<T, 16>, blocks, threads, st, a);
+    case 1: return launch(scan_bwd_kernel<T, 1, VEC>, blocks, threads, st, a);
+    case 2: return launch(scan_bwd_kernel<T, 2, VEC>, blocks, threads, st, a);
+    case 4: return launch(scan_bwd_kernel<T, 4, VEC>, blocks, threads, st, a);
+    case 8: return launch(scan_bwd_kernel<T, 8, VEC>, blocks, threads, st, a);
+    default: return launch(scan_bwd_kernel<T, 16, VEC>, blocks, threads, st, a);
   }
 }
+template <typename T>
+hipError_t launch_bwd(const ScanArgs &a, const ScanPlan &p, hipStream_t st) {
+  return a.vec ? launch_bwd<T, true>(a, p, st) : launch_bwd<T, false>(a, p, st);
+}
 
-template <typename T, int SQ>
+template <typename T, int SQ, bool VEC>
 hipError_t launch_step(ScanArgs a, hipStream_t st) {
   a.tiles = (int)rec_cdiv(a.Dg, STEP_CH);
   const long long blocks = rec_cdiv(a.B, SQ) * a.G * a.tiles;
   switch (state_regs(a.N)) {
-    case 1: return launch(scan_step_kernel<T, 1, SQ>, blocks, NT, st, a);
-    case 2: return launch(scan_step_kernel<T, 2, SQ>, blocks, NT, st, a);
-    case 4: return launch(scan_step_kernel<T, 4, SQ>, blocks, NT, st, a);
-    case 8: return launch(scan_step_kernel<T, 8, SQ>, blocks, NT, st, a);
-    default: return launch(scan_step_kernel<T, 16, SQ>, blocks, NT, st, a);
+    case 1: return launch(scan_step_kernel<T, 1, SQ, VEC>, blocks, NT, st, a);
+    case 2: return launch(scan_step_kernel<T, 2, SQ, VEC>, blocks, NT, st, a);
+    case 4: return launch(scan_step_kernel<T, 4, SQ, VEC>, blocks, NT, st, a);
+    case 8: return launch(scan_step_kernel<T, 8, SQ, VEC>, blocks, NT, st, a);
+    default: return launch(scan_step_kernel<T, 16, SQ, VEC>, blocks, NT, st, a);
   }
 }
 // Four sequences a workgroup where that still leaves four workgroups a CU.
 template <typename T>
 hipError_t launch_step(const ScanArgs &a, hipStream_t st) {
   const bool many = (long long)a.B * a.G * rec_cdiv(a.Dg, STEP_CH) >= 4096;
-  return many ? launch_step<T, 4>(a, st) : launch_step<T, 1>(a, st);
+  if (!a.vec) return launch_step<T, 1, false>(a, st);
+  return many ? launch_step<T, 4, true>(a, st) : launch_step<T, 1, true>(a, st);
 }
 
 hipError_t launch_combine(const ScanArgs &a, hipStream_t st) {
@@ -1073,15 +1124,14 @@ ScanArgs scan_args(const void *u, const void *delta, const float *A, const void 
   a.softplus = softplus != 0;
   a.out_bf16 = out_dtype == RET_BF16;
   const size_t e = rec_esize(in_dtype);
-  a.vec = a.Dg % 4 == 0 && wide(u, u_ld, e) && wide(delta, delta_ld, e) && wide(z, z_ld, e);
-  a.vec_bc = N % 4 == 0 && wide(Bm, b_ld, e) && wide(Cm, c_ld, e);
+  a.vec = a.Dg % 4 == 0 && N % 4 == 0 && wide(u, u_ld, e) && wide(delta, delta_ld, e) && wide(z, z_ld, e) &&
+          wide(Bm, b_ld, e) && wide(Cm, c_ld, e) && wide(D_skip, 0, 4) && wide(bias, 0, 4);
   return a;
 }
 
-// States may be accessed by fours: the caller's, A, and the workspace's.
+// Whether states are aligned for access by fours: the caller's, A, and the workspace's.
 bool wide_states(const ScanArgs &a) {
   const void *ps[] = {a.A, a.h0, a.hT, a.dhT, a.dh0, a.seg};
-  if (a.N % 4) return false;
   for (const void *p : ps)
     if (!rec_aligned(p, 16)) return false;
   return true;
@@ -1162,8 +1212,7 @@ ret_status_t selective_scan(const void *u, const void *delta, const float *A, co
   a.seg = (float *)((char *)workspace + p.seg);
   a.sdt = (float *)((char *)workspace + p.sdt);
   const bool bf = in_dtype == RET_BF16;
-  a.vec = a.vec && wide(out, D, oe);
-  a.vec_n = wide_states(a);
+  a.vec = a.vec && wide(out, D, oe) && wide_states(a);
   hipError_t err = hipSuccess;
   if (p.nseg > 1) {
     if ((err = launch_pass<STATES>(a, bf, p.cj, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess)
@@ -1234,6 +1283,8 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   a.seg_len = p.seg_len;
   a.nseg = p.nseg;
   a.subs = p.subs;
+  a.span = p.span;
+  a.nspan = p.nspan;
   a.seg = (float *)(ws + p.seg);
   a.sdt = (float *)(ws + p.sdt);
   a.gseg = (float *)(ws + p.gseg);
@@ -1244,8 +1295,7 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   a.dDpart = (float *)(ws + p.dDpart);
   a.dbpart = (float *)(ws + p.dbpart);
   const bool bf = in_dtype == RET_BF16;
-  a.vec = a.vec && wide(d_o, D, e) && wide(du, D, oe) && wide(ddelta, D, oe) && wide(dz, D, oe);
-  a.vec_n = wide_states(a);
+  a.vec = a.vec && wide(d_o, D, e) && wide(du, D, oe) && wide(ddelta, D, oe) && wide(dz, D, oe) && wide_states(a);
   hipError_t err;
   if ((err = launch_pass<CHECKPOINTS>(a, bf, p.cj, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess ||
       (err = bf ? launch_bwd<uint16_t>(a, p, st) : launch_bwd<float>(a, p, st)) != hipSuccess)
@@ -1254,7 +1304,7 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   a.tiles = p.bwd_tiles;
   hipLaunchKernelGGL(scan_reduce_bc_kernel, dim3((unsigned)rec_cdiv(rows * 2 * bc, NT)), dim3(NT), 0, st, a, dB, dC);
   if ((err = hipGetLastError()) != hipSuccess) return rec_status(err);
-  const int parts = B * p.nseg;
+  const long long parts = (long long)B * p.nspan;
   if ((err = column_sum(a.dApart, dA, nullptr, parts, (long long)D * N, 0, st)) != hipSuccess) return rec_status(err);
   if (dD && (err = column_sum(a.dDpart, dD, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
   if (ddelta_bias && (err = column_sum(a.dbpart, ddelta_bias, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
@@ -1283,7 +1333,7 @@ ret_status_t selective_scan_step(const void *u, const void *delta, const float *
                          {"D_skip", D_skip, (size_t)D * 4}, {"delta_bias", delta_bias, (size_t)D * 4}};
   const RecSpan outs[] = {{"out", out, (size_t)B * D * oe}, {"state", state, (size_t)B * D * N * 4}};
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
-  a.vec_n = wide_states(a);
+  a.vec = a.vec && wide_states(a);
   hipStream_t st = (hipStream_t)hip_stream;
   return rec_status(in_dtype == RET_BF16 ? launch_step<uint16_t>(a, st) : launch_step<float>(a, st));
 }
