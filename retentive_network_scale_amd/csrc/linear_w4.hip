@@ -7,13 +7,15 @@
 // on the same accumulator takes the offset out again.  A group's sum is thus one of
 // exact bf16 products in fp32, and its scale is applied in fp32.
 //
-// A workgroup covers 16 rows of W and up to 64 tokens; its waves share out the blocks
-// of K (128 of them for groups of 128, 64 and 32 below) and meet in LDS.  Inside a
-// block, lane (n = lane & 15, kq = lane >> 4) reads WORDS consecutive words of its row,
-// eight weights each; a product step takes one word of every lane, so that the four kq
-// cover WORDS * 8 apart ranges of K.  x is read by the same map.  Which k sits in which
-// slot of a step does not matter, as long as both operands agree: the packed order
-// (0 4 1 5 2 6 3 7) of a word's nibbles is matched by permuting x.
+// A workgroup covers 16 rows of W and MT tiles of 16 tokens, its waves share out K and
+// meet in LDS.  Both operands go through LDS, a chunk of K at a time, requested while the
+// chunk before is worked on and read from memory along the rows: lanes that fetched their
+// matrix operands themselves, from 16 rows each, took 64 address cycles a load and met in
+// few L2 channels (rows lie a power of two apart): 20 us for 64 tokens, N = 2048, K = 4096.
+//
+// Which k sits in which slot of a matrix step does not matter, as long as both operands
+// agree: lane (n = lane & 15, kq = lane >> 4) takes WORDS consecutive words of its row,
+// eight weights each, and a step takes one word of every lane.
 #include <algorithm>
 
 #include "launch.hpp"
@@ -36,7 +38,7 @@ struct W4Args {
   int M, N, K, group, out_bf16;
 };
 
-// Eight elements of x, as loaded and in the order 0 4 1 5 2 6 3 7.
+// Eight elements of x, and in the order 0 4 1 5 2 6 3 7, that of a word's nibbles below.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load_x(const uint16_t *p) {
   if constexpr (VEC) return *(const u32x4 *)p;
@@ -45,13 +47,13 @@ __device__ __forceinline__ u32x4 load_x(const uint16_t *p) {
   for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
   return v;
 }
-__device__ __forceinline__ bf16x8 permuted(u32x4 v) {
+__device__ __forceinline__ u32x4 permuted(u32x4 v) {
   u32x4 r;
   r[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
   r[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
   r[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);
   r[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302);
-  return __builtin_bit_cast(bf16x8, r);
+  return r;
 }
 
 // Eight weights of a word as 16 + q, same order.
@@ -64,103 +66,128 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// MT tiles of 16 tokens; WORDS words of a row per lane and block; WAVES waves.
-template <int MT, int WORDS, int WAVES, bool VEC>
-__global__ __launch_bounds__(WAVES * 64) void w4_kernel(W4Args a) {
-  __shared__ f32x4 red[WAVES][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, kq = lane >> 4;
-  const int n = blockIdx.x * 16 + col, nr = min(n, a.N - 1), m0 = blockIdx.y * MT * 16;
-  constexpr int KB = WORDS * 32;  // k per block
-  constexpr int U = 16 / (WORDS * MT) < 1 ? 1 : 16 / (WORDS * MT) > 4 ? 4 : 16 / (WORDS * MT);
-  const int groups = a.K / a.group;
-  const uint32_t *q = a.q + (long long)nr * (a.K / 8) + kq * WORDS;
-  const uint16_t *scale = a.scale + (long long)nr * groups;
-  const uint8_t *zero = a.zero ? a.zero + (long long)nr * groups : nullptr;
-  const uint16_t *x[MT];
+// MT tiles of 16 tokens, shared out over MS waves; KS waves share out the blocks of
+// WORDS * 32 elements of K.
+template <int MT, int WORDS, int KS, int MS, bool VEC>
+__global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Args a) {
+  constexpr int NTH = KS * MS * 64, MW = MT / MS;
+  constexpr int KC = MT == 4 ? 512 : 1024, KB = WORDS * 32, NB = KC / KB, U = NB / KS;  // K per chunk, per block; blocks
+  constexpr int XROW = KC + 8, QROW = KC / 8 + 4;  // 16 bytes more: a quarter wave's rows start in different banks
+  constexpr int XQ = MT * 16 * (KC / 8) / NTH;     // a thread's share of x, by 16 bytes
+  __shared__ union {
+    struct {
+      uint16_t x[MT * 16][XROW];
+      uint32_t q[16][QROW];
+      float scale[NB][16];
+      uint32_t minus[NB][16];  // -(16 + zero), twice
+    } c;
+    f32x4 red[KS][MT][64];
+  } lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, kq = lane >> 4;
+  const int ks = wave % KS, mt0 = wave / KS * MW;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16;
+  const int rows = min(a.M - m0, MT * 16), groups = a.K / a.group, blocks = a.K / KB;
+  const unsigned per = a.group / KB;  // blocks per group; 1 for the groups of 32 and 64
+  // the thread's share of a chunk: 16 bytes of a row of q, x by 16 bytes, one block's scale and zero point
+  const int qr = tid / (KC / 32), qc = tid % (KC / 32), sb = tid / 16, sr = min(n0 + tid % 16, a.N - 1);
+  const uint32_t *qp = a.q + (long long)min(n0 + qr, a.N - 1) * (a.K / 8) + qc * 4;
+  u32x4 qv = {0u, 0u, 0u, 0u}, xv[XQ];
+  uint16_t sv = 0;
+  uint8_t zv = 8;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) x[m] = a.x + (long long)min(m0 + m * 16 + col, a.M - 1) * a.x_ld + kq * WORDS * 8;
-  f32x4 tot[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) tot[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int blocks = a.K / KB;
-  for (int kb0 = wave; kb0 < blocks; kb0 += WAVES * U) {
-    // everything that U blocks need is requested before the first is used: a wave has few
-    // blocks, and their latency is most of its time.  Blocks behind the end: the last one
-    // again, with scale 0.
-    uint32_t w[U][WORDS], z[U];
-    u32x4 xv[U][MT][WORDS];
-    float s[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = min(kb0 + u * WAVES, blocks - 1), g = (int)((long long)kb * KB / a.group);
-      if constexpr (WORDS == 4) {
-        const u32x4 v = *(const u32x4 *)(q + (long long)kb * 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[u][i] = v[i];
-      } else if constexpr (WORDS == 2) {
-        const uint2 v = *(const uint2 *)(q + (long long)kb * 8);
-        w[u][0] = v.x;
-        w[u][1] = v.y;
-      } else {
-        w[u][0] = q[(long long)kb * 4];
-      }
-      z[u] = zero ? zero[g] & 15u : 8u;
-      s[u] = kb0 + u * WAVES < blocks ? bf2f(scale[g]) : 0.0f;
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) xv[u][m][i] = load_x<VEC>(x[m] + (long long)kb * KB + i * 8);
+  for (int i = 0; i < XQ; ++i) xv[i] = u32x4{0u, 0u, 0u, 0u};
+  auto fetch = [&](int k0) {
+    if (qr < 16 && k0 + qc * 32 < a.K) qv = *(const u32x4 *)(qp + k0 / 8);
+    if (sb < NB && k0 / KB + sb < blocks) {
+      const unsigned kb = k0 / KB + sb, g = WORDS < 4 || per == 1 ? kb : kb / per;
+      sv = a.scale[(long long)sr * groups + g];
+      if (a.zero) zv = a.zero[(long long)sr * groups + g];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t off = (0xC180u | z[u] << 3) * 0x10001u;
-      const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
+    for (int i = 0; i < XQ; ++i) {
+      const int e = i * NTH + tid, r = e / (KC / 8), c = e % (KC / 8) * 8;
+      if (r < rows && k0 + c < a.K) xv[i] = load_x<VEC>(a.x + (long long)(m0 + r) * a.x_ld + k0 + c);
+    }
+  };
+  f32x4 tot[MW];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < MW; ++m) tot[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  fetch(0);
+  for (int k0 = 0; k0 < a.K; k0 += KC) {
+    if (k0) __syncthreads();  // the chunk before has been read
+    if (qr < 16) *(u32x4 *)&lds.c.q[qr][qc * 4] = qv;
+    if (sb < NB) {
+      lds.c.scale[sb][tid % 16] = bf2f(sv);
+      lds.c.minus[sb][tid % 16] = (0xC180u | (zv & 15u) << 3) * 0x10001u;
+    }
+#pragma unroll
+    for (int i = 0; i < XQ; ++i) {
+      const int e = i * NTH + tid;
+      *(u32x4 *)&lds.c.x[e / (KC / 8)][e % (KC / 8) * 8] = permuted(xv[i]);
+    }
+    __syncthreads();
+    if (k0 + KC < a.K) fetch(k0 + KC);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int kb = ks * U + u;
+      if (k0 / KB + kb >= blocks) break;
+      const uint32_t off = lds.c.minus[kb][col];
+      const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
+      const float sc = lds.c.scale[kb][col];
+      const uint32_t *w = &lds.c.q[col][kb * (KB / 8) + kq * WORDS];
+      uint32_t wq[WORDS];
+      if constexpr (WORDS == 4)
+        *(u32x4 *)wq = *(const u32x4 *)w;
+      else if constexpr (WORDS == 2)
+        *(uint2 *)wq = *(const uint2 *)w;
+      else
+        wq[0] = w[0];
+#pragma unroll
+      for (int m = 0; m < MW; ++m) {
+        // rows without a token hold anything: they reach only their own rows of the result
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          const bf16x8 xp = permuted(xv[u][m][i]);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp, unpack(w[u][i]), acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xp, minus, acc, 0, 0, 0);
+          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[(mt0 + m) * 16 + col][kb * KB + kq * WORDS * 8 + i * 8];
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[i]), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus, acc, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[m][i] += s[u] * acc[i];
+        for (int i = 0; i < 4; ++i) tot[m][i] += sc * acc[i];
       }
     }
   }
+  __syncthreads();
 #pragma unroll
-  for (int m = 0; m < MT; ++m) red[wave][m][lane] = tot[m];
+  for (int m = 0; m < MW; ++m) lds.red[ks][mt0 + m][lane] = tot[m];
   __syncthreads();
   // lane (n = lane & 15, rows (lane >> 4) * 4 ..) of tile m
-  for (int m = wave; m < MT; m += WAVES) {
-    f32x4 y = red[0][m][lane];
+  for (int m = wave; m < MT; m += KS * MS) {
+    f32x4 y = lds.red[0][m][lane];
 #pragma unroll
-    for (int k = 1; k < WAVES; ++k) y += red[k][m][lane];
+    for (int k = 1; k < KS; ++k) y += lds.red[k][m][lane];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = m0 + m * 16 + kq * 4 + i;
-      if (row < a.M && n < a.N) store_elem(a.out, (long long)row * a.N + n, y[i], a.out_bf16);
+      if (row < a.M && n0 + col < a.N) store_elem(a.out, (long long)row * a.N + n0 + col, y[i], a.out_bf16);
     }
   }
 }
 
-template <int MT, int WORDS, int WAVES>
+template <int MT, int WORDS>
 hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
+  constexpr int MS = MT == 4 ? 2 : 1, KS = 8 / MS;
   const dim3 grid((unsigned)rec_cdiv(a.N, 16), (unsigned)rec_cdiv(a.M, MT * 16));
   if (vec)
-    hipLaunchKernelGGL((w4_kernel<MT, WORDS, WAVES, true>), grid, dim3(WAVES * 64), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<MT, WORDS, KS, MS, true>), grid, dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((w4_kernel<MT, WORDS, WAVES, false>), grid, dim3(WAVES * 64), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<MT, WORDS, KS, MS, false>), grid, dim3(512), 0, st, a);
   return hipGetLastError();
 }
-// Sixteen waves a workgroup where the grid alone does not give every CU eight.
 template <int MT>
 hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
-  const bool few = rec_cdiv(a.N, 16) * rec_cdiv(a.M, MT * 16) <= 256;
-  if (a.group % 128 == 0) return few ? launch_w<MT, 4, 16>(a, vec, st) : launch_w<MT, 4, 8>(a, vec, st);
-  if (a.group == 64) return few ? launch_w<MT, 2, 16>(a, vec, st) : launch_w<MT, 2, 8>(a, vec, st);
-  return few ? launch_w<MT, 1, 16>(a, vec, st) : launch_w<MT, 1, 8>(a, vec, st);
+  if (a.group % 128 == 0) return launch_w<MT, 4>(a, vec, st);
+  return a.group == 64 ? launch_w<MT, 2>(a, vec, st) : launch_w<MT, 1>(a, vec, st);
 }
 
 }  // namespace
