@@ -67,16 +67,19 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
 }
 
 // MT tiles of 16 tokens, shared out over MS waves; KS waves share out the blocks of
-// WORDS * 32 elements of K.
-template <int MT, int WORDS, int KS, int MS, bool VEC>
-__global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Args a) {
+// WORDS * 32 elements of K.  XR: rows of x kept, 16 MT, or 4 for at most four tokens,
+// which leaves room for chunks twice as long (K = 2048 is one: 7.8 -> 6 us for one token).
+template <int MT, int XR, int WORDS, int KS, int MS, bool VEC>
+__global__ __launch_bounds__(KS * MS * 64, 4) void w4_kernel(W4Args a) {
   constexpr int NTH = KS * MS * 64, MW = MT / MS;
-  constexpr int KC = MT == 4 ? 512 : 1024, KB = WORDS * 32, NB = KC / KB, U = NB / KS;  // K per chunk, per block; blocks
+  constexpr int KC = XR == 4 ? 2048 : MT == 4 ? 512 : 1024;         // K per chunk
+  constexpr int KB = WORDS * 32, NB = KC / KB, U = NB / KS;         // per block; blocks of a chunk, of a wave
   constexpr int XROW = KC + 8, QROW = KC / 8 + 4;  // 16 bytes more: a quarter wave's rows start in different banks
-  constexpr int XQ = MT * 16 * (KC / 8) / NTH;     // a thread's share of x, by 16 bytes
+  constexpr int XQ = XR * (KC / 8) / NTH, QQ = (16 * (KC / 32) + NTH - 1) / NTH;  // a thread's 16 bytes of x and q
+  constexpr int SQ = (NB * 16 + NTH - 1) / NTH;                                     // and its scales
   __shared__ union {
     struct {
-      uint16_t x[MT * 16][XROW];
+      uint16_t x[XR][XROW];
       uint32_t q[16][QROW];
       float scale[NB][16];
       uint32_t minus[NB][16];  // -(16 + zero), twice
@@ -88,20 +91,31 @@ __global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Arg
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16;
   const int rows = min(a.M - m0, MT * 16), groups = a.K / a.group, blocks = a.K / KB;
   const unsigned per = a.group / KB;  // blocks per group; 1 for the groups of 32 and 64
-  // the thread's share of a chunk: 16 bytes of a row of q, x by 16 bytes, one block's scale and zero point
-  const int qr = tid / (KC / 32), qc = tid % (KC / 32), sb = tid / 16, sr = min(n0 + tid % 16, a.N - 1);
-  const uint32_t *qp = a.q + (long long)min(n0 + qr, a.N - 1) * (a.K / 8) + qc * 4;
-  u32x4 qv = {0u, 0u, 0u, 0u}, xv[XQ];
-  uint16_t sv = 0;
-  uint8_t zv = 8;
+  // the thread's share of a chunk: q and x by 16 bytes along their rows, blocks' scales and zero points
+  u32x4 qv[QQ], xv[XQ];
+  uint16_t sv[SQ];
+  uint8_t zv[SQ];
+#pragma unroll
+  for (int i = 0; i < QQ; ++i) qv[i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < XQ; ++i) xv[i] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < SQ; ++i) sv[i] = 0, zv[i] = 8;
+  const int sr = min(n0 + tid % 16, a.N - 1);
   auto fetch = [&](int k0) {
-    if (qr < 16 && k0 + qc * 32 < a.K) qv = *(const u32x4 *)(qp + k0 / 8);
-    if (sb < NB && k0 / KB + sb < blocks) {
-      const unsigned kb = k0 / KB + sb, g = WORDS < 4 || per == 1 ? kb : kb / per;
-      sv = a.scale[(long long)sr * groups + g];
-      if (a.zero) zv = a.zero[(long long)sr * groups + g];
+#pragma unroll
+    for (int i = 0; i < QQ; ++i) {
+      const int e = i * NTH + tid, r = e / (KC / 32), c = e % (KC / 32) * 32;
+      if (r < 16 && k0 + c < a.K)
+        qv[i] = *(const u32x4 *)(a.q + (long long)min(n0 + r, a.N - 1) * (a.K / 8) + (k0 + c) / 8);
+    }
+#pragma unroll
+    for (int i = 0; i < SQ; ++i) {
+      const unsigned sb = (i * NTH + tid) / 16, kb = k0 / KB + sb, g = WORDS < 4 || per == 1 ? kb : kb / per;
+      if (sb < NB && (int)kb < blocks) {
+        sv[i] = a.scale[(long long)sr * groups + g];
+        if (a.zero) zv[i] = a.zero[(long long)sr * groups + g];
+      }
     }
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
@@ -115,15 +129,23 @@ __global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Arg
   fetch(0);
   for (int k0 = 0; k0 < a.K; k0 += KC) {
     if (k0) __syncthreads();  // the chunk before has been read
-    if (qr < 16) *(u32x4 *)&lds.c.q[qr][qc * 4] = qv;
-    if (sb < NB) {
-      lds.c.scale[sb][tid % 16] = bf2f(sv);
-      lds.c.minus[sb][tid % 16] = (0xC180u | (zv & 15u) << 3) * 0x10001u;
+#pragma unroll
+    for (int i = 0; i < QQ; ++i) {
+      const int e = i * NTH + tid, r = e / (KC / 32);
+      if (r < 16) *(u32x4 *)&lds.c.q[r][e % (KC / 32) * 4] = qv[i];
+    }
+#pragma unroll
+    for (int i = 0; i < SQ; ++i) {
+      const int sb = (i * NTH + tid) / 16;
+      if (sb < NB) {
+        lds.c.scale[sb][tid % 16] = bf2f(sv[i]);
+        lds.c.minus[sb][tid % 16] = (0xC180u | (zv[i] & 15u) << 3) * 0x10001u;
+      }
     }
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
-      const int e = i * NTH + tid;
-      *(u32x4 *)&lds.c.x[e / (KC / 8)][e % (KC / 8) * 8] = permuted(xv[i]);
+      const int e = i * NTH + tid, r = e / (KC / 8);
+      if (r < rows) *(u32x4 *)&lds.c.x[r][e % (KC / 8) * 8] = permuted(xv[i]);
     }
     __syncthreads();
     if (k0 + KC < a.K) fetch(k0 + KC);
@@ -144,11 +166,11 @@ __global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Arg
         wq[0] = w[0];
 #pragma unroll
       for (int m = 0; m < MW; ++m) {
-        // rows without a token hold anything: they reach only their own rows of the result
+        // rows without a token hold anything (or another's): they reach only their own rows of the result
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[(mt0 + m) * 16 + col][kb * KB + kq * WORDS * 8 + i * 8];
+          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[((mt0 + m) * 16 + col) % XR][kb * KB + kq * WORDS * 8 + i * 8];
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[i]), acc, 0, 0, 0);
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus, acc, 0, 0, 0);
         }
@@ -174,20 +196,20 @@ __global__ __launch_bounds__(KS * MS * 64, MT == 1 ? 6 : 4) void w4_kernel(W4Arg
   }
 }
 
-template <int MT, int WORDS>
+template <int MT, int XR, int WORDS>
 hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
   constexpr int MS = MT == 4 ? 2 : 1, KS = 8 / MS;
   const dim3 grid((unsigned)rec_cdiv(a.N, 16), (unsigned)rec_cdiv(a.M, MT * 16));
   if (vec)
-    hipLaunchKernelGGL((w4_kernel<MT, WORDS, KS, MS, true>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<MT, XR, WORDS, KS, MS, true>), grid, dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((w4_kernel<MT, WORDS, KS, MS, false>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<MT, XR, WORDS, KS, MS, false>), grid, dim3(512), 0, st, a);
   return hipGetLastError();
 }
-template <int MT>
+template <int MT, int XR = 16 * MT>
 hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
-  if (a.group % 128 == 0) return launch_w<MT, 4>(a, vec, st);
-  return a.group == 64 ? launch_w<MT, 2>(a, vec, st) : launch_w<MT, 1>(a, vec, st);
+  if (a.group % 128 == 0) return launch_w<MT, XR, 4>(a, vec, st);
+  return a.group == 64 ? launch_w<MT, XR, 2>(a, vec, st) : launch_w<MT, XR, 1>(a, vec, st);
 }
 
 }  // namespace
@@ -228,7 +250,7 @@ hipError_t launch_w4(const void *x, const void *q, const void *scale, const void
   const long long rows = rec_cdiv(N, 16);
   if (M > 32 && rows * rec_cdiv(M, 64) >= 512) return launch_mt<4>(a, vec, st);
   if (M > 16 && rows * rec_cdiv(M, 32) >= 512) return launch_mt<2>(a, vec, st);
-  return launch_mt<1>(a, vec, st);
+  return M <= 4 ? launch_mt<1, 4>(a, vec, st) : launch_mt<1>(a, vec, st);
 }
 
 }  // namespace ret
