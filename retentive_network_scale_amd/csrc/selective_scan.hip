@@ -118,6 +118,32 @@ __device__ __forceinline__ float row16_sum(float x) {
   return x;
 }
 
+// c[i] += x_{n0 + i} y for the lane's four states, where the lanes of a quad hold x_{n0} ..
+// x_{n0 + 3} of their row and y is the lane's own (its channel's): an outer product per
+// quad, one step of the matrix cores (16 blocks of 4 x 4, in fp32) for four multiplications
+// of the vector unit, which is what bounds these kernels.
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+__device__ __forceinline__ f32x4 quad_outer(float x, float y, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_4x4x1f32(x, y, c, 0, 0, 0);
+}
+
+// h <- e h + dtu B for one channel's NS states: Bq are the quad's values of B, Bv the lane's.
+template <int NS>
+__device__ __forceinline__ void advance(float (&h)[NS], const float (&e)[NS], float dtu, const float (&Bq)[(NS + 3) / 4],
+                                        const float (&Bv)[NS]) {
+  if constexpr (NS % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) {
+      const f32x4 r = quad_outer(Bq[i / 4], dtu, f32x4{e[i] * h[i], e[i + 1] * h[i + 1], e[i + 2] * h[i + 2], e[i + 3] * h[i + 3]});
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[i + k] = r[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) h[i] = e[i] * h[i] + dtu * Bv[i];
+  }
+}
+
 // NS states of a lane from n0 on.  VEC: N and n0 are multiples of four, p is aligned.
 template <int NS, bool VEC>
 __device__ __forceinline__ void load_state(const float *p, int N, int n0, bool ok, float (&h)[NS]) {
@@ -237,6 +263,14 @@ __device__ __forceinline__ void get_states(const float *p, float (&r)[NS]) {
 #pragma unroll
     for (int i = 0; i < NS; ++i) r[i] = p[i];
   }
+}
+
+// The quad's values of a row of states: the lane's is the one of its place in the quad.
+template <int NS>
+__device__ __forceinline__ void get_quad(const float *p, int lane, float (&r)[(NS + 3) / 4]) {
+  if constexpr (NS % 4 == 0)
+#pragma unroll
+    for (int i = 0; i < NS; i += 4) r[i / 4] = p[i + (lane & 3)];
 }
 
 // A lane's share of a tile of B or C: quads of states, NS of them per token.  Wide loads
@@ -417,23 +451,26 @@ __global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
       float y[CJ][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS];
+        float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS], Bq[(NS + 3) / 4];
         get_lane(&dts[t4 + k][c0], dt);
         get_lane(&dus[t4 + k][c0], dtu);
-        get_states(&Bs[t4 + k][n0], Bv);
+        get_quad<NS>(&Bs[t4 + k][n0], lane, Bq);
+        if constexpr (NS % 4) get_states(&Bs[t4 + k][n0], Bv);
         if constexpr (MODE != STATES) get_states(&Cs[t4 + k][n0], Cv);
         if constexpr (MODE == CHECKPOINTS) get_lane(&dys[t4 + k][c0], dy);
 #pragma unroll
         for (int j = 0; j < CJ; ++j) {
           float acc = 0.0f;
           if constexpr (MODE != OUTPUT) sum[j] += dt[j];
+          float e[NS];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) e[i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
+          advance(h[j], e, dtu[j], Bq, Bv);
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            const float e = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
-            h[j][i] = e * h[j][i] + dtu[j] * Bv[i];
             if constexpr (MODE == OUTPUT) acc += h[j][i] * Cv[i];
             if constexpr (MODE == CHECKPOINTS) {
-              pr[j][i] *= e;
+              pr[j][i] *= e[i];
               gs[j][i] += pr[j][i] * (dy[j] * Cv[i]);
             }
           }
@@ -696,17 +733,20 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
       checkpoint();
 #pragma unroll
       for (int t = 0; t < SUB; ++t) {
-        float dt[CJ], dtu[CJ], Bv[NS], Cv[NS];
+        float dt[CJ], dtu[CJ], Bv[NS], Cv[NS], Bq[(NS + 3) / 4];
         get_lane(&s.dt[t1 + t][c0], dt);
         get_lane(&s.du[t1 + t][c0], dtu);
-        get_states(&s.B[t1 + t][n0], Bv);
+        get_quad<NS>(&s.B[t1 + t][n0], lane, Bq);
+        if constexpr (NS % 4) get_states(&s.B[t1 + t][n0], Bv);
         get_states(&s.C[t1 + t][n0], Cv);
 #pragma unroll
         for (int j = 0; j < CJ; ++j) {
-          float acc = 0.0f;
+          float acc = 0.0f, e[NS];
+#pragma unroll
+          for (int i = 0; i < NS; ++i) e[i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]);
+          advance(h[j], e, dtu[j], Bq, Bv);
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            h[j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]) * h[j][i] + dtu[j] * Bv[i];
             hh[t][j][i] = h[j][i];
             acc += h[j][i] * Cv[i];
           }
@@ -725,18 +765,31 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
 #pragma unroll
         for (int q = 3; q >= 0; --q) {
           const int t = t4 + q;
-          float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS], pB[NS], pC[NS];
+          float dt[CJ], dtu[CJ], dy[CJ], Bv[NS], Cv[NS], Cq[(NS + 3) / 4], pB[NS], pC[NS];
           get_lane(&s.dt[t1 + t][c0], dt);
           get_lane(&s.du[t1 + t][c0], dtu);
           get_lane(&s.dy[t1 + t][c0], dy);
           get_states(&s.B[t1 + t][n0], Bv);
-          get_states(&s.C[t1 + t][n0], Cv);
+          get_quad<NS>(&s.C[t1 + t][n0], lane, Cq);
+          if constexpr (NS % 4) get_states(&s.C[t1 + t][n0], Cv);
 #pragma unroll
           for (int j = 0; j < CJ; ++j) {
             gB[j][q] = sA[j][q] = 0.0f;
+            float gt[NS];
+            if constexpr (NS % 4 == 0) {
+#pragma unroll
+              for (int i = 0; i < NS; i += 4) {
+                const f32x4 r = quad_outer(Cq[i / 4], dy[j], f32x4{carry[j][i], carry[j][i + 1], carry[j][i + 2], carry[j][i + 3]});
+#pragma unroll
+                for (int k = 0; k < 4; ++k) gt[i + k] = r[k];
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < NS; ++i) gt[i] = Cv[i] * dy[j] + carry[j][i];
+            }
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-              const float g = Cv[i] * dy[j] + carry[j][i];
+              const float g = gt[i];
               carry[j][i] = __builtin_amdgcn_exp2f(dt[j] * A2[j][i]) * g;
               const float wv = carry[j][i] * (t > 0 ? hh[t > 0 ? t - 1 : 0][j][i] : hstart[j][i]);
               sA[j][q] += A2[j][i] * wv;  // times log2 e; taken out below
