@@ -6,6 +6,7 @@
 // a run of tokens, so each input is read once but for the K - 1 in front of a run.  The
 // loads of a step's tokens go out together.
 #include <algorithm>
+#include <type_traits>
 
 #include "recurrent.hpp"
 
@@ -27,23 +28,35 @@ struct ConvArgs {
   long long main_threads, state_at;  // runs' threads; the first of the state's, a workgroup's start behind them
 };
 
+// VC neighbouring channels as they come from memory.
+template <typename T, int VC>
+struct Raw {
+  using V = std::conditional_t<VC == 1, T, std::conditional_t<sizeof(T) == 2, uint2, float4>>;
+  V v;
+  __device__ __forceinline__ void load(const T *p) { v = *(const V *)p; }
+  __device__ __forceinline__ void get(float (&r)[VC]) const {
+    if constexpr (VC == 4 && sizeof(T) == 2) {
+      r[0] = __uint_as_float(v.x << 16);
+      r[1] = __uint_as_float(v.x & 0xffff0000u);
+      r[2] = __uint_as_float(v.y << 16);
+      r[3] = __uint_as_float(v.y & 0xffff0000u);
+    } else if constexpr (VC == 4) {
+      r[0] = v.x;
+      r[1] = v.y;
+      r[2] = v.z;
+      r[3] = v.w;
+    } else if constexpr (sizeof(T) == 2) {
+      r[0] = bf2f(v);
+    } else {
+      r[0] = v;
+    }
+  }
+};
 template <typename T, int VC>
 __device__ __forceinline__ void loadc(const T *p, float (&r)[VC]) {
-  if constexpr (VC == 4 && sizeof(T) == 2) {
-    const uint2 v = *(const uint2 *)p;
-    r[0] = __uint_as_float(v.x << 16);
-    r[1] = __uint_as_float(v.x & 0xffff0000u);
-    r[2] = __uint_as_float(v.y << 16);
-    r[3] = __uint_as_float(v.y & 0xffff0000u);
-  } else if constexpr (VC == 4) {
-    const float4 v = *(const float4 *)p;
-    r[0] = v.x;
-    r[1] = v.y;
-    r[2] = v.z;
-    r[3] = v.w;
-  } else {
-    r[0] = load_elem(p, 0, sizeof(T) == 2);
-  }
+  Raw<T, VC> v;
+  v.load(p);
+  v.get(r);
 }
 
 template <typename T, int VC>
@@ -103,11 +116,18 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
   if (t0 >= t1) return;
   float w[K][VC], bias[VC], win[K - 1 + STEP][VC];
   load_taps<T, K, VC>(a, d, w, bias);
+  Raw<T, VC> next[STEP];
+  auto fetch = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) next[i].load((const T *)a.x + (b * a.L + min(t + i, t1 - 1)) * a.x_ld + d);
+  };
+  fetch(t0);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) input_at<T, K, VC>(a, b, t0 - (K - 1) + j, d, win[j]);
   for (int t = t0; t < t1; t += STEP) {
 #pragma unroll
-    for (int i = 0; i < STEP; ++i) input_at<T, K, VC>(a, b, min(t + i, t1 - 1), d, win[K - 1 + i]);
+    for (int i = 0; i < STEP; ++i) next[i].get(win[K - 1 + i]);
+    fetch(t + STEP);
 #pragma unroll
     for (int i = 0; i < STEP; ++i) {
       float y[VC];
@@ -161,16 +181,24 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
       }
       // token t closes input s = t - (K - 1); the first run starts with s = -(K - 1)
       const int end = max(t1, t0) + K - 1;
-      for (int t = t0; t < end; t += S) {
-        float go[S][VC];
+      Raw<T, VC> xr[S] = {}, gr[S] = {};  // the next step's
+      auto fetch = [&](int t) {
 #pragma unroll
         for (int i = 0; i < S; ++i) {  // tokens behind the end: any inside, and no g
           const int r = min(t + i, len - 1);
-          if (len > 0) {
-            loadc<T, VC>((const T *)a.x + (b * a.L + r) * a.x_ld + d, x[K - 1 + i]);
-            loadc<T, VC>((const T *)a.d_o + (b * a.L + r) * a.D + d, go[i]);
-          }
+          xr[i].load((const T *)a.x + (b * a.L + r) * a.x_ld + d);
+          gr[i].load((const T *)a.d_o + (b * a.L + r) * a.D + d);
         }
+      };
+      if (len > 0) fetch(t0);
+      for (int t = t0; t < end; t += S) {
+        float go[S][VC];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          xr[i].get(x[K - 1 + i]);
+          gr[i].get(go[i]);
+        }
+        if (len > 0) fetch(t + S);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
 #pragma unroll
