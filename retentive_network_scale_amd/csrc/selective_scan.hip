@@ -36,9 +36,10 @@ struct ScanArgs {
   void *out;
   float *hT;
   long long u_ld, delta_ld, z_ld, b_ld, c_ld;
+  int waves;                     // of a pass
   int B, L, D, N, G, Dg, tiles;  // Dg = D / G channels per group, tiles of them per workgroup
   int seg_len, nseg, softplus, out_bf16;
-  int span, nspan;  // segments that a workgroup of the backward's main pass walks, and how many such spans
+  int span, nspan, span_len;  // spans: segments that a workgroup of the backward's main pass walks; their tokens
   int vec;  // everything may be accessed by fours: channels, states, B and C
   // workspace: segment states [B * nseg][D][N], sums of dt [B * nseg][D]
   float *seg, *sdt;
@@ -60,26 +61,27 @@ constexpr int wide_cj(int NS) { return NS <= 4 ? 4 : 16 / NS; }
 // states, SUB CJ NS fp32, stay in 64 registers.
 constexpr int bwd_cj(int NS) { return NS >= 8 ? 1 : 2; }
 constexpr int bwd_sub(int NS) { return std::min(TT, 64 / (NS * bwd_cj(NS))); }
-constexpr int BWD_WAVES = 4;
+constexpr int BWD_WAVES = 4, PASS_WAVES = 4;
 
 // What a workgroup works on: a segment, or a span of them.
 struct Where {
   int b, s, g, tile, len, t_lo, t_hi;
 };
 template <bool SPANS>
-__device__ __forceinline__ Where where(const ScanArgs &a) {
+__device__ __forceinline__ Where where(const ScanArgs &a, int id) {
   Where w;
-  int id = blockIdx.x;
   w.tile = id % a.tiles;
   id /= a.tiles;
   w.g = id % a.G;
   id /= a.G;
-  const int parts = SPANS ? a.nspan : a.nseg, tokens = SPANS ? a.span * a.seg_len : a.seg_len;
+  const int parts = SPANS ? a.nspan : a.nseg;
   w.s = id % parts;
   w.b = id / parts;
   w.len = a.lengths ? min(max(a.lengths[w.b], 0), a.L) : a.L;
-  w.t_lo = (int)min((long long)w.s * tokens, (long long)w.len);
-  w.t_hi = (int)min((long long)w.t_lo + tokens, (long long)w.len);
+  const int p = SPANS ? w.s : w.s / a.span;  // segments end with their span
+  const long long end = (long long)(p + 1) * a.span_len, lo = (long long)p * a.span_len + (SPANS ? 0 : w.s % a.span * a.seg_len);
+  w.t_lo = (int)min(min(lo, end), (long long)w.len);
+  w.t_hi = (int)min(SPANS ? end : min(lo + a.seg_len, end), (long long)w.len);
   return w;
 }
 
@@ -350,14 +352,21 @@ enum { OUTPUT, STATES, CHECKPOINTS };
 //     sub-tile, and the gradient that the segment's own outputs send to the state in
 //     front of it, sum_t exp(A sum dt) C_t dy_t.
 template <typename T, int NS, int CJ, int MODE, bool VEC>
-__global__ __launch_bounds__(64, 3) void scan_pass_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * PASS_WAVES, 3) void scan_pass_kernel(ScanArgs a) {
   constexpr int NP = 4 * NS, CW = 16 * CJ, SUB = bwd_sub(NS);
-  __shared__ __align__(16) float dts[TT][CW], dus[TT][CW];  // dt, dt u; OUTPUT: y replaces dt u
-  __shared__ __align__(16) float dys[MODE == CHECKPOINTS ? TT : 1][CW];
-  __shared__ __align__(16) float Bs[TT][NP], Cs[MODE == STATES ? 1 : TT][NP];
-  const Where w = where<false>(a);
+  struct WaveLds {
+    float dt[TT][CW], du[TT][CW];  // dt, dt u; OUTPUT: y replaces dt u
+    float dy[MODE == CHECKPOINTS ? TT : 1][CW];
+    float B[TT][NP], C[MODE == STATES ? 1 : TT][NP];
+  };
+  __shared__ __align__(16) WaveLds lds[PASS_WAVES];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), id = blockIdx.x * (blockDim.x >> 6) + wave;
+  if (id >= a.waves) return;
+  float(*const dts)[CW] = lds[wave].dt, (*const dus)[CW] = lds[wave].du, (*const dys)[CW] = lds[wave].dy;
+  float(*const Bs)[NP] = lds[wave].B, (*const Cs)[NP] = lds[wave].C;
+  const Where w = where<false>(a, id);
   const bool last = w.s == a.nseg - 1;
-  const int lane = threadIdx.x, row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
+  const int lane = threadIdx.x & 63, row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
   const int rel = w.tile * CW + c0;
   const long long d = (long long)w.g * a.Dg + rel;
   const long long sd = ((long long)w.b * a.nseg + w.s) * a.D + d;
@@ -631,7 +640,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
   };
   __shared__ __align__(16) WaveLds lds[BWD_WAVES];
   __shared__ float part[2][BWD_WAVES][TT][2][NP];  // each wave's sums over its channels
-  const Where w = where<true>(a);
+  const Where w = where<true>(a, blockIdx.x);
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int row = lane >> 4, c0 = (lane & 15) * CJ, n0 = row * NS;
   const int base = (w.tile * waves + wave) * CW, rel = base + c0;
@@ -985,7 +994,7 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
 int state_regs(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 struct ScanPlan {
-  int cj, seg_len, nseg, subs, span, nspan;
+  int cj, seg_len, nseg, subs, span, nspan, span_len;
   int bwd_waves, bwd_tiles;
   size_t seg, sdt, gseg, ck, ckdt, bcpart, dApart, dDpart, dbpart, total;
 };
@@ -1000,32 +1009,34 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   const int wide = wide_cj(NS);
   const long long groups = (long long)B * G, ww = groups * rec_cdiv(Dg, 16 * wide), w16 = groups * rec_cdiv(Dg, 16);
   const long long most = rec_cdiv(L, 4 * TT);  // segments of at least four tiles
-  long long nseg = 1;
   if (bwd) {
-    // The checkpoints' pass wants three waves per SIMD; the main pass, at two, few long
-    // spans: each starts with loads that nothing hides.
+    // The main pass, at two waves per SIMD, takes few long spans: each starts with loads that
+    // nothing hides.  The checkpoints' pass, at three, cuts them further.
     const int cw = 16 * bwd_cj(NS);
     p.bwd_waves = (int)std::min<long long>(BWD_WAVES, rec_cdiv(Dg, cw));
     p.bwd_tiles = (int)rec_cdiv(Dg, (long long)cw * p.bwd_waves);
+    const long long spans = std::min(rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves), rec_cdiv(L, 2 * TT));
+    p.span_len = (int)(rec_cdiv(rec_cdiv(L, spans), TT) * TT);
+    p.nspan = (int)rec_cdiv(L, p.span_len);
     p.cj = ww * rec_cdiv(L, 2 * TT) >= 1024 ? wide : 1;
-    nseg = std::min(rec_cdiv(4096, p.cj == 1 ? w16 : ww), rec_cdiv(L, 2 * TT));
+    const long long cut = std::min<long long>(std::max<long long>(3072 / ((p.cj == 1 ? w16 : ww) * p.nspan), 1),
+                                              rec_cdiv(p.span_len, 2 * TT));
+    p.seg_len = (int)(rec_cdiv(rec_cdiv(p.span_len, cut), TT) * TT);
+    p.span = (int)rec_cdiv(p.span_len, p.seg_len);
+    p.nseg = p.nspan * p.span;
   } else {
     p.bwd_waves = p.bwd_tiles = 0;
     p.cj = ww >= 1024 ? wide : 1;
+    long long nseg = 1;
     if (w16 < 1024 && most > 1) {
       p.cj = ww * most >= 1024 ? wide : 1;
       nseg = std::min(most, rec_cdiv(3072, p.cj == 1 ? w16 : ww));
     }
+    p.seg_len = p.span_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
+    p.nseg = p.nspan = (int)rec_cdiv(L, p.seg_len);
+    p.span = 1;
   }
-  p.seg_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
-  p.nseg = (int)rec_cdiv(L, p.seg_len);
   p.subs = p.seg_len / SUB;
-  p.span = p.nspan = 1;
-  if (bwd) {
-    const long long spans = std::min<long long>(p.nseg, rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves));
-    p.span = (int)rec_cdiv(p.nseg, spans);
-    p.nspan = (int)rec_cdiv(p.nseg, p.span);
-  }
   size_t off = 0;
   auto take = [&off](size_t floats) {
     const size_t at = off;
@@ -1087,10 +1098,15 @@ template <typename T, int NS, int MODE>
 hipError_t launch_pass(ScanArgs a, int cj, hipStream_t st) {
   if (!a.vec) cj = 1;
   a.tiles = (int)rec_cdiv(a.Dg, 16 * cj);
-  const long long blocks = (long long)a.B * a.nseg * a.G * a.tiles;
-  if (!a.vec) return launch(scan_pass_kernel<T, NS, 1, MODE, false>, blocks, 64, st, a);
-  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE, true>, blocks, 64, st, a)
-                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE, true>, blocks, 64, st, a);
+  // the waves do not meet: workgroups of four spread them evenly over the SIMDs, of one over the CUs
+  const long long waves = (long long)a.B * a.nseg * a.G * a.tiles;
+  if (waves > 0x7fffffffLL) return hipErrorInvalidValue;
+  a.waves = (int)waves;
+  const int per = waves > 1024 ? PASS_WAVES : 1;
+  const long long blocks = rec_cdiv(waves, per);
+  if (!a.vec) return launch(scan_pass_kernel<T, NS, 1, MODE, false>, blocks, 64 * per, st, a);
+  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE, true>, blocks, 64 * per, st, a)
+                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE, true>, blocks, 64 * per, st, a);
 }
 template <typename T, int MODE>
 hipError_t launch_pass(const ScanArgs &a, int cj, hipStream_t st) {
@@ -1260,8 +1276,9 @@ ret_status_t selective_scan(const void *u, const void *delta, const float *A, co
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
   const RecSpan hin[] = {hi}, others[] = {outs[0], outs[2]};
   if ((s = rec_check_overlap(hin, others)) != RET_OK) return s;
-  a.seg_len = p.seg_len;
+  a.seg_len = a.span_len = p.seg_len;
   a.nseg = p.nseg;
+  a.span = 1;
   a.seg = (float *)((char *)workspace + p.seg);
   a.sdt = (float *)((char *)workspace + p.sdt);
   const bool bf = in_dtype == RET_BF16;
@@ -1338,6 +1355,7 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   a.subs = p.subs;
   a.span = p.span;
   a.nspan = p.nspan;
+  a.span_len = p.span_len;
   a.seg = (float *)(ws + p.seg);
   a.sdt = (float *)(ws + p.sdt);
   a.gseg = (float *)(ws + p.gseg);
