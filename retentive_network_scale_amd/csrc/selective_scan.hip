@@ -53,9 +53,11 @@ struct ScanArgs {
   int subs;           // sub-tiles per segment
 };
 
-// Channels per lane of a pass where there are channels enough: 16 elements per lane share
-// what a token costs beside them.
-constexpr int wide_cj(int NS) { return NS <= 4 ? 4 : 16 / NS; }
+// Channels per lane of a pass where there are channels enough: up to 16 elements per lane
+// share what a token costs beside them.  Four channels instead of two were no faster for
+// outputs and slower for checkpoints (223 against 179 us at B 2, L 4096, D 4096, N 16), where
+// they leave two waves per SIMD.
+constexpr int wide_cj(int NS) { return NS <= 8 ? 2 : 1; }
 
 // Channels per lane and tokens per sub-tile of the backward's main pass: a sub-tile's
 // states, SUB CJ NS fp32, stay in 64 registers.
@@ -1011,7 +1013,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   const long long most = rec_cdiv(L, 4 * TT);  // segments of at least four tiles
   if (bwd) {
     // The main pass, at two waves per SIMD, takes few long spans: each starts with loads that
-    // nothing hides.  The checkpoints' pass, at three, cuts them further.
+    // nothing hides.  The checkpoints' pass, at four, cuts them further.
     const int cw = 16 * bwd_cj(NS);
     p.bwd_waves = (int)std::min<long long>(BWD_WAVES, rec_cdiv(Dg, cw));
     p.bwd_tiles = (int)rec_cdiv(Dg, (long long)cw * p.bwd_waves);
@@ -1019,7 +1021,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.span_len = (int)(rec_cdiv(rec_cdiv(L, spans), TT) * TT);
     p.nspan = (int)rec_cdiv(L, p.span_len);
     p.cj = ww * rec_cdiv(L, 2 * TT) >= 1024 ? wide : 1;
-    const long long cut = std::min<long long>(std::max<long long>(3072 / ((p.cj == 1 ? w16 : ww) * p.nspan), 1),
+    const long long cut = std::min<long long>(std::max<long long>(4096 / ((p.cj == 1 ? w16 : ww) * p.nspan), 1),
                                               rec_cdiv(p.span_len, 2 * TT));
     p.seg_len = (int)(rec_cdiv(rec_cdiv(p.span_len, cut), TT) * TT);
     p.span = (int)rec_cdiv(p.span_len, p.seg_len);
@@ -1030,7 +1032,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     long long nseg = 1;
     if (w16 < 1024 && most > 1) {
       p.cj = ww * most >= 1024 ? wide : 1;
-      nseg = std::min(most, rec_cdiv(3072, p.cj == 1 ? w16 : ww));
+      nseg = std::min(most, rec_cdiv(8192, p.cj == 1 ? w16 : ww));
     }
     p.seg_len = p.span_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
     p.nseg = p.nspan = (int)rec_cdiv(L, p.seg_len);

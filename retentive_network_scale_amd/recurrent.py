@@ -21,7 +21,7 @@ CausalConvGrads = namedtuple("CausalConvGrads", "dx dw dbias d_state_in")
 
 # The calls here are short (a decode step's kernels take a few microseconds), so what
 # every call does on the host is kept to a few comparisons per tensor.
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _bad(t, name, shape, dtype, index):
@@ -56,7 +56,12 @@ def _rows(t, name, lead, shape, dtype, index, width):
         _bad(t, name, shape, dtype, index)
     if t.is_contiguous():
         return t.data_ptr(), width
-    strides, want, bad = t.stride(), 1, False
+    strides = t.stride()
+    ld = strides[lead - 1]
+    if (shape[lead - 1] > 1 and ld >= width and (lead == 1 or strides[0] == shape[1] * ld) and strides[-1] == 1
+            and (len(shape) == lead + 1 or strides[-2] == shape[-1])):
+        return t.data_ptr(), ld
+    want, bad = 1, False  # axes of one element may have any stride
     for n, s in zip(reversed(shape[lead:]), reversed(strides[lead:])):
         bad |= n > 1 and s != want
         want *= n
@@ -107,7 +112,7 @@ class _Call:
         return t, _dense(t, "workspace", None, None, self.index), t.numel() * t.element_size()
 
     def run(self, fn, *args):
-        if torch.cuda.current_device() == self.index:
+        if _current_device() == self.index:
             status = fn(*args, self.raw)
         else:
             with torch.cuda.device(self.index):
