@@ -7,8 +7,8 @@
 // on the same accumulator takes the offset out again.  A group's sum is thus one of
 // exact bf16 products in fp32, and its scale is applied in fp32.
 //
-// A workgroup covers 16 rows of W and MT tiles of 16 tokens, its waves share out K and
-// meet in LDS.  Both operands go through LDS, a chunk of K at a time, requested while the
+// A workgroup covers NN tiles of 16 rows of W and MT of 16 tokens, its waves share out K
+// and meet in LDS.  Both operands go through LDS, a chunk of K at a time, requested while the
 // chunk before is worked on and read from memory along the rows: lanes that fetched their
 // matrix operands themselves, from 16 rows each, took 64 address cycles a load and met in
 // few L2 channels (rows lie a power of two apart): 20 us for 64 tokens, N = 2048, K = 4096.
@@ -28,6 +28,8 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
+constexpr int KS = 8;  // waves of a workgroup
 
 struct W4Args {
   const uint16_t *x, *scale;
@@ -66,29 +68,27 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
-// MT tiles of 16 tokens, shared out over MS waves; KS waves share out the blocks of
+// NN tiles of 16 rows of W, MT tiles of 16 tokens; the KS waves share out the blocks of
 // WORDS * 32 elements of K.  XR: rows of x kept, 16 MT, or 4 for at most four tokens,
-// which leaves room for chunks twice as long (K = 2048 is one: 7.8 -> 6 us for one token).
-template <int MT, int XR, int WORDS, int KS, int MS, bool VEC>
-__global__ __launch_bounds__(KS * MS * 64, 4) void w4_kernel(W4Args a) {
-  constexpr int NTH = KS * MS * 64, MW = MT / MS;
-  constexpr int KC = XR == 4 ? 2048 : MT == 4 ? 512 : 1024;         // K per chunk
+// which leaves room for chunks twice as long (K = 2048 is one: 7.8 -> 5.4 us for one token).
+template <int NN, int MT, int XR, int WORDS, bool VEC>
+__global__ __launch_bounds__(KS * 64, NN * MT > 2 ? 2 : 4) void w4_kernel(W4Args a) {
+  constexpr int NTH = KS * 64, KC = XR == 4 ? 2048 : 1024;          // K per chunk
   constexpr int KB = WORDS * 32, NB = KC / KB, U = NB / KS;         // per block; blocks of a chunk, of a wave
   constexpr int XROW = KC + 8, QROW = KC / 8 + 4;  // 16 bytes more: a quarter wave's rows start in different banks
-  constexpr int XQ = XR * (KC / 8) / NTH, QQ = (16 * (KC / 32) + NTH - 1) / NTH;  // a thread's 16 bytes of x and q
-  constexpr int SQ = (NB * 16 + NTH - 1) / NTH;                                     // and its scales
+  constexpr int XQ = XR * (KC / 8) / NTH, QQ = (16 * NN * (KC / 32) + NTH - 1) / NTH;  // a thread's 16 bytes of x and q
+  constexpr int NR = 16 * NN, SQ = (NB * NR + NTH - 1) / NTH;  // rows of W; a thread's scales
   __shared__ union {
     struct {
       uint16_t x[XR][XROW];
-      uint32_t q[16][QROW];
-      float scale[NB][16];
-      uint32_t minus[NB][16];  // -(16 + zero), twice
+      uint32_t q[NR][QROW];
+      float scale[NB][NR];
+      uint32_t minus[NB][NR];  // -(16 + zero), twice
     } c;
-    f32x4 red[KS][MT][64];
+    f32x4 red[KS][NN * MT][64];
   } lds;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, kq = lane >> 4;
-  const int ks = wave % KS, mt0 = wave / KS * MW;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * MT * 16;
+  const int n0 = blockIdx.x * NR, m0 = blockIdx.y * MT * 16;
   const int rows = min(a.M - m0, MT * 16), groups = a.K / a.group, blocks = a.K / KB;
   const unsigned per = a.group / KB;  // blocks per group; 1 for the groups of 32 and 64
   // the thread's share of a chunk: q and x by 16 bytes along their rows, blocks' scales and zero points
@@ -101,17 +101,17 @@ __global__ __launch_bounds__(KS * MS * 64, 4) void w4_kernel(W4Args a) {
   for (int i = 0; i < XQ; ++i) xv[i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < SQ; ++i) sv[i] = 0, zv[i] = 8;
-  const int sr = min(n0 + tid % 16, a.N - 1);
+  const int sr = min(n0 + tid % NR, a.N - 1);
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < QQ; ++i) {
       const int e = i * NTH + tid, r = e / (KC / 32), c = e % (KC / 32) * 32;
-      if (r < 16 && k0 + c < a.K)
+      if (r < NR && k0 + c < a.K)
         qv[i] = *(const u32x4 *)(a.q + (long long)min(n0 + r, a.N - 1) * (a.K / 8) + (k0 + c) / 8);
     }
 #pragma unroll
     for (int i = 0; i < SQ; ++i) {
-      const unsigned sb = (i * NTH + tid) / 16, kb = k0 / KB + sb, g = WORDS < 4 || per == 1 ? kb : kb / per;
+      const unsigned sb = (i * NTH + tid) / NR, kb = k0 / KB + sb, g = WORDS < 4 || per == 1 ? kb : kb / per;
       if (sb < NB && (int)kb < blocks) {
         sv[i] = a.scale[(long long)sr * groups + g];
         if (a.zero) zv[i] = a.zero[(long long)sr * groups + g];
@@ -123,23 +123,25 @@ __global__ __launch_bounds__(KS * MS * 64, 4) void w4_kernel(W4Args a) {
       if (r < rows && k0 + c < a.K) xv[i] = load_x<VEC>(a.x + (long long)(m0 + r) * a.x_ld + k0 + c);
     }
   };
-  f32x4 tot[MW];
+  f32x4 tot[NN][MT];
 #pragma unroll
-  for (int m = 0; m < MW; ++m) tot[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int t = 0; t < NN; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tot[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   fetch(0);
   for (int k0 = 0; k0 < a.K; k0 += KC) {
     if (k0) __syncthreads();  // the chunk before has been read
 #pragma unroll
     for (int i = 0; i < QQ; ++i) {
       const int e = i * NTH + tid, r = e / (KC / 32);
-      if (r < 16) *(u32x4 *)&lds.c.q[r][e % (KC / 32) * 4] = qv[i];
+      if (r < NR) *(u32x4 *)&lds.c.q[r][e % (KC / 32) * 4] = qv[i];
     }
 #pragma unroll
     for (int i = 0; i < SQ; ++i) {
-      const int sb = (i * NTH + tid) / 16;
+      const int sb = (i * NTH + tid) / NR;
       if (sb < NB) {
-        lds.c.scale[sb][tid % 16] = bf2f(sv[i]);
-        lds.c.minus[sb][tid % 16] = (0xC180u | (zv[i] & 15u) << 3) * 0x10001u;
+        lds.c.scale[sb][tid % NR] = bf2f(sv[i]);
+        lds.c.minus[sb][tid % NR] = (0xC180u | (zv[i] & 15u) << 3) * 0x10001u;
       }
     }
 #pragma unroll
@@ -151,65 +153,77 @@ __global__ __launch_bounds__(KS * MS * 64, 4) void w4_kernel(W4Args a) {
     if (k0 + KC < a.K) fetch(k0 + KC);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = ks * U + u;
+      const int kb = wave * U + u;
       if (k0 / KB + kb >= blocks) break;
-      const uint32_t off = lds.c.minus[kb][col];
-      const bf16x8 minus = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
-      const float sc = lds.c.scale[kb][col];
-      const uint32_t *w = &lds.c.q[col][kb * (KB / 8) + kq * WORDS];
-      uint32_t wq[WORDS];
-      if constexpr (WORDS == 4)
-        *(u32x4 *)wq = *(const u32x4 *)w;
-      else if constexpr (WORDS == 2)
-        *(uint2 *)wq = *(const uint2 *)w;
-      else
-        wq[0] = w[0];
+      bf16x8 minus[NN];
+      float sc[NN];
+      uint32_t wq[NN][WORDS];
 #pragma unroll
-      for (int m = 0; m < MW; ++m) {
+      for (int t = 0; t < NN; ++t) {
+        const uint32_t off = lds.c.minus[kb][t * 16 + col];
+        minus[t] = __builtin_bit_cast(bf16x8, u32x4{off, off, off, off});
+        sc[t] = lds.c.scale[kb][t * 16 + col];
+        const uint32_t *w = &lds.c.q[t * 16 + col][kb * (KB / 8) + kq * WORDS];
+        if constexpr (WORDS == 4)
+          *(u32x4 *)wq[t] = *(const u32x4 *)w;
+        else if constexpr (WORDS == 2)
+          *(uint2 *)wq[t] = *(const uint2 *)w;
+        else
+          wq[t][0] = w[0];
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
         // rows without a token hold anything (or another's): they reach only their own rows of the result
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 acc[NN] = {};
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[((mt0 + m) * 16 + col) % XR][kb * KB + kq * WORDS * 8 + i * 8];
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[i]), acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus, acc, 0, 0, 0);
+          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[(m * 16 + col) % XR][kb * KB + kq * WORDS * 8 + i * 8];
+#pragma unroll
+          for (int t = 0; t < NN; ++t) {
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[t][i]), acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus[t], acc[t], 0, 0, 0);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[m][i] += sc * acc[i];
+        for (int t = 0; t < NN; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tot[t][m][i] += sc[t] * acc[t][i];
       }
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int m = 0; m < MW; ++m) lds.red[ks][mt0 + m][lane] = tot[m];
-  __syncthreads();
-  // lane (n = lane & 15, rows (lane >> 4) * 4 ..) of tile m
-  for (int m = wave; m < MT; m += KS * MS) {
-    f32x4 y = lds.red[0][m][lane];
+  for (int t = 0; t < NN; ++t)
 #pragma unroll
-    for (int k = 1; k < KS; ++k) y += lds.red[k][m][lane];
+    for (int m = 0; m < MT; ++m) lds.red[wave][t * MT + m][lane] = tot[t][m];
+  __syncthreads();
+  // lane (n = lane & 15, rows (lane >> 4) * 4 ..) of a tile
+  for (int e = wave; e < NN * MT; e += KS) {
+    f32x4 y = lds.red[0][e][lane];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) y += lds.red[k][e][lane];
+    const int n = n0 + e / MT * 16 + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = m0 + m * 16 + kq * 4 + i;
-      if (row < a.M && n0 + col < a.N) store_elem(a.out, (long long)row * a.N + n0 + col, y[i], a.out_bf16);
+      const int row = m0 + e % MT * 16 + kq * 4 + i;
+      if (row < a.M && n < a.N) store_elem(a.out, (long long)row * a.N + n, y[i], a.out_bf16);
     }
   }
 }
 
-template <int MT, int XR, int WORDS>
+template <int NN, int MT, int XR, int WORDS>
 hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
-  constexpr int MS = MT == 4 ? 2 : 1, KS = 8 / MS;
-  const dim3 grid((unsigned)rec_cdiv(a.N, 16), (unsigned)rec_cdiv(a.M, MT * 16));
+  const dim3 grid((unsigned)rec_cdiv(a.N, 16 * NN), (unsigned)rec_cdiv(a.M, MT * 16));
   if (vec)
-    hipLaunchKernelGGL((w4_kernel<MT, XR, WORDS, KS, MS, true>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, WORDS, true>), grid, dim3(KS * 64), 0, st, a);
   else
-    hipLaunchKernelGGL((w4_kernel<MT, XR, WORDS, KS, MS, false>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, WORDS, false>), grid, dim3(KS * 64), 0, st, a);
   return hipGetLastError();
 }
-template <int MT, int XR = 16 * MT>
+template <int NN, int MT, int XR = 16 * MT>
 hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
-  if (a.group % 128 == 0) return launch_w<MT, XR, 4>(a, vec, st);
-  return a.group == 64 ? launch_w<MT, XR, 2>(a, vec, st) : launch_w<MT, XR, 1>(a, vec, st);
+  if (a.group % 128 == 0) return launch_w<NN, MT, XR, 4>(a, vec, st);
+  return a.group == 64 ? launch_w<NN, MT, XR, 2>(a, vec, st) : launch_w<NN, MT, XR, 1>(a, vec, st);
 }
 
 }  // namespace
@@ -244,13 +258,15 @@ hipError_t launch_w4(const void *x, const void *q, const void *scale, const void
   a.group = group;
   a.out_bf16 = out_bf16;
   const bool vec = x_ld % 8 == 0 && rec_aligned(x, 16);
-  // Tokens per workgroup: 64 read a weight once; where that leaves CUs idle, fewer tokens
-  // and more workgroups, whose weights then come from L2 (N / 16 workgroups apart, a
-  // multiple of the eight dies in the usual case).
-  const long long rows = rec_cdiv(N, 16);
-  if (M > 32 && rows * rec_cdiv(M, 64) >= 512) return launch_mt<4>(a, vec, st);
-  if (M > 16 && rows * rec_cdiv(M, 32) >= 512) return launch_mt<2>(a, vec, st);
-  return M <= 4 ? launch_mt<1, 4>(a, vec, st) : launch_mt<1>(a, vec, st);
+  // A larger tile reads x and W fewer times from L2, a smaller one gives more workgroups.
+  // Measured, us, for tiles of 16 x 16, 32 x 16, 64 x 32 (rows of W x tokens): M 16, N 2048,
+  // K 4096: 6.9, 7.9, 14.6; M 64, N 2048, K 4096: 10.2, 8.2, 14.7; M 16, N 12288, K 2048: 9.4,
+  // 7.3, 8.5; M 32: 15.5, 10.9, 9.3; M 64, N 16384, K 8192: 126, 75, 58.  So the larger one
+  // as soon as it still gives about a workgroup per CU.
+  if (M <= 4) return launch_mt<1, 1, 4>(a, vec, st);
+  if (M > 16 && rec_cdiv(N, 64) * rec_cdiv(M, 32) >= 192) return launch_mt<4, 2>(a, vec, st);
+  if (rec_cdiv(N, 32) * rec_cdiv(M, 16) >= 256) return launch_mt<2, 1>(a, vec, st);
+  return launch_mt<1, 1>(a, vec, st);
 }
 
 }  // namespace ret
