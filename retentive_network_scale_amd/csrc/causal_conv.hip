@@ -271,6 +271,42 @@ __global__ __launch_bounds__(NT) void conv_bwd_kernel(ConvArgs a) {
   }
 }
 
+// dw and dbias: the sums over the workgroups along the tokens, in a fixed order and in double.
+// A workgroup takes COLS columns of part, its threads' rows run ROWS apart, eight loads ahead.
+constexpr int COLS = 32, ROWS = 16;
+__global__ __launch_bounds__(COLS * ROWS) void conv_sum_kernel(const float *part, float *dw, float *dbias,
+                                                               long long rows, int D, int K) {
+  __shared__ double red[ROWS][COLS];
+  const int c = threadIdx.x % COLS, r0 = threadIdx.x / COLS;
+  const long long col = (long long)blockIdx.x * COLS + c, cols = (long long)D * (K + 1);
+  constexpr int U = 8;
+  double x = 0.0;
+  if (col < cols)
+    for (long long r = r0; r < rows; r += U * ROWS) {
+      float v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) v[k] = r + k * ROWS < rows ? part[(r + k * ROWS) * cols + col] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < U; ++k) x += v[k];
+    }
+  red[r0][c] = x;
+  __syncthreads();
+  if (r0 != 0 || col >= cols) return;
+#pragma unroll
+  for (int k = 1; k < ROWS; ++k) x += red[k][c];
+  const long long d = col / (K + 1);
+  const int j = (int)(col % (K + 1));
+  if (j < K)
+    dw[d * K + j] = (float)x;
+  else if (dbias)
+    dbias[d] = (float)x;
+}
+hipError_t conv_sum(const float *part, float *dw, float *dbias, long long rows, int D, int K, hipStream_t st) {
+  hipLaunchKernelGGL(conv_sum_kernel, dim3((unsigned)rec_cdiv((long long)D * (K + 1), COLS)), dim3(COLS * ROWS), 0, st,
+                     part, dw, dbias, rows, D, K);
+  return hipGetLastError();
+}
+
 template <typename T, int K, int VC>
 __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
   const int dv = a.D / VC;
@@ -485,14 +521,14 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
       const int vc = channels(qs, 2, D, 0, e);
       err = launch<FWD>(c, bf, vc, (long long)B * (K - 1) * (D / vc), st);
     }
-    if (err == hipSuccess) err = column_sum(nullptr, dw, dbias, 0, (long long)D * (K + 1), K + 1, st);
+    if (err == hipSuccess) err = conv_sum(nullptr, dw, dbias, 0, D, K, st);
     return rec_status(err);
   }
   const int vc = channels(ps, 6, D, x_ld, e);
   set_runs(a, vc, BWD_RUN);
   hipError_t err = launch<BWD>(a, bf, vc, a.main_threads, st);
   if (err != hipSuccess) return rec_status(err);
-  return rec_status(column_sum(a.part, dw, dbias, B * rec_cdiv(a.runs, WAVES), (long long)D * (K + 1), K + 1, st));
+  return rec_status(conv_sum(a.part, dw, dbias, B * rec_cdiv(a.runs, WAVES), D, K, st));
 }
 
 ret_status_t causal_conv1d_step(const void *x, const void *w, const void *bias, void *out, void *state, int B, int D,

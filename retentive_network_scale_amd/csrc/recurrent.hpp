@@ -60,13 +60,6 @@ inline ret_status_t rec_check_overlap(const RecSpan (&ins)[NI], const RecSpan (&
 }
 inline bool rec_aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// out[col] = sum over rows of part[rows][cols] (column_sum.hip), in a fixed order, in
-// double: thousands of partial sums may come together.  Columns come in groups of
-// `group`, the last of which goes to `last` (or nowhere if NULL) and the others, dense, to
-// out; group 0: all of them to out.
-hipError_t column_sum(const float *part, float *out, float *last, long long rows, long long cols, int group,
-                      hipStream_t st);
-
 // ------------------------------------------------------------------ device side
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kLog2eLow = (float)(1.4426950408889634 - (double)1.4426950408889634f);

@@ -906,16 +906,63 @@ __global__ __launch_bounds__(NT) void scan_bwd_tail_kernel(ScanArgs a) {
   }
 }
 
-// dB and dC: the sum over the group's channel tiles, in their order.
-__global__ __launch_bounds__(NT) void scan_reduce_bc_kernel(ScanArgs a, void *dB, void *dC) {
-  const long long total = (long long)a.B * a.L * a.G * 2 * a.N, id = (long long)blockIdx.x * NT + threadIdx.x;
-  if (id >= total) return;
-  const int n = id % a.N, k = id / a.N % 2;
-  const long long rg = id / (2 * a.N), r = rg / a.G;
-  float x = 0.0f;
-  if (!a.lengths || r % a.L < a.lengths[r / a.L])
-    for (int t = 0; t < a.tiles; ++t) x += a.bcpart[t * total + id];
-  store_elem(k ? dC : dB, rg * a.N + n, x, a.out_bf16);
+// The backward's last sums, over the workgroups of the main pass, in their order: dB and dC
+// over a group's channel tiles (the first bc_blocks workgroups, a thread a value), and dA,
+// dD and the bias's gradient over sequences and spans (COLS values a workgroup, ROWS threads
+// each, in double: thousands of partial sums may come together).
+constexpr int COLS = 32, ROWS = 16;
+__global__ __launch_bounds__(COLS * ROWS) void scan_reduce_kernel(ScanArgs a, void *dB, void *dC, float *dA, float *dD,
+                                                                  float *dbias, long long bc_blocks) {
+  constexpr int U = 8;
+  if (blockIdx.x < bc_blocks) {
+    const long long total = (long long)a.B * a.L * a.G * 2 * a.N, id = (long long)blockIdx.x * (COLS * ROWS) + threadIdx.x;
+    if (id >= total) return;
+    const long long rg = id / (2 * a.N), r = rg / a.G;
+    const int k = (int)(id - rg * 2 * a.N);
+    float x = 0.0f;
+    if (!a.lengths || r % a.L < a.lengths[r / a.L])
+      for (int t = 0; t < a.tiles; t += U) {
+        float v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = t + i < a.tiles ? a.bcpart[(t + i) * total + id] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) x += v[i];
+      }
+    store_elem(k < a.N ? dB : dC, rg * a.N + (k < a.N ? k : k - a.N), x, a.out_bf16);
+    return;
+  }
+  __shared__ double red[ROWS][COLS];
+  const int c = threadIdx.x % COLS, r0 = threadIdx.x / COLS, rows = a.B * a.nspan;
+  long long col = (blockIdx.x - bc_blocks) * COLS + c, cols = (long long)a.D * a.N;
+  const float *part = a.dApart;
+  float *out = dA;
+  if (col >= cols) {
+    col -= cols;
+    cols = a.D;
+    part = a.dDpart;
+    out = dD;
+    if (col >= cols) {
+      col -= cols;
+      part = a.dbpart;
+      out = dbias;
+    }
+  }
+  const bool there = col < cols && out;
+  double x = 0.0;
+  if (there)
+    for (int r = r0; r < rows; r += U * ROWS) {
+      float v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) v[k] = r + k * ROWS < rows ? part[(r + k * ROWS) * cols + col] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < U; ++k) x += v[k];
+    }
+  red[r0][c] = x;
+  __syncthreads();
+  if (r0 != 0 || !there) return;
+#pragma unroll
+  for (int k = 1; k < ROWS; ++k) x += red[k][c];
+  out[col] = (float)x;
 }
 
 __global__ __launch_bounds__(NT) void state_copy_kernel(float *dst, const float *src, long long n) {
@@ -1375,12 +1422,11 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
     return rec_status(err);
   if (lengths && (err = launch(scan_bwd_tail_kernel, rows, NT, st, a)) != hipSuccess) return rec_status(err);
   a.tiles = p.bwd_tiles;
-  hipLaunchKernelGGL(scan_reduce_bc_kernel, dim3((unsigned)rec_cdiv(rows * 2 * bc, NT)), dim3(NT), 0, st, a, dB, dC);
+  const long long bc_blocks = rec_cdiv(rows * 2 * bc, COLS * ROWS);
+  const long long cols = (long long)D * (N + 2);
+  hipLaunchKernelGGL(scan_reduce_kernel, dim3((unsigned)(bc_blocks + rec_cdiv(cols, COLS))), dim3(COLS * ROWS), 0, st, a,
+                     dB, dC, dA, dD, ddelta_bias, bc_blocks);
   if ((err = hipGetLastError()) != hipSuccess) return rec_status(err);
-  const long long parts = (long long)B * p.nspan;
-  if ((err = column_sum(a.dApart, dA, nullptr, parts, (long long)D * N, 0, st)) != hipSuccess) return rec_status(err);
-  if (dD && (err = column_sum(a.dDpart, dD, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
-  if (ddelta_bias && (err = column_sum(a.dbpart, ddelta_bias, nullptr, parts, D, 0, st)) != hipSuccess) return rec_status(err);
   return rec_status(hipSuccess);
 }
 

@@ -377,6 +377,8 @@ def test_conv_strided_rows_and_steps():
 W4_SHAPES = [  # M, N, K, group
     (1, 1, 32, 32), (1, 16, 64, 64), (2, 17, 128, 128), (16, 40, 256, 128), (17, 16, 96, 32), (33, 100, 192, 64),
     (64, 64, 384, 128), (65, 33, 512, 256), (5, 24, 1024, 512), (130, 8, 160, 32), (3, 500, 2048, 128), (1, 7, 384, 384),
+    (9, 8200, 96, 32), (16, 8200, 192, 64), (20, 4100, 256, 128), (33, 6150, 160, 32), (40, 6100, 384, 384), (64, 6150, 1152, 64),
+    (4, 40, 4224, 128),
 ]
 
 
