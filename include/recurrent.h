@@ -143,9 +143,10 @@ ret_status_t causal_conv1d_step(const void *x, const void *w, const void *bias, 
  *   x : [M, K] bf16 (row stride x_ld)        out : [M, N] bf16 or fp32, dense
  *   q : [N, K / 2] bytes, element 2 i in the low half of byte i, 2 i + 1 in the high one
  *   scale : [N, K / group] bf16     zero : [N, K / group] bytes in 0..15, or NULL for 8
- * group is 32, 64 or a multiple of 128 and divides K; q is 16-byte aligned.  The products are exact
- * (integers against bf16), sums fp32, each group's sum scaled in fp32.  The weights
- * are read once for every 64 tokens: made for M up to about that.
+ * group is 32, 64 or a multiple of 128 and divides K; q is 16-byte aligned.  The products
+ * are exact (integers against bf16), sums fp32, each group's sum scaled in fp32.  The
+ * zero points are taken out of sums of x (16 + q), so x has to be finite and below 2^118
+ * in magnitude: an infinity gives NaN.  Made for few tokens; any M is computed.
  */
 ret_status_t linear_w4(const void *x, const void *q, const void *scale, const void *zero, void *out,
                        int M, int N, int K, int group, long long x_ld, ret_dtype_t out_dtype,

@@ -82,14 +82,16 @@ __device__ __forceinline__ void store4(void *base, long long off, int n, const f
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x|.  The exponential's argument is taken to
 // base 2 in two parts, so that far negative x keep their relative accuracy; 1 + e rounds,
 // and what it lost is added to the logarithm (over s = 1 + e, which matters only where s
-// is near 1).  The hardware's exp2 and log2 are good to 1.5 half steps, near 1 too: 3
-// half steps in all, measured over e^-18 .. 20.
+// is near 1).  The hardware's exp2 and log2 are good to 2 half steps, near 1 too: 3 half
+// steps in all, measured over e^-18 .. 20.  Below -150 e is 0 in fp32 anyway: x of -inf or
+// the type's lowest value (a token that does nothing) gives 0; NaN stays NaN.
 __device__ __forceinline__ float softplus(float x) {
-  const float m = -fabsf(x), hi = m * kLog2e, lo = fmaf(m, kLog2eLow, fmaf(m, kLog2e, -hi));
+  const float a = -fabsf(x), m = a < -150.0f ? -150.0f : a;
+  const float hi = m * kLog2e, lo = fmaf(m, kLog2eLow, fmaf(m, kLog2e, -hi));
   float e = __builtin_amdgcn_exp2f(hi);
   e = fmaf(e, lo * kLn2, e);
   const float s = 1.0f + e, lost = e - (s - 1.0f);
-  return fmaxf(x, 0.0f) + fmaf(__builtin_amdgcn_logf(s), kLn2, lost);
+  return (x > 0.0f ? x : 0.0f) + fmaf(__builtin_amdgcn_logf(s), kLn2, lost);
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }

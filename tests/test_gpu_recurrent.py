@@ -184,6 +184,27 @@ def test_scan_large_time_steps_and_rates():
     _check_scan(v, True, None, out, st, "large steps")
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_scan_tokens_masked_by_their_time_step(dt):
+    """delta of -inf or the type's lowest value makes a token do nothing, forward and backward; +inf
+    and NaN reach only their own channel from their token on."""
+    v = _scan_inputs(2, 40, 68, 16, 1, dt, 19, bias=False, state=True)
+    v["delta"][0, 3:20] = float("-inf")
+    v["delta"][1, 5:9, ::2] = torch.finfo(dt).min
+    out, st = _scan_gpu(v, state_out=True)
+    _check_scan(v, True, None, out, st, "masked")
+    d_o = torch.randn(2, 40, 68, generator=_gen(190)).to(dt)
+    _check_bwd(v, d_o, None, True, None, _bwd(v, d_o, None), "masked")
+    bad = {k: None if t is None else t.clone() for k, t in v.items()}
+    bad["delta"][0, 25, 7] = float("nan")
+    bad["u"][1, 30, 66] = float("inf")
+    o2, s2 = _scan_gpu(bad, state_out=True)
+    clean = torch.ones(2, 40, 68, dtype=torch.bool)
+    clean[0, 25:, 7] = clean[1, 30:, 66] = False
+    assert torch.equal(o2.cpu()[clean], out.cpu()[clean])
+    assert not torch.isfinite(o2.cpu()[~clean]).any() and torch.isnan(s2[0, 7]).all()
+
+
 def _bwd(v, d_o, dhT, softplus=True, lengths=None, **kw):
     d = {k: _dev(t) for k, t in v.items()}
     ln = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
@@ -470,6 +491,38 @@ def test_msr_step_w4(B, dm, H, dk, dv, g, zeros, rot):
         torch.testing.assert_close(s1, s2, rtol=1e-4, atol=1e-4)
         off = (y1.double() - y2.double()).norm() / y2.double().norm()
         assert off <= 3 * 2.0 ** -8, off
+
+
+# ------------------------------------------------------------------------------ long sequences
+def test_offsets_beyond_32_bits():
+    """2^31 elements and more in one tensor: the last tokens, and their gradients, equal those of a call
+    on these tokens alone that starts from the state in front of them (computed by a call on the rest)."""
+    L, cut, d, n = (1 << 19) + 40, 1 << 19, 4096, 4
+    gen = torch.Generator(device=DEV).manual_seed(90)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV, dtype=BF)  # noqa: E731
+    u, delta, bc = r(1, L, d), r(1, L, d), r(1, L, 2, 1, n)
+    A = -2 * torch.rand(d, n, generator=gen, device=DEV)
+    w, bias = r(d, 4), r(d)
+    c, cs = rn.causal_conv1d(u, w, bias, state_out=True)
+    tail, ts = rn.causal_conv1d(u[:, cut:].contiguous(), w, bias, state_in=u[:, cut - 3:cut].contiguous(), state_out=True)
+    assert torch.equal(c[:, cut:], tail) and torch.equal(cs, ts)
+    del c
+    Bm, Cm = bc[:, :, 0], bc[:, :, 1]
+    whole, end = rn.selective_scan(u, delta, A, Bm, Cm, delta_softplus=True, state_out=True)
+    _, h = rn.selective_scan(u[:, :cut], delta[:, :cut], A, Bm[:, :cut], Cm[:, :cut], delta_softplus=True, state_out=True)
+    part, e2 = rn.selective_scan(u[:, cut:], delta[:, cut:], A, Bm[:, cut:], Cm[:, cut:], delta_softplus=True,
+                                 state_in=h, state_out=True)
+    # other segments, other orders: fp32 roundings of some 40 tokens, then bf16's
+    torch.testing.assert_close(end, e2, rtol=1e-4, atol=1e-4)
+    torch.testing.assert_close(whole[:, cut:].float(), part.float(), rtol=2 ** -7, atol=1e-3)
+    del whole
+    d_o = r(1, L, d)
+    g = rn.selective_scan_bwd(u, delta, A, Bm, Cm, d_o, delta_softplus=True)
+    t = rn.selective_scan_bwd(u[:, cut:], delta[:, cut:], A, Bm[:, cut:], Cm[:, cut:], d_o[:, cut:].contiguous(),
+                              delta_softplus=True, state_in=h)
+    for a, b in ((g.du, t.du), (g.ddelta, t.ddelta), (g.dB, t.dB), (g.dC, t.dC)):
+        off = (a[:, cut:].float() - b.float()).norm() / b.float().norm()
+        assert off <= 2 ** -8, off
 
 
 # ------------------------------------------------------------------------------ graphs, streams
