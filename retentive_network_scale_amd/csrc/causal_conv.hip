@@ -133,10 +133,11 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
       float y[VC];
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
-        float s = bias[c];
+        float s = w[0][c] * win[i][c];
 #pragma unroll
-        for (int j = 0; j < K; ++j) s += w[j][c] * win[i + j][c];
-        y[c] = a.silu ? s * sigmoid(s) : s;
+        for (int j = 1; j < K; ++j) s += w[j][c] * win[i + j][c];
+        s += bias[c];
+        y[c] = a.silu ? silu(s) : s;
       }
       if (t + i < t1) storec<T, VC>((T *)a.out + (b * a.L + t + i) * a.D + d, y);
     }
@@ -322,10 +323,11 @@ __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
   loadc<T, VC>((const T *)a.x + b * a.x_ld + d, x[K - 1]);
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
-    float s = bias[c];
+    float s = w[0][c] * x[0][c];
 #pragma unroll
-    for (int j = 0; j < K; ++j) s += w[j][c] * x[j][c];
-    y[c] = a.silu ? s * sigmoid(s) : s;
+    for (int j = 1; j < K; ++j) s += w[j][c] * x[j][c];
+    s += bias[c];
+    y[c] = a.silu ? silu(s) : s;
   }
   storec<T, VC>((T *)a.out + b * a.D + d, y);
 #pragma unroll

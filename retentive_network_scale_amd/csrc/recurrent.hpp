@@ -94,6 +94,21 @@ __device__ __forceinline__ float softplus(float x) {
   return (x > 0.0f ? x : 0.0f) + fmaf(__builtin_amdgcn_logf(s), kLn2, lost);
 }
 
+// x / (1 + e^-x) to within two roundings: the exponential's argument to base 2 in two parts
+// around its nearest whole number, the quotient with one correction.  The convolution uses
+// it, since its result may be rounded to bf16 and then drive a state in fp32: a few units
+// of 2^-24 more turn more of the values next to a rounding border into the other neighbour.
+__device__ __forceinline__ float silu(float x) {
+  const float t = __builtin_amdgcn_fmed3f(-x, -150.0f, 150.0f);
+  float hi = t * kLog2e;
+  asm("" : "+v"(hi));  // the product as rounded, also where it is subtracted from
+  const float lo = fmaf(t, kLog2eLow, fmaf(t, kLog2e, -hi)), n = rintf(hi);
+  const float d = 1.0f + ldexpf(__builtin_amdgcn_exp2f((hi - n) + lo), (int)n), r = __builtin_amdgcn_rcpf(d);
+  const float q = x * r;
+  return __builtin_amdgcn_div_fixupf(fmaf(fmaf(-q, d, x), r, q), d, x);
+}
+
+// The same within a few roundings, where the result is not rounded on the way.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
 }  // namespace ret
