@@ -531,47 +531,33 @@ __global__ __launch_bounds__(64 * PASS_WAVES, 3) void scan_pass_kernel(ScanArgs 
   }
 }
 
-// Segment states -> states entering the segments, in place; with gseg also the
-// gradients entering them from behind.  One thread per (sequence, channel, state); the
-// chain over segments is short next to its loads, which go ahead by eight.
+// Segment states -> states entering the segments, in place (blockIdx.y 0), and gradients of
+// the segments -> gradients entering them from behind (1).  One thread per (sequence,
+// channel, state); the chain over segments is short next to its loads, which go ahead by 32.
 __global__ __launch_bounds__(NT) void scan_combine_kernel(ScanArgs a) {
   const long long DN = (long long)a.D * a.N, id = (long long)blockIdx.x * NT + threadIdx.x;
   if (id >= a.B * DN) return;
-  constexpr int U = 8;
+  constexpr int U = 32;
   const long long b = id / DN, e = id % DN, d = e / a.N;
+  const bool back = blockIdx.y != 0;
   const float A2 = a.A[e] * kLog2e;
-  const float *sdt = a.sdt + b * a.nseg * a.D + d;
-  float own[U], dt[U];
-  float carry = a.h0 ? a.h0[id] : 0.0f;
-  float *S = a.seg + b * a.nseg * DN + e;
+  // from the first segment on, or from the last back
+  const long long first = b * a.nseg + (back ? a.nseg - 1 : 0), way = back ? -1 : 1;
+  const float *sdt = a.sdt + first * a.D + d;
+  float *S = (back ? a.gseg : a.seg) + first * DN + e;
+  const float *h = back ? a.dhT : a.h0;
+  float own[U], dt[U], carry = h ? h[id] : 0.0f;
   for (int s0 = 0; s0 < a.nseg; s0 += U) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int s = min(s0 + k, a.nseg - 1);
+      const long long s = way * min(s0 + k, a.nseg - 1);
       own[k] = S[s * DN];
-      dt[k] = sdt[(long long)s * a.D];
+      dt[k] = sdt[s * a.D];
     }
 #pragma unroll
     for (int k = 0; k < U; ++k)
       if (s0 + k < a.nseg) {
-        S[(s0 + k) * DN] = carry;
-        carry = __builtin_amdgcn_exp2f(A2 * dt[k]) * carry + own[k];
-      }
-  }
-  if (!a.gseg) return;
-  float *Gs = a.gseg + b * a.nseg * DN + e;
-  carry = a.dhT ? a.dhT[id] : 0.0f;
-  for (int s0 = a.nseg - 1; s0 >= 0; s0 -= U) {
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int s = max(s0 - k, 0);
-      own[k] = Gs[s * DN];
-      dt[k] = sdt[(long long)s * a.D];
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (s0 - k >= 0) {
-        Gs[(s0 - k) * DN] = carry;
+        S[way * (s0 + k) * DN] = carry;
         carry = __builtin_amdgcn_exp2f(A2 * dt[k]) * carry + own[k];
       }
   }
@@ -1211,7 +1197,9 @@ hipError_t launch_step(const ScanArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_combine(const ScanArgs &a, hipStream_t st) {
-  return launch(scan_combine_kernel, rec_cdiv((long long)a.B * a.D * a.N, NT), NT, st, a);
+  const dim3 grid((unsigned)rec_cdiv((long long)a.B * a.D * a.N, NT), a.gseg ? 2 : 1);
+  hipLaunchKernelGGL(scan_combine_kernel, grid, dim3(NT), 0, st, a);
+  return hipGetLastError();
 }
 
 ScanArgs scan_args(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
