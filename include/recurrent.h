@@ -40,7 +40,11 @@ extern "C" {
 #define RECURRENT_MAX_STATE 64             /* N of the scan */
 #define RECURRENT_MAX_TAPS 8               /* K of the convolution */
 #define RECURRENT_MAX_TOKENS (1LL << 28)   /* B * L of one call */
-#define RECURRENT_MAX_ELEMENTS (1LL << 37) /* B * D * L, B * D * N, B * D * K of one call */
+#define RECURRENT_MAX_ELEMENTS (1LL << 37) /* B * L * D, B * L * G * N of one call */
+#define RECURRENT_MAX_CHANNELS (1LL << 20) /* D */
+#define RECURRENT_MAX_STATES (1LL << 31)   /* B * D * N, B * D * K of one call */
+/* Beside them, B * G * ceil(D / G / 16) of a scan is below 2^24, and N and K of
+ * linear_w4 at most 2^26. */
 
 /*
  * The scan over L tokens.

@@ -377,7 +377,8 @@ ret_status_t check_sizes(int B, int L, int D, int K, long long x_ld, ret_dtype_t
     return rec_fail(RET_ERR_UNSUPPORTED, "K=%d outside 2..%d", K, RECURRENT_MAX_TAPS);
   if (x_ld < D) return rec_fail(RET_ERR_INVALID_ARG, "a row stride is shorter than its row");
   if (x_ld > (1LL << 31)) return rec_fail(RET_ERR_UNSUPPORTED, "a row stride above 2^31");
-  if ((long long)B * std::max(L, 1) > RECURRENT_MAX_TOKENS || (double)B * std::max(L, K) * D > RECURRENT_MAX_ELEMENTS)
+  if (D > RECURRENT_MAX_CHANNELS || (long long)B * std::max(L, 1) > RECURRENT_MAX_TOKENS ||
+      (double)B * L * D > RECURRENT_MAX_ELEMENTS || (double)B * K * D > RECURRENT_MAX_STATES)
     return rec_fail(RET_ERR_UNSUPPORTED, "too many tokens (B=%d L=%d D=%d)", B, L, D);
   return RET_OK;
 }
@@ -458,12 +459,16 @@ ret_status_t causal_conv1d(const void *x, const void *w, const void *bias, void 
   }
   const long long threads = a.state_at + (state_out ? (long long)B * (K - 1) * (D / vc) : 0);
   if (threads == 0) return rec_status(hipSuccess);
+  if (!rec_grid_ok((double)rec_cdiv(threads, NT), NT))
+    return rec_fail(RET_ERR_UNSUPPORTED, "too many tokens (B=%d L=%d D=%d)", B, L, D);
   return rec_status(launch<FWD>(a, dtype == RET_BF16, vc, threads, (hipStream_t)hip_stream));
 }
 
 size_t causal_conv1d_bwd_workspace_bytes(int B, int L, int D, int K) {
   if (B <= 0 || L <= 0 || D <= 0 || K < 2 || K > RECURRENT_MAX_TAPS) return 0;
-  if ((long long)B * L > RECURRENT_MAX_TOKENS || (double)B * L * D > RECURRENT_MAX_ELEMENTS) return 0;
+  if (D > RECURRENT_MAX_CHANNELS || (long long)B * L > RECURRENT_MAX_TOKENS ||
+      (double)B * L * D > RECURRENT_MAX_ELEMENTS)
+    return 0;
   return rec_align((size_t)bwd_parts(B, L, D) * D * (K + 1) * 4);
 }
 
@@ -530,6 +535,8 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
   }
   const int vc = channels(ps, 6, D, x_ld, e);
   set_runs(a, vc, BWD_RUN);
+  if (!rec_grid_ok((double)rec_cdiv(D / vc, 64) * rec_cdiv(a.runs, WAVES) * B, NT))
+    return rec_fail(RET_ERR_UNSUPPORTED, "too many tokens (B=%d L=%d D=%d)", B, L, D);
   hipError_t err = launch<BWD>(a, bf, vc, a.main_threads, st);
   if (err != hipSuccess) return rec_status(err);
   return rec_status(conv_sum(a.part, dw, dbias, B * rec_cdiv(a.runs, WAVES), D, K, st));

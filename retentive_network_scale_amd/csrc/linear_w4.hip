@@ -240,6 +240,7 @@ const char *w4_refusal(const void *q, const void *scale, int N, int K, int group
   *unsupported = true;
   if (group != 32 && group != 64 && group % 128) return "group must be 32, 64 or a multiple of 128";
   if (K % group) return "K must be a multiple of group";
+  if (N > 1 << 26 || K > 1 << 26) return "N or K above 2^26";
   return nullptr;
 }
 

@@ -58,6 +58,8 @@ inline ret_status_t rec_check_overlap(const RecSpan (&ins)[NI], const RecSpan (&
   }
   return RET_OK;
 }
+// Whether a launch's threads can be counted in 32 bits, as HIP requires.
+inline bool rec_grid_ok(double blocks, int threads) { return blocks * threads < 4294967296.0; }
 inline bool rec_aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 // ------------------------------------------------------------------ device side

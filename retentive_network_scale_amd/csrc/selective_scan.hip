@@ -883,12 +883,13 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
 
 // Rows behind the sequences' ends: zero gradients of u, delta and z.
 __global__ __launch_bounds__(NT) void scan_bwd_tail_kernel(ScanArgs a) {
-  const long long r = blockIdx.x, b = r / a.L;
-  if (r % a.L < min(max(a.lengths[b], 0), a.L)) return;
-  for (int d = threadIdx.x; d < a.D; d += NT) {
-    store_elem(a.du, r * a.D + d, 0.0f, a.out_bf16);
-    store_elem(a.ddelta, r * a.D + d, 0.0f, a.out_bf16);
-    if (a.dz) store_elem(a.dz, r * a.D + d, 0.0f, a.out_bf16);
+  for (long long r = blockIdx.x; r < (long long)a.B * a.L; r += gridDim.x) {
+    if (r % a.L < min(max(a.lengths[r / a.L], 0), a.L)) continue;
+    for (int d = threadIdx.x; d < a.D; d += NT) {
+      store_elem(a.du, r * a.D + d, 0.0f, a.out_bf16);
+      store_elem(a.ddelta, r * a.D + d, 0.0f, a.out_bf16);
+      if (a.dz) store_elem(a.dz, r * a.D + d, 0.0f, a.out_bf16);
+    }
   }
 }
 
@@ -901,20 +902,21 @@ __global__ __launch_bounds__(COLS * ROWS) void scan_reduce_kernel(ScanArgs a, vo
                                                                   float *dbias, long long bc_blocks) {
   constexpr int U = 8;
   if (blockIdx.x < bc_blocks) {
-    const long long total = (long long)a.B * a.L * a.G * 2 * a.N, id = (long long)blockIdx.x * (COLS * ROWS) + threadIdx.x;
-    if (id >= total) return;
-    const long long rg = id / (2 * a.N), r = rg / a.G;
-    const int k = (int)(id - rg * 2 * a.N);
-    float x = 0.0f;
-    if (!a.lengths || r % a.L < a.lengths[r / a.L])
-      for (int t = 0; t < a.tiles; t += U) {
-        float v[U];
+    const long long total = (long long)a.B * a.L * a.G * 2 * a.N, step = bc_blocks * (COLS * ROWS);
+    for (long long id = (long long)blockIdx.x * (COLS * ROWS) + threadIdx.x; id < total; id += step) {
+      const long long rg = id / (2 * a.N), r = rg / a.G;
+      const int k = (int)(id - rg * 2 * a.N);
+      float x = 0.0f;
+      if (!a.lengths || r % a.L < a.lengths[r / a.L])
+        for (int t = 0; t < a.tiles; t += U) {
+          float v[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) v[i] = t + i < a.tiles ? a.bcpart[(t + i) * total + id] : 0.0f;
+          for (int i = 0; i < U; ++i) v[i] = t + i < a.tiles ? a.bcpart[(t + i) * total + id] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < U; ++i) x += v[i];
-      }
-    store_elem(k < a.N ? dB : dC, rg * a.N + (k < a.N ? k : k - a.N), x, a.out_bf16);
+          for (int i = 0; i < U; ++i) x += v[i];
+        }
+      store_elem(k < a.N ? dB : dC, rg * a.N + (k < a.N ? k : k - a.N), x, a.out_bf16);
+    }
     return;
   }
   __shared__ double red[ROWS][COLS];
@@ -1097,12 +1099,13 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   return p;
 }
 
-// Sizes a call takes: within the header's limits, and a workgroup grid that can be launched.
+// Sizes a call takes, the header's limits.  They keep every grid below 2^32 threads: 64
+// times the waves, 256 times the workgroups of a single token, a thread a state.
 bool plan_ok(int B, int L, int D, int N, int G) {
   return B > 0 && L > 0 && D > 0 && N > 0 && G > 0 && D % G == 0 && N <= RECURRENT_MAX_STATE &&
-         (long long)B * L <= RECURRENT_MAX_TOKENS && (double)B * L * D <= RECURRENT_MAX_ELEMENTS &&
-         (double)B * D * N <= RECURRENT_MAX_ELEMENTS && (double)B * G * rec_cdiv(D / G, 16) < 2e9 &&
-         (double)B * L * G * N <= RECURRENT_MAX_ELEMENTS;
+         D <= RECURRENT_MAX_CHANNELS && (long long)B * L <= RECURRENT_MAX_TOKENS &&
+         (double)B * L * D <= RECURRENT_MAX_ELEMENTS && (double)B * L * G * N <= RECURRENT_MAX_ELEMENTS &&
+         (double)B * D * N <= RECURRENT_MAX_STATES && (double)B * G * rec_cdiv(D / G, 16) < 1 << 24;
 }
 
 ret_status_t check_sizes(int B, int L, int D, int N, int G, ret_dtype_t in_dtype, ret_dtype_t out_dtype) {
@@ -1122,7 +1125,6 @@ bool wide(const void *p, long long ld, size_t e) { return !p || (ld % 4 == 0 && 
 
 template <typename K>
 hipError_t launch(K kernel, long long blocks, int threads, hipStream_t st, const ScanArgs &a) {
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
   return hipGetLastError();
 }
@@ -1135,7 +1137,6 @@ hipError_t launch_pass(ScanArgs a, int cj, hipStream_t st) {
   a.tiles = (int)rec_cdiv(a.Dg, 16 * cj);
   // the waves do not meet: workgroups of four spread them evenly over the SIMDs, of one over the CUs
   const long long waves = (long long)a.B * a.nseg * a.G * a.tiles;
-  if (waves > 0x7fffffffLL) return hipErrorInvalidValue;
   a.waves = (int)waves;
   const int per = waves > 1024 ? PASS_WAVES : 1;
   const long long blocks = rec_cdiv(waves, per);
@@ -1408,9 +1409,11 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   if ((err = launch_pass<CHECKPOINTS>(a, bf, p.cj, st)) != hipSuccess || (err = launch_combine(a, st)) != hipSuccess ||
       (err = bf ? launch_bwd<uint16_t>(a, p, st) : launch_bwd<float>(a, p, st)) != hipSuccess)
     return rec_status(err);
-  if (lengths && (err = launch(scan_bwd_tail_kernel, rows, NT, st, a)) != hipSuccess) return rec_status(err);
+  // grids of at most 2^20 workgroups, which walk what is more
+  if (lengths && (err = launch(scan_bwd_tail_kernel, std::min(rows, 1LL << 20), NT, st, a)) != hipSuccess)
+    return rec_status(err);
   a.tiles = p.bwd_tiles;
-  const long long bc_blocks = rec_cdiv(rows * 2 * bc, COLS * ROWS);
+  const long long bc_blocks = std::min(rec_cdiv(rows * 2 * bc, COLS * ROWS), 1LL << 20);
   const long long cols = (long long)D * (N + 2);
   hipLaunchKernelGGL(scan_reduce_kernel, dim3((unsigned)(bc_blocks + rec_cdiv(cols, COLS))), dim3(COLS * ROWS), 0, st, a,
                      dB, dC, dA, dD, ddelta_bias, bc_blocks);

@@ -276,6 +276,28 @@ def test_scan_bwd_lengths(shape, lengths):
     _check_bwd(clean, d_o, dhT, True, lengths, got, "lengths")
 
 
+def test_scan_bwd_more_tokens_than_workgroups():
+    # 2^22 tokens and some, N 64: the last sums walk more values than their grid has threads, as do the rows behind
+    # the end.  The last tokens' du, dz and dB follow from the tokens behind them alone, so a short piece has them too.
+    L, n, d, piece = (1 << 22) + 999, 64, 4, 200
+    end = L - 400
+    g = torch.Generator(DEV).manual_seed(60)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    u, delta, d_o, B, C = r(1, L, d), 0.5 * r(1, L, d), r(1, L, d), r(1, L, 1, n), r(1, L, 1, n)
+    A = -1 - torch.rand(d, n, generator=g, device=DEV)
+    for shape in ((1, L, d), (1, L, d), (1, L, 1, n), (1, L, 1, n)):
+        torch.full(shape, float("nan"), device=DEV)  # what the outputs' memory may hold
+    got = rn.selective_scan_bwd(u, delta, A, B, C, d_o, delta_softplus=True,
+                                lengths=torch.tensor([end], dtype=torch.int32, device=DEV))
+    for t in (got.du, got.ddelta, got.dB, got.dC):
+        assert bool((t[:, end:] == 0).all()) and bool(torch.isfinite(t).all())
+    v = {k: t[:, end - piece:end].cpu() for k, t in dict(u=u, delta=delta, B=B, C=C, d_o=d_o).items()}
+    args = (v["u"], v["delta"], A.cpu(), v["B"], v["C"], v["d_o"])
+    want, mags = ref.scan_bwd(*args, softplus_on=True), ref.scan_bwd(*args, softplus_on=True, absolute=True)
+    for name in ("du", "dB"):
+        assert_near(getattr(got, name)[:, end - piece:end], want[name], mags[name], 12 * piece + 4 * n + 512 + d, name)
+
+
 def test_scan_repeats_to_the_bit():
     v = _scan_inputs(2, 300, 192, 16, 1, BF, 28, state=True)
     d_o = torch.randn(2, 300, 192, generator=_gen(29)).to(BF)

@@ -48,6 +48,10 @@ def _scan(fn="selective_scan", **kw):
     (dict(out=P(1, 100)), INVALID), (dict(hT=P(2)), INVALID), (dict(hT=P(10, 64)), INVALID), (dict(out=P(10)), INVALID),
     (dict(ws=P(4)), INVALID), (dict(ws=P(9)), INVALID), (dict(ws=P(10)), INVALID), (dict(lengths=P(9)), INVALID),
     (dict(bt=1 << 20, L=1 << 10), UNSUPPORTED), (dict(bt=1 << 20, L=1, d=1 << 20, g=1, uld=1 << 20, dld=1 << 20), UNSUPPORTED),
+    # grids of 2^32 threads and more: too many channels, states, or groups of few channels
+    (dict(bt=1, L=1, d=1 << 21, g=1, uld=1 << 21, dld=1 << 21, zld=1 << 21), UNSUPPORTED),
+    (dict(bt=1 << 16, L=1, d=1 << 12, g=1, uld=1 << 12, dld=1 << 12, zld=1 << 12), UNSUPPORTED),
+    (dict(bt=1 << 18, L=1, d=64, n=1, g=64, bld=64, cld=64), UNSUPPORTED),
 ])
 def test_scan_refuses(kw, code):
     assert _scan(**kw) == code
@@ -81,6 +85,7 @@ def _bwd(**kw):
     (dict(dd=P(12, 64)), INVALID), (dict(dh0=P(11)), INVALID), (dict(dA=P(3)), INVALID), (dict(dC=P(15)), INVALID),
     (dict(ws=P(9)), INVALID), (dict(dD=P(17, 2)), INVALID), (dict(dB=P(15, 1)), INVALID), (dict(g=5), INVALID),
     (dict(n=80), UNSUPPORTED), (dict(cld=16), INVALID), (dict(ind=3), INVALID), (dict(L=0, dA=None), INVALID),
+    (dict(bt=1 << 18, L=1, d=64, n=1, g=64, bld=64, cld=64), UNSUPPORTED),
 ])
 def test_scan_bwd_refuses(kw, code):
     assert _bwd(**kw) == code
@@ -97,6 +102,7 @@ def _step(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(h=None), INVALID), (dict(out=None), INVALID), (dict(h=P(1)), INVALID), (dict(out=P(10)), INVALID),
     (dict(h=P(10, 2)), INVALID), (dict(n=100), UNSUPPORTED), (dict(bt=-1), INVALID), (dict(zld=5), INVALID),
+    (dict(bt=1 << 18, n=1, g=64, bld=64, cld=64), UNSUPPORTED),
 ])
 def test_scan_step_refuses(kw, code):
     assert _step(**kw) == code
@@ -120,6 +126,7 @@ def _conv_bwd(**kw):
     (dict(bt=0), INVALID), (dict(L=-1), INVALID), (dict(d=0), INVALID), (dict(k=0), INVALID), (dict(k=1), UNSUPPORTED),
     (dict(k=9), UNSUPPORTED), (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(xld=60), INVALID),
     (dict(dt=2), INVALID), (dict(x=P(1, 1)), INVALID), (dict(xld=1 << 33), UNSUPPORTED),
+    (dict(d=1 << 21, xld=1 << 21), UNSUPPORTED), (dict(bt=1 << 20, L=1, d=1 << 10, xld=1 << 10), UNSUPPORTED),
 ])
 def test_conv_refuses(kw, code):
     assert _conv(**kw) == code
@@ -132,6 +139,9 @@ def test_conv_refuses_overlaps_and_workspaces():
     for kw in (dict(dx=P(4)), dict(dw=P(2)), dict(ds0=P(6)), dict(dw=None), dict(dx=None), dict(ws=P(4)), dict(dw=P(8, 2))):
         assert _conv_bwd(**kw) == INVALID, kw
     assert _conv_bwd(ws=None) == WORKSPACE == _conv_bwd(wb=64)
+    # 2^24 workgroups of 256 threads
+    assert _conv_bwd(bt=1 << 24, L=1, d=1, xld=1, x=P(1, 0), ws=P(200), wb=1 << 33, dx=P(100), d_o=P(120), s0=None, dsT=None,
+                     ds0=None) == UNSUPPORTED
     lib = rn.lib()
     assert lib.causal_conv1d_bwd_workspace_bytes(2, 50, 64, 4) > 0
     assert lib.causal_conv1d_bwd_workspace_bytes(2, 0, 64, 4) == 0 == lib.causal_conv1d_bwd_workspace_bytes(2, 50, 64, 9)
@@ -150,7 +160,7 @@ def _w4(**kw):
     (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(g=0), INVALID), (dict(g=16), UNSUPPORTED), (dict(g=96), UNSUPPORTED),
     (dict(k=192, xld=192), UNSUPPORTED), (dict(q=P(2, 4)), INVALID), (dict(s=P(3, 1)), INVALID), (dict(xld=255), INVALID),
     (dict(out=P(1)), INVALID), (dict(out=P(2)), INVALID), (dict(out=P(4)), INVALID), (dict(od=5), INVALID),
-    (dict(m=1 << 30), UNSUPPORTED),
+    (dict(m=1 << 30), UNSUPPORTED), (dict(n=(1 << 26) + 1), UNSUPPORTED), (dict(k=1 << 27, xld=1 << 27), UNSUPPORTED),
 ])
 def test_w4_refuses(kw, code):
     assert _w4(**kw) == code
