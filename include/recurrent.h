@@ -51,7 +51,9 @@ extern "C" {
  *   u, delta, z : [B, L, D] in_dtype (z NULL: no gate)  row strides u_ld, delta_ld, z_ld
  *   Bm, Cm      : [B, L, G, N] in_dtype, row strides b_ld, c_ld; channel d reads group
  *                 d / (D / G); G divides D
- *   A           : [D, N] fp32      D_skip, delta_bias : [D] fp32 or NULL
+ *   A           : [D, N] fp32, meant to be at most 0 (where it is not, the products of
+ *                 exp(dt A) along the call have to stay finite); -inf decays at once
+ *   D_skip, delta_bias : [D] fp32 or NULL
  *   out         : [B, L, D] out_dtype, dense
  *   state_in    : [B, D, N] fp32 state before token 0, or NULL for zeros
  *   state_out   : [B, D, N] fp32 state after the last token, or NULL; may be state_in

@@ -10,9 +10,11 @@
 // LDS, from where all four rows read them back.  The loads of the next tile are in flight
 // meanwhile.
 //
-// What bounds it: the exponential (a quarter-rate instruction) and four fp32 operations per
-// token, channel and state, 8 issue slots; N = 16 of them and some 50 slots of softplus,
-// gate and conversions stand against 8 bytes of a bf16 token and channel.
+// What bounds it: the vector unit.  Per token, channel and state the exponential (two issue
+// slots by the counters), its argument, the decay and the product with C, 5 slots; N = 16
+// of them and some 30 to 50 slots of softplus, gate and conversions stand against 8 bytes
+// of a bf16 token and channel, and the chip has 39e12 lanes' slots a second against 5e12
+// bytes.  So dt u B is left to the matrix cores (quad_outer).
 //
 // Long sequences are cut into segments, so that few channels still fill the chip: the
 // decay of a state over a segment is exp(A sum dt), so the states entering the
@@ -146,6 +148,13 @@ __device__ __forceinline__ void advance(float (&h)[NS], const float (&e)[NS], fl
 #pragma unroll
     for (int i = 0; i < NS; ++i) h[i] = e[i] * h[i] + dtu * Bv[i];
   }
+}
+
+// A to base 2, kept finite: a rate of the lowest value or -inf still decays at once, and a
+// time step of 0 (a masked token, one behind the end) still leaves the state as it is.
+__device__ __forceinline__ float rate2(float A) {
+  const float r = A * kLog2e;
+  return r < -3e38f ? -3e38f : r;
 }
 
 // NS states of a lane from n0 on.  VEC: N and n0 are multiples of four, p is aligned.
@@ -346,7 +355,9 @@ __device__ __forceinline__ void load_channels(const float *p, int n, float (&r)[
 
 enum { OUTPUT, STATES, CHECKPOINTS };
 
-// One pass over a segment.
+// One pass over a segment.  Bound by the vector unit: at B 1, L 32768, D 2048, N 16, bf16
+// OUTPUT takes 283 us (537 MB; busy 82 %), STATES 214 us (70 to 78 %), and CHECKPOINTS 178 us
+// at B 2, L 4096, D 4096.
 //   OUTPUT: from the state entering the segment, the gated outputs; the last segment
 //     writes the final state.
 //   STATES: from zero, the segment's own final state and its sum of dt.
@@ -396,7 +407,7 @@ __global__ __launch_bounds__(64 * PASS_WAVES, 3) void scan_pass_kernel(ScanArgs 
     sum[j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      A2[j][i] *= kLog2e;
+      A2[j][i] = rate2(A2[j][i]);
       h[j][i] = 0.0f;
       gs[j][i] = 0.0f;
       pr[j][i] = 1.0f;
@@ -540,7 +551,7 @@ __global__ __launch_bounds__(NT) void scan_combine_kernel(ScanArgs a) {
   constexpr int U = 32;
   const long long b = id / DN, e = id % DN, d = e / a.N;
   const bool back = blockIdx.y != 0;
-  const float A2 = a.A[e] * kLog2e;
+  const float A2 = rate2(a.A[e]);
   // from the first segment on, or from the last back
   const long long first = b * a.nseg + (back ? a.nseg - 1 : 0), way = back ? -1 : 1;
   const float *sdt = a.sdt + first * a.D + d;
@@ -615,7 +626,8 @@ __device__ __forceinline__ void channel_sums(const float (&pB)[NS], const float 
 // registers; then the gradient of the state runs against time, computing the decays once
 // more (keeping them too took the registers that hold the next checkpoint's loads).  The
 // waves of a workgroup work on neighbouring channels and meet once per tile, to add up
-// their sums for dB and dC.
+// their sums for dB and dC.  Bound by the vector unit (busy 81 %): 465 us at B 2, L 4096,
+// D 4096, N 16, bf16; with the decays kept in registers 580 became 760 us.
 template <typename T, int NS, bool VEC>
 __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_kernel(ScanArgs a) {
   constexpr int NP = 4 * NS, CJ = bwd_cj(NS), CW = 16 * CJ, SUB = bwd_sub(NS);
@@ -659,7 +671,7 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
     load_state<NS, VEC>(a.gseg + (((long long)w.b * a.nseg + end) * a.D + d + j) * a.N, a.N, n0, ok, carry[j]);
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      A2[j][i] *= kLog2e;
+      A2[j][i] = rate2(A2[j][i]);
       dA[j][i] = 0.0f;
     }
   }
@@ -967,7 +979,7 @@ hipError_t state_copy(float *dst, const float *src, long long n, hipStream_t st)
 constexpr int STEP_CH = 64;  // channels of a workgroup's four waves
 
 // One token: a wave's lanes as in the passes above with one channel each; bound by reading
-// and writing the states once.
+// and writing the states once: 15.5 us for B 128, D 4096, N 16, 75 MB, 4.9 TB/s.
 // SQ sequences share their channels' A and have their loads in flight together.
 template <typename T, int NS, int SQ, bool VEC>
 __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
@@ -1002,7 +1014,7 @@ __global__ __launch_bounds__(NT) void scan_step_kernel(ScanArgs a) {
   load_state<NS, VEC>(a.A + d * a.N, a.N, n0, ok, A);
   const float bias = ok && a.bias ? a.bias[d] : 0.0f, skip = ok && a.Dskip ? a.Dskip[d] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < NS; ++i) A[i] *= kLog2e;
+  for (int i = 0; i < NS; ++i) A[i] = rate2(A[i]);
 #pragma unroll
   for (int q = 0; q < SQ; ++q) {
     const float dt = a.softplus ? softplus(x[q] + bias) : x[q] + bias, dtu = dt * u[q];

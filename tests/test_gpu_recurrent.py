@@ -184,6 +184,28 @@ def test_scan_large_time_steps_and_rates():
     _check_scan(v, True, None, out, st, "large steps")
 
 
+@pytest.mark.parametrize("L", [40, 300])
+def test_scan_rates_of_the_lowest_value(L):
+    """Such a state forgets at every token that has a time step, and no other: tokens of no time step leave it."""
+    v = _scan_inputs(2, L, 64, 8, 1, F32, 61, bias=False, state=True)
+    v["A"][:, 1] = torch.finfo(F32).min
+    v["A"][:, 2] = -3e38
+    lengths = [L, L - 23]
+    d_o = torch.randn(2, L, 64, generator=_gen(62))
+    _check_bwd(v, d_o, None, True, lengths, _bwd(v, d_o, None, lengths=lengths), "lowest")
+    v["delta"][0, 5:9] = v["delta"][1, 3:40:2] = float("-inf")
+    out, st = _scan_gpu(v, lengths=lengths, state_out=True, out=torch.zeros(2, L, 64, device=DEV))
+    _check_scan(v, True, lengths, out, st, "lowest, masked")
+    state = _dev(v["h0"]).clone()
+    rn.selective_scan_step(*(_dev(t[:, 5]) for t in (v["u"], v["delta"])), _dev(v["A"]), *(_dev(v[k][:, 5]) for k in "BC"),
+                           state, delta_softplus=True)
+    assert torch.equal(state[0], _dev(v["h0"])[0]) and torch.equal(state[1], _dev(v["h0"])[1])
+    v = _scan_inputs(2, L, 64, 8, 1, F32, 63, state=True)
+    v["A"][:, 1] = float("-inf")
+    out, st = _scan_gpu(v, lengths=lengths, state_out=True, out=torch.zeros(2, L, 64, device=DEV))
+    _check_scan(v, True, lengths, out, st, "-inf")
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_scan_tokens_masked_by_their_time_step(dt):
     """delta of -inf or the type's lowest value makes a token do nothing, forward and backward; +inf
@@ -648,6 +670,53 @@ def test_calls_on_another_stream():
     got = [rn.selective_scan(*args, **kw, stream=side)[0] for _ in range(4)]
     side.synchronize()
     assert all(torch.equal(g, want) for g in got)
+
+
+def test_two_calls_at_once():
+    """Calls of one kind on two streams, each with its own workspace, while both run."""
+    v = {k: _dev(t) for k, t in _scan_inputs(1, 3000, 192, 16, 1, BF, 71).items()}
+    d_o = torch.randn(1, 3000, 192, generator=_gen(72)).to(BF).to(DEV)
+    q, s = rn.pack_w4(torch.randint(0, 16, (256, 192), generator=_gen(73))).to(DEV), torch.ones(256, 3, dtype=BF, device=DEV)
+
+    def both(u, stream):
+        kw = dict(D=v["D"], z=v["z"], delta_bias=v["bias"], delta_softplus=True, stream=stream)
+        o, st = rn.selective_scan(u, v["delta"], v["A"], v["B"], v["C"], state_out=True, **kw)
+        g = rn.selective_scan_bwd(u, v["delta"], v["A"], v["B"], v["C"], d_o, **kw)
+        h = rn.causal_conv1d_bwd(v["u"], v["w"], d_o, stream=stream)
+        return [o, st, rn.linear_w4(u[0], q, s, stream=stream), *(t for t in (*g, *h) if t is not None)]
+
+    v["w"] = torch.randn(192, 4, generator=_gen(74)).to(BF).to(DEV)
+    us = [v["u"], (2 * v["u"]).contiguous()]
+    want = [both(u, None) for u in us]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[both(u, stream) for u, stream in zip(us, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, w in zip(pair, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_calls_without_tokens(dt):
+    """L = 0: the state passes through, sums over no tokens are zero."""
+    v = {k: _dev(t) for k, t in _scan_inputs(2, 1, 68, 5, 2, dt, 75, state=True).items()}
+    none = lambda t: t[:, :0]  # noqa: E731
+    args = [none(v["u"]), none(v["delta"]), v["A"], none(v["B"]), none(v["C"])]
+    out, st = rn.selective_scan(*args, z=none(v["z"]), state_in=v["h0"], state_out=True)
+    assert out.shape == (2, 0, 68) and torch.equal(st, v["h0"])
+    assert (rn.selective_scan(*args, state_out=True)[1] == 0).all()
+    dh = torch.randn(2, 68, 5, device=DEV)
+    g = rn.selective_scan_bwd(*args, none(v["u"]), D=v["D"], delta_bias=v["bias"], state_in=v["h0"], d_state_out=dh)
+    assert torch.equal(g.d_state_in, dh) and not any(bool(t.any()) for t in (g.dA, g.dD, g.ddelta_bias))
+    g = rn.selective_scan_bwd(*args, none(v["u"]), state_in=v["h0"])
+    assert not g.d_state_in.any()
+    w, s0 = torch.randn(68, 4, device=DEV).to(dt), torch.randn(2, 3, 68, device=DEV).to(dt)
+    out, st = rn.causal_conv1d(none(v["u"]), w, state_in=s0, state_out=True)
+    assert out.shape == (2, 0, 68) and torch.equal(st, s0)
+    assert not rn.causal_conv1d(none(v["u"]), w, state_out=True)[1].any()
+    g = rn.causal_conv1d_bwd(none(v["u"]), w, none(v["u"]), bias=w[:, 0].contiguous(), state_in=s0, d_state_out=s0)
+    assert torch.equal(g.d_state_in, s0) and not g.dw.any() and not g.dbias.any()
 
 
 def test_layer_prompt_then_tokens():
