@@ -1051,7 +1051,10 @@ struct ScanPlan {
 // How a call is cut.  Waves of 16 wide_cj channels share a token's LDS reads and sums
 // among 16 elements per lane, waves of 16 channels are up to four times as many.  A sequence is
 // cut into segments only where its channels give less than a wave per SIMD (1024), since
-// that computes every exponential twice.
+// that computes every exponential twice, and from 257 tokens on, since it takes three
+// launches.  Uncut and cut, us: 512 waves, N 16: L 100 22 and 29, L 333 50 and 52, L 777 107
+// and 81, L 4096 527 and 256; 256 waves: L 100 24 and 30, L 333 48 and 34; 512 waves, N 64:
+// L 100 37 and 84, L 333 105 and 105, L 777 232 and 182.
 ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   ScanPlan p;
   const int NS = state_regs(N), SUB = bwd_sub(NS), Dg = D / G;
@@ -1077,7 +1080,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.bwd_waves = p.bwd_tiles = 0;
     p.cj = ww >= 1024 ? wide : 1;
     long long nseg = 1;
-    if (w16 < 1024 && most > 1) {
+    if (w16 < 1024 && L > 256) {
       p.cj = ww * most >= 1024 ? wide : 1;
       nseg = std::min(most, rec_cdiv(8192, p.cj == 1 ? w16 : ww));
     }
