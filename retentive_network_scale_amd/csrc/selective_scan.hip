@@ -355,6 +355,14 @@ __device__ __forceinline__ void load_channels(const float *p, int n, float (&r)[
 
 enum { OUTPUT, STATES, CHECKPOINTS };
 
+// A wave's part of LDS in a pass.
+template <int NS, int CJ, int MODE>
+struct PassLds {
+  float dt[TT][16 * CJ], du[TT][16 * CJ];  // dt, dt u; OUTPUT: y replaces dt u
+  float dy[MODE == CHECKPOINTS ? TT : 1][16 * CJ];
+  float B[TT][4 * NS], C[MODE == STATES ? 1 : TT][4 * NS];
+};
+
 // One pass over a segment.  Bound by the vector unit: at B 1, L 32768, D 2048, N 16, bf16
 // OUTPUT takes 283 us (537 MB; busy 82 %), STATES 214 us (70 to 78 %), and CHECKPOINTS 178 us
 // at B 2, L 4096, D 4096.
@@ -365,14 +373,10 @@ enum { OUTPUT, STATES, CHECKPOINTS };
 //     sub-tile, and the gradient that the segment's own outputs send to the state in
 //     front of it, sum_t exp(A sum dt) C_t dy_t.
 template <typename T, int NS, int CJ, int MODE, bool VEC>
-__global__ __launch_bounds__(64 * PASS_WAVES, 3) void scan_pass_kernel(ScanArgs a) {
+__global__ __launch_bounds__(64 * PASS_WAVES, MODE == CHECKPOINTS && NS * CJ >= 16 ? 2 : 3) void scan_pass_kernel(ScanArgs a) {
   constexpr int NP = 4 * NS, CW = 16 * CJ, SUB = bwd_sub(NS);
-  struct WaveLds {
-    float dt[TT][CW], du[TT][CW];  // dt, dt u; OUTPUT: y replaces dt u
-    float dy[MODE == CHECKPOINTS ? TT : 1][CW];
-    float B[TT][NP], C[MODE == STATES ? 1 : TT][NP];
-  };
-  __shared__ __align__(16) WaveLds lds[PASS_WAVES];
+  extern __shared__ __align__(16) char shared[];
+  PassLds<NS, CJ, MODE> *lds = (PassLds<NS, CJ, MODE> *)shared;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), id = blockIdx.x * (blockDim.x >> 6) + wave;
   if (id >= a.waves) return;
   float(*const dts)[CW] = lds[wave].dt, (*const dus)[CW] = lds[wave].du, (*const dys)[CW] = lds[wave].dy;
@@ -458,7 +462,13 @@ __global__ __launch_bounds__(64 * PASS_WAVES, 3) void scan_pass_kernel(ScanArgs 
     if constexpr (MODE != STATES) cn.put(&Cs[0][0], a, w, t0, lane);
     fetch(t0 + TT);
     wave_sync();
-    const int nt = min(TT, w.t_hi - t0);
+    // Unrolled over all of the tile (tokens behind the end have no time step and leave the state),
+    // so that the reads of later tokens go ahead of the chain: uncut, 1024 waves, N 16, 4096
+    // tokens: 518 -> 443 us.  Not with two states a lane (575 -> 623 us) and for
+    // checkpoints, which would spill.
+    constexpr int AHEAD = MODE == CHECKPOINTS || NS == 2 ? 1 : 4;
+    const int nt = AHEAD == 4 ? TT : min(TT, w.t_hi - t0);
+#pragma unroll AHEAD
     for (int t4 = 0; t4 < nt; t4 += 4) {
       if constexpr (MODE == CHECKPOINTS) {
         if (t4 % SUB == 0) {
@@ -1053,8 +1063,7 @@ struct ScanPlan {
 // cut into segments only where its channels give less than a wave per SIMD (1024), since
 // that computes every exponential twice, and from 257 tokens on, since it takes three
 // launches.  Uncut and cut, us: 512 waves, N 16: L 100 22 and 29, L 333 50 and 52, L 777 107
-// and 81, L 4096 527 and 256; 256 waves: L 100 24 and 30, L 333 48 and 34; 512 waves, N 64:
-// L 100 37 and 84, L 333 105 and 105, L 777 232 and 182.
+// and 81, L 4096 527 and 256; 256 waves: L 100 24 and 30, L 333 48 and 34.
 ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   ScanPlan p;
   const int NS = state_regs(N), SUB = bwd_sub(NS), Dg = D / G;
@@ -1139,25 +1148,30 @@ ret_status_t check_sizes(int B, int L, int D, int N, int G, ret_dtype_t in_dtype
 bool wide(const void *p, long long ld, size_t e) { return !p || (ld % 4 == 0 && rec_aligned(p, 4 * e)); }
 
 template <typename K>
-hipError_t launch(K kernel, long long blocks, int threads, hipStream_t st, const ScanArgs &a) {
-  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
+hipError_t launch(K kernel, long long blocks, int threads, hipStream_t st, const ScanArgs &a, size_t lds = 0) {
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(threads), lds, st, a);
   return hipGetLastError();
 }
 
 // Where rows or states cannot be accessed by fours, one kernel per type and NS will do:
 // the narrow one.
-template <typename T, int NS, int MODE>
-hipError_t launch_pass(ScanArgs a, int cj, hipStream_t st) {
-  if (!a.vec) cj = 1;
-  a.tiles = (int)rec_cdiv(a.Dg, 16 * cj);
-  // the waves do not meet: workgroups of four spread them evenly over the SIMDs, of one over the CUs
+template <typename T, int NS, int CJ, int MODE, bool VEC>
+hipError_t launch_pass_kernel(ScanArgs a, hipStream_t st) {
+  a.tiles = (int)rec_cdiv(a.Dg, 16 * CJ);
+  // the waves do not meet: workgroups of four spread them evenly over the SIMDs, of one over the
+  // CUs (each with the LDS of its waves: with that of four, three fitted a CU at N 64, and
+  // 1024 waves took two turns, 2885 us instead of 1080 for 4096 tokens)
   const long long waves = (long long)a.B * a.nseg * a.G * a.tiles;
   a.waves = (int)waves;
   const int per = waves > 1024 ? PASS_WAVES : 1;
-  const long long blocks = rec_cdiv(waves, per);
-  if (!a.vec) return launch(scan_pass_kernel<T, NS, 1, MODE, false>, blocks, 64 * per, st, a);
-  return cj == 1 ? launch(scan_pass_kernel<T, NS, 1, MODE, true>, blocks, 64 * per, st, a)
-                 : launch(scan_pass_kernel<T, NS, wide_cj(NS), MODE, true>, blocks, 64 * per, st, a);
+  return launch(scan_pass_kernel<T, NS, CJ, MODE, VEC>, rec_cdiv(waves, per), 64 * per, st, a,
+                per * sizeof(PassLds<NS, CJ, MODE>));
+}
+template <typename T, int NS, int MODE>
+hipError_t launch_pass(const ScanArgs &a, int cj, hipStream_t st) {
+  if (!a.vec) return launch_pass_kernel<T, NS, 1, MODE, false>(a, st);
+  return cj == 1 ? launch_pass_kernel<T, NS, 1, MODE, true>(a, st)
+                 : launch_pass_kernel<T, NS, wide_cj(NS), MODE, true>(a, st);
 }
 template <typename T, int MODE>
 hipError_t launch_pass(const ScanArgs &a, int cj, hipStream_t st) {
