@@ -1059,7 +1059,10 @@ struct ScanPlan {
 };
 
 // How a call is cut.  Waves of 16 wide_cj channels share a token's LDS reads and sums
-// among 16 elements per lane, waves of 16 channels are up to four times as many.  A sequence is
+// among up to 16 elements per lane; waves of 16 channels are more.  The wide ones are taken
+// where they still give three waves per SIMD (3072): 24 sequences of 2048 tokens, D 2048, N 16
+// (1536 wide waves) 581 us with them and 459 without, 32 of them 575 and 564, 48 801 and 813; in
+// segments, one sequence of 1500 tokens 52 and 43.  A sequence is
 // cut into segments only where its channels give less than a wave per SIMD (1024), since
 // that computes every exponential twice, and from 257 tokens on, since it takes three
 // launches.  Uncut and cut, us: 512 waves, N 16: L 100 22 and 29, L 333 50 and 52, L 777 107
@@ -1079,7 +1082,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     const long long spans = std::min(rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves), rec_cdiv(L, 2 * TT));
     p.span_len = (int)(rec_cdiv(rec_cdiv(L, spans), TT) * TT);
     p.nspan = (int)rec_cdiv(L, p.span_len);
-    p.cj = ww * rec_cdiv(L, 2 * TT) >= 1024 ? wide : 1;
+    p.cj = ww * rec_cdiv(L, 2 * TT) >= 3072 ? wide : 1;
     const long long cut = std::min<long long>(std::max<long long>(4096 / ((p.cj == 1 ? w16 : ww) * p.nspan), 1),
                                               rec_cdiv(p.span_len, 2 * TT));
     p.seg_len = (int)(rec_cdiv(rec_cdiv(p.span_len, cut), TT) * TT);
@@ -1087,10 +1090,10 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.nseg = p.nspan * p.span;
   } else {
     p.bwd_waves = p.bwd_tiles = 0;
-    p.cj = ww >= 1024 ? wide : 1;
+    p.cj = ww >= 3072 ? wide : 1;
     long long nseg = 1;
     if (w16 < 1024 && L > 256) {
-      p.cj = ww * most >= 1024 ? wide : 1;
+      p.cj = ww * most >= 3072 ? wide : 1;
       nseg = std::min(most, rec_cdiv(8192, p.cj == 1 ? w16 : ww));
     }
     p.seg_len = p.span_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
