@@ -56,7 +56,7 @@ struct ScanArgs {
 };
 
 // Channels per lane of a pass where there are channels enough: up to 16 elements per lane
-// share what a token costs beside them.  Four channels instead of two were no faster for
+// share what a token costs beside them (scan_plan says where).  Four channels instead of two were no faster for
 // outputs and slower for checkpoints (223 against 179 us at B 2, L 4096, D 4096, N 16), where
 // they leave two waves per SIMD.
 constexpr int wide_cj(int NS) { return NS <= 8 ? 2 : 1; }
@@ -364,7 +364,7 @@ struct PassLds {
 };
 
 // One pass over a segment.  Bound by the vector unit: at B 1, L 32768, D 2048, N 16, bf16
-// OUTPUT takes 283 us (537 MB; busy 82 %), STATES 214 us (70 to 78 %), and CHECKPOINTS 178 us
+// OUTPUT takes 286 us (537 MB; busy 93 %), STATES 218 us (88 %), and CHECKPOINTS 173 us (87 %)
 // at B 2, L 4096, D 4096.
 //   OUTPUT: from the state entering the segment, the gated outputs; the last segment
 //     writes the final state.
@@ -555,6 +555,7 @@ __global__ __launch_bounds__(64 * PASS_WAVES, MODE == CHECKPOINTS && NS * CJ >= 
 // Segment states -> states entering the segments, in place (blockIdx.y 0), and gradients of
 // the segments -> gradients entering them from behind (1).  One thread per (sequence,
 // channel, state); the chain over segments is short next to its loads, which go ahead by 32.
+// Bound by their latency: 4 to 16 us (128 segments of 32768 states).
 __global__ __launch_bounds__(NT) void scan_combine_kernel(ScanArgs a) {
   const long long DN = (long long)a.D * a.N, id = (long long)blockIdx.x * NT + threadIdx.x;
   if (id >= a.B * DN) return;
@@ -636,7 +637,7 @@ __device__ __forceinline__ void channel_sums(const float (&pB)[NS], const float 
 // registers; then the gradient of the state runs against time, computing the decays once
 // more (keeping them too took the registers that hold the next checkpoint's loads).  The
 // waves of a workgroup work on neighbouring channels and meet once per tile, to add up
-// their sums for dB and dC.  Bound by the vector unit (busy 81 %): 465 us at B 2, L 4096,
+// their sums for dB and dC.  Bound by the vector unit (busy 82 %): 460 us at B 2, L 4096,
 // D 4096, N 16, bf16; with the decays kept in registers 580 became 760 us.
 template <typename T, int NS, bool VEC>
 __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_kernel(ScanArgs a) {
