@@ -66,6 +66,7 @@ constexpr int wide_cj(int NS) { return NS <= 8 ? 2 : 1; }
 constexpr int bwd_cj(int NS) { return NS >= 8 ? 1 : 2; }
 constexpr int bwd_sub(int NS) { return std::min(TT, 64 / (NS * bwd_cj(NS))); }
 constexpr int BWD_WAVES = 4, PASS_WAVES = 4;
+constexpr int SIMDS = 1024;  // of the chip
 
 // What a workgroup works on: a segment, or a span of them.
 struct Where {
@@ -1061,7 +1062,7 @@ struct ScanPlan {
 
 // How a call is cut.  Waves of 16 wide_cj channels share a token's LDS reads and sums
 // among up to 16 elements per lane; waves of 16 channels are more.  The wide ones are taken
-// where they still give three waves per SIMD (3072): 24 sequences of 2048 tokens, D 2048, N 16
+// where they still give three waves per SIMD: 24 sequences of 2048 tokens, D 2048, N 16
 // (1536 wide waves) 581 us with them and 459 without, 32 of them 575 and 564, 48 801 and 813; in
 // segments, one sequence of 1500 tokens 52 and 43.  A sequence is
 // cut into segments only where its channels give less than a wave per SIMD (1024), since
@@ -1083,7 +1084,7 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     const long long spans = std::min(rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves), rec_cdiv(L, 2 * TT));
     p.span_len = (int)(rec_cdiv(rec_cdiv(L, spans), TT) * TT);
     p.nspan = (int)rec_cdiv(L, p.span_len);
-    p.cj = ww * rec_cdiv(L, 2 * TT) >= 3072 ? wide : 1;
+    p.cj = ww * rec_cdiv(L, 2 * TT) >= 3 * SIMDS ? wide : 1;
     const long long cut = std::min<long long>(std::max<long long>(4096 / ((p.cj == 1 ? w16 : ww) * p.nspan), 1),
                                               rec_cdiv(p.span_len, 2 * TT));
     p.seg_len = (int)(rec_cdiv(rec_cdiv(p.span_len, cut), TT) * TT);
@@ -1091,10 +1092,10 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.nseg = p.nspan * p.span;
   } else {
     p.bwd_waves = p.bwd_tiles = 0;
-    p.cj = ww >= 3072 ? wide : 1;
+    p.cj = ww >= 3 * SIMDS ? wide : 1;
     long long nseg = 1;
-    if (w16 < 1024 && L > 256) {
-      p.cj = ww * most >= 3072 ? wide : 1;
+    if (w16 < SIMDS && L > 256) {
+      p.cj = ww * most >= 3 * SIMDS ? wide : 1;
       nseg = std::min(most, rec_cdiv(8192, p.cj == 1 ? w16 : ww));
     }
     p.seg_len = p.span_len = (int)(rec_cdiv(rec_cdiv(L, nseg), TT) * TT);
@@ -1167,7 +1168,7 @@ hipError_t launch_pass_kernel(ScanArgs a, hipStream_t st) {
   // 1024 waves took two turns, 2885 us instead of 1080 for 4096 tokens)
   const long long waves = (long long)a.B * a.nseg * a.G * a.tiles;
   a.waves = (int)waves;
-  const int per = waves > 1024 ? PASS_WAVES : 1;
+  const int per = waves > SIMDS ? PASS_WAVES : 1;
   return launch(scan_pass_kernel<T, NS, CJ, MODE, VEC>, rec_cdiv(waves, per), 64 * per, st, a,
                 per * sizeof(PassLds<NS, CJ, MODE>));
 }
