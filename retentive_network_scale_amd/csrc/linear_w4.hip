@@ -69,11 +69,14 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
 }
 
 // NN tiles of 16 rows of W, MT tiles of 16 tokens; the KS waves share out the blocks of
-// WORDS * 32 elements of K.  XR: rows of x kept, 16 MT, or 4 for at most four tokens,
-// which leaves room for chunks twice as long (K = 2048 is one: 7.8 -> 5.4 us for one token).
-template <int NN, int MT, int XR, int WORDS, bool VEC>
-__global__ __launch_bounds__(KS * 64, NN * MT > 2 ? 2 : 4) void w4_kernel(W4Args a) {
-  constexpr int NTH = KS * 64, KC = XR == 4 ? 2048 : 1024;          // K per chunk
+// WORDS * 32 elements of K, which come KC elements a chunk.  XR: rows of x kept, 16 MT, or 4
+// for at most four tokens, which leaves room for chunks twice as long (K = 2048 is one: 7.8 ->
+// 5.4 us for one token, N 12288).  Bound by the latency of the launch and one dependent chain
+// (load, LDS, matrix steps, the join), until N K is some 2^27 (M 16, N 8192, K 8192: 14 us for
+// 35 MB; M 64, N 16384, K 8192: 58 us for 67 MB and 34 GFLOP with both steps).
+template <int NN, int MT, int XR, int KC, int WORDS, bool VEC>
+__global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 : 4) void w4_kernel(W4Args a) {
+  constexpr int NTH = KS * 64;
   constexpr int KB = WORDS * 32, NB = KC / KB, U = NB / KS;         // per block; blocks of a chunk, of a wave
   constexpr int XROW = KC + 8, QROW = KC / 8 + 4;  // 16 bytes more: a quarter wave's rows start in different banks
   constexpr int XQ = XR * (KC / 8) / NTH, QQ = (16 * NN * (KC / 32) + NTH - 1) / NTH;  // a thread's 16 bytes of x and q
@@ -211,19 +214,19 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 ? 2 : 4) void w4_kernel(W4Args
   }
 }
 
-template <int NN, int MT, int XR, int WORDS>
+template <int NN, int MT, int XR, int KC, int WORDS>
 hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
   const dim3 grid((unsigned)rec_cdiv(a.N, 16 * NN), (unsigned)rec_cdiv(a.M, MT * 16));
   if (vec)
-    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, WORDS, true>), grid, dim3(KS * 64), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, true>), grid, dim3(KS * 64), 0, st, a);
   else
-    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, WORDS, false>), grid, dim3(KS * 64), 0, st, a);
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, false>), grid, dim3(KS * 64), 0, st, a);
   return hipGetLastError();
 }
-template <int NN, int MT, int XR = 16 * MT>
+template <int NN, int MT, int KC, int XR = 16 * MT>
 hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
-  if (a.group % 128 == 0) return launch_w<NN, MT, XR, 4>(a, vec, st);
-  return a.group == 64 ? launch_w<NN, MT, XR, 2>(a, vec, st) : launch_w<NN, MT, XR, 1>(a, vec, st);
+  if (a.group % 128 == 0) return launch_w<NN, MT, XR, KC, 4>(a, vec, st);
+  return a.group == 64 ? launch_w<NN, MT, XR, KC, 2>(a, vec, st) : launch_w<NN, MT, XR, KC, 1>(a, vec, st);
 }
 
 }  // namespace
@@ -264,10 +267,14 @@ hipError_t launch_w4(const void *x, const void *q, const void *scale, const void
   // K 4096: 6.9, 7.9, 14.6; M 64, N 2048, K 4096: 10.2, 8.2, 14.7; M 16, N 12288, K 2048: 9.4,
   // 7.3, 8.5; M 32: 15.5, 10.9, 9.3; M 64, N 16384, K 8192: 126, 75, 58.  So the larger one
   // as soon as it still gives about a workgroup per CU.
-  if (M <= 4) return launch_mt<1, 1, 4>(a, vec, st);
-  if (M > 16 && rec_cdiv(N, 64) * rec_cdiv(M, 32) >= 192) return launch_mt<4, 2>(a, vec, st);
-  if (rec_cdiv(N, 32) * rec_cdiv(M, 16) >= 256) return launch_mt<2, 1>(a, vec, st);
-  return launch_mt<1, 1>(a, vec, st);
+  if (M <= 4) return launch_mt<1, 1, 2048, 4>(a, vec, st);
+  if (M > 16 && rec_cdiv(N, 64) * rec_cdiv(M, 32) >= 192) return launch_mt<4, 2, 1024>(a, vec, st);
+  if (rec_cdiv(N, 32) * rec_cdiv(M, 16) >= 192) return launch_mt<2, 1, 1024>(a, vec, st);
+  // Chunks twice as long, whose LDS leaves a CU one workgroup, where there are no more than that:
+  // M 16, N 2048, K 4096, groups of 64: 7.3 -> 6.4 us, K 2048: 4.8 -> 4.3 us.  For 32 rows of W they
+  // took longer from K 4096 on (M 64, N 2048: 8.3 -> 8.9 us).
+  if (rec_cdiv(N, 16) * rec_cdiv(M, 16) <= 256 && K > 1024) return launch_mt<1, 1, 2048>(a, vec, st);
+  return launch_mt<1, 1, 1024>(a, vec, st);
 }
 
 }  // namespace ret
