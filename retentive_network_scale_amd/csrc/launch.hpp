@@ -69,7 +69,7 @@ hipError_t blaslt_gemm_nt(const uint16_t *X, const uint16_t *W, void *C, int T, 
 constexpr int W4_MAX_ROWS = 65535 * 16;  // M, by the launch grid
 const char *w4_refusal(const void *q, const void *scale, int N, int K, int group, bool *unsupported);
 hipError_t launch_w4(const void *x, const void *q, const void *scale, const void *zero, void *out, int M, int N, int K,
-                     int group, long long x_ld, bool out_bf16, hipStream_t st);
+                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos = nullptr);
 
 // Row-wise bf16 passes of the residual block (block.hip): LayerNorm without
 // affine (y may alias x) and exact gelu in place.

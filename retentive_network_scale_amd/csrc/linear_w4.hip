@@ -38,6 +38,7 @@ struct W4Args {
   void *out;
   long long x_ld;
   int M, N, K, group, out_bf16;
+  int *pos;  // a decode step's positions, advanced beside the products, or NULL
 };
 
 // Eight elements of x, and in the order 0 4 1 5 2 6 3 7, that of a word's nibbles below.
@@ -194,6 +195,8 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
       }
     }
   }
+  if (a.pos && blockIdx.x == 0 && wave == 0)
+    for (int b = m0 + lane; b < m0 + rows; b += 64) a.pos[b] += 1;
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < NN; ++t)
@@ -248,8 +251,9 @@ const char *w4_refusal(const void *q, const void *scale, int N, int K, int group
 }
 
 hipError_t launch_w4(const void *x, const void *q, const void *scale, const void *zero, void *out, int M, int N, int K,
-                     int group, long long x_ld, bool out_bf16, hipStream_t st) {
+                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos) {
   W4Args a;
+  a.pos = pos;
   a.x = (const uint16_t *)x;
   a.q = (const uint32_t *)q;
   a.scale = (const uint16_t *)scale;

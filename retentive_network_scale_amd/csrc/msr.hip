@@ -390,9 +390,10 @@ ret_status_t msr_layer_step_w4(const void *x, const void *in_q, const void *in_s
   if (e != hipSuccess) return launch_fail(e);
   if ((e = step_retention(proj, z, state, pos, B, H, dk, dv, gamma, theta, gn_eps, st)) != hipSuccess)
     return launch_fail(e);
-  if ((e = launch_w4(z, o_q, o_scale, o_zero, y, B, d_model, H * dv, o_group, (long long)H * dv, true, st)) != hipSuccess)
+  // the last product advances the positions too: the retention step has read them
+  if ((e = launch_w4(z, o_q, o_scale, o_zero, y, B, d_model, H * dv, o_group, (long long)H * dv, true, st,
+                     advance_pos ? pos : nullptr)) != hipSuccess)
     return launch_fail(e);
-  if (advance_pos && (e = launch_advance_pos(pos, B, st)) != hipSuccess) return launch_fail(e);
   return retention_fail_(RET_OK, "");
 }
 

@@ -537,6 +537,42 @@ def test_msr_step_w4(B, dm, H, dk, dv, g, zeros, rot):
         assert off <= 3 * 2.0 ** -8, off
 
 
+def test_msr_step_w4_positions_in_a_graph():
+    """The positions advance within the step (40 sequences: several tiles of tokens), or stay; a captured
+    step replays as the eager steps, bit for bit."""
+    B, dm, H, dk, dv = 40, 256, 2, 64, 128
+    gen = _gen(47)
+
+    def mat(n, k):
+        return (rn.pack_w4(torch.randint(0, 16, (n, k), generator=gen)).to(DEV),
+                (0.01 * torch.rand(n, k // 64, generator=gen)).to(BF).to(DEV), None)
+
+    w_in, w_o = mat(2 * H * dk + 2 * H * dv, dm), mat(dm, H * dv)
+    gamma, theta = torch.tensor([0.97, 0.99]), torch.rand(dk // 2, generator=gen)
+    start = torch.randint(0, 5000, (B,), generator=gen, dtype=torch.int32).to(DEV)
+    s1 = torch.zeros(B, H, dk, dv, device=DEV)
+    s2, p1, p2 = s1.clone(), start.clone(), start.clone()
+    x = torch.randn(B, dm, generator=gen).to(BF).to(DEV)
+    step = lambda s, p, **kw: rn.msr_layer_step_w4(x, w_in, w_o, s, p, H, dk, dv, gamma, theta, **kw)  # noqa: E731
+    step(s1.clone(), p1, advance_pos=False)
+    assert torch.equal(p1, start)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(s1.clone(), p1.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y1 = step(s1, p1)
+    for i in range(4):
+        x.copy_(torch.randn(B, dm, generator=_gen(48 + i)).to(BF))
+        graph.replay()
+        y2 = step(s2, p2)
+        torch.cuda.synchronize()
+        assert torch.equal(y1, y2) and torch.equal(s1, s2) and torch.equal(p1, p2)
+        assert torch.equal(p1, start + i + 1)
+
+
 # ------------------------------------------------------------------------------ long sequences
 def test_offsets_beyond_32_bits():
     """2^31 elements and more in one tensor: the last tokens, and their gradients, equal those of a call
