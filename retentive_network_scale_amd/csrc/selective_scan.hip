@@ -1074,7 +1074,9 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
   const int NS = state_regs(N), SUB = bwd_sub(NS), Dg = D / G;
   const int wide = wide_cj(NS);
   const long long groups = (long long)B * G, ww = groups * rec_cdiv(Dg, 16 * wide), w16 = groups * rec_cdiv(Dg, 16);
-  const long long most = rec_cdiv(L, 4 * TT);  // segments of at least four tiles
+  // Segments of at least four tiles; of two, where many states make a tile long and there would be
+  // less than two waves per SIMD (1000 tokens, D 512, N 64: 46 -> 35 us; N 16: 27 either way).
+  const long long most = rec_cdiv(L, (NS >= 8 && w16 * rec_cdiv(L, 4 * TT) < 2 * SIMDS ? 2 : 4) * TT);
   if (bwd) {
     // The main pass, at two waves per SIMD, takes few long spans: each starts with loads that
     // nothing hides.  The checkpoints' pass, at four, cuts them further.

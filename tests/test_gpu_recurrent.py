@@ -72,7 +72,7 @@ def _check_scan(v, softplus, lengths, out, state, what):
 SCAN_SHAPES = [  # Bt, L, D, N, G
     (1, 1, 1, 1, 1), (2, 1, 64, 16, 1), (1, 15, 67, 3, 1), (3, 16, 64, 4, 2), (1, 17, 130, 5, 2), (2, 33, 96, 8, 3),
     (1, 65, 256, 16, 1), (2, 50, 66, 17, 2), (1, 40, 64, 32, 1), (1, 37, 20, 33, 4), (2, 21, 130, 64, 1),
-    (1, 300, 64, 16, 1), (1, 257, 70, 24, 1), (2, 500, 12, 2, 3),
+    (1, 300, 64, 16, 1), (1, 257, 70, 24, 1), (2, 500, 12, 2, 3), (1, 290, 20, 64, 1),
 ]
 
 
