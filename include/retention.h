@@ -281,8 +281,8 @@ ret_status_t msr_layer_step(const void *x, const void *w_q, const void *w_k, con
  * W_Q, W_K, W_V, W_G.
  *   in_q [2 H dk + 2 H dv, d_model / 2], in_scale, in_zero [2 H dk + 2 H dv, d_model / in_group]
  *   o_q [d_model, H dv / 2], o_scale, o_zero [d_model, H dv / o_group]   (zeros or NULL)
- * Everything else, the step's mathematics included, as msr_layer_step; no library
- * GEMM is called.
+ * Everything else, the step's mathematics included, as msr_layer_step, but the gated
+ * heads go to W_O in fp32 (as two bf16 parts, 2^-16 of a value); no library GEMM is called.
  */
 size_t msr_layer_step_w4_workspace_bytes(int B, int d_model, int H, int dk, int dv);
 ret_status_t msr_layer_step_w4(const void *x, const void *in_q, const void *in_scale,

@@ -65,11 +65,12 @@ hipError_t blaslt_gemm_nt(const uint16_t *X, const uint16_t *W, void *C, int T, 
 
 // Products with 4-bit weights (linear_w4.hip): out [M, N] = x [M, K] W^T, arguments as
 // linear_w4's, already checked (q, scale, N, K and group by w4_refusal: the reason to
-// refuse them, or nullptr).
+// refuse them, or nullptr).  x_f32: x is fp32, rows 16-byte aligned, and is multiplied as two
+// bf16 parts (2^-16 of a value at most is lost).
 constexpr int W4_MAX_ROWS = 65535 * 16;  // M, by the launch grid
 const char *w4_refusal(const void *q, const void *scale, int N, int K, int group, bool *unsupported);
 hipError_t launch_w4(const void *x, const void *q, const void *scale, const void *zero, void *out, int M, int N, int K,
-                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos = nullptr);
+                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos = nullptr, bool x_f32 = false);
 
 // Row-wise bf16 passes of the residual block (block.hip): LayerNorm without
 // affine (y may alias x) and exact gelu in place.

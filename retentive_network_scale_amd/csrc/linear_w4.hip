@@ -32,7 +32,8 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 constexpr int KS = 8;  // waves of a workgroup
 
 struct W4Args {
-  const uint16_t *x, *scale;
+  const void *x;  // bf16, or fp32 where the kernel reads it in two parts
+  const uint16_t *scale;
   const uint32_t *q;
   const uint8_t *zero;
   void *out;
@@ -59,6 +60,17 @@ __device__ __forceinline__ u32x4 permuted(u32x4 v) {
   return r;
 }
 
+// Eight fp32 elements of x as two bf16 parts in that order, hi + lo, lo the remainder's: 2^-16 of
+// the value at most is lost.
+__device__ __forceinline__ void split_x(u32x4 a, u32x4 b, u32x4 &hi, u32x4 &lo) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float u = __uint_as_float(a[i]), v = __uint_as_float(b[i]);
+    hi[i] = pack_bf2(u, v);
+    lo[i] = pack_bf2(u - __uint_as_float(hi[i] << 16), v - __uint_as_float(hi[i] & 0xffff0000u));
+  }
+}
+
 // Eight weights of a word as 16 + q, same order.
 __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
   u32x4 r;
@@ -75,8 +87,12 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
 // 5.4 us for one token, N 12288).  Bound by the latency of the launch and one dependent chain
 // (load, LDS, matrix steps, the join), until N K is some 2^27 (M 16, N 8192, K 8192: 14 us for
 // 35 MB; M 64, N 16384, K 8192: 58 us for 67 MB and 34 GFLOP with both steps).
-template <int NN, int MT, int XR, int KC, int WORDS, bool VEC>
-__global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 : 4) void w4_kernel(W4Args a) {
+// SPLIT: x is fp32 (16-byte aligned, VEC) and multiplied in its two parts, whose rows of LDS and
+// matrix steps are twice as many: 9.0 us instead of 6.4 (M 16, N 2048, K 4096), 13.8 instead of 9.6
+// (M 64).  An accumulator for each part, or shorter chunks, were no faster.
+template <int NN, int MT, int XR, int KC, int WORDS, bool VEC, bool SPLIT>
+__global__ __launch_bounds__(KS * 64, NN * MT > 2 || SPLIT || (KC > 1024 && XR > 4) ? 2 : 4) void w4_kernel(W4Args a) {
+  constexpr int PARTS = SPLIT ? 2 : 1;
   constexpr int NTH = KS * 64;
   constexpr int KB = WORDS * 32, NB = KC / KB, U = NB / KS;         // per block; blocks of a chunk, of a wave
   constexpr int XROW = KC + 8, QROW = KC / 8 + 4;  // 16 bytes more: a quarter wave's rows start in different banks
@@ -84,7 +100,7 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
   constexpr int NR = 16 * NN, SQ = (NB * NR + NTH - 1) / NTH;  // rows of W; a thread's scales
   __shared__ union {
     struct {
-      uint16_t x[XR][XROW];
+      uint16_t x[PARTS][XR][XROW];
       uint32_t q[NR][QROW];
       float scale[NB][NR];
       uint32_t minus[NB][NR];  // -(16 + zero), twice
@@ -96,13 +112,15 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
   const int rows = min(a.M - m0, MT * 16), groups = a.K / a.group, blocks = a.K / KB;
   const unsigned per = a.group / KB;  // blocks per group; 1 for the groups of 32 and 64
   // the thread's share of a chunk: q and x by 16 bytes along their rows, blocks' scales and zero points
-  u32x4 qv[QQ], xv[XQ];
+  u32x4 qv[QQ], xv[XQ][PARTS];
   uint16_t sv[SQ];
   uint8_t zv[SQ];
 #pragma unroll
   for (int i = 0; i < QQ; ++i) qv[i] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < XQ; ++i) xv[i] = u32x4{0u, 0u, 0u, 0u};
+  for (int i = 0; i < XQ; ++i)
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) xv[i][k] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < SQ; ++i) sv[i] = 0, zv[i] = 8;
   const int sr = min(n0 + tid % NR, a.N - 1);
@@ -124,7 +142,14 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
       const int e = i * NTH + tid, r = e / (KC / 8), c = e % (KC / 8) * 8;
-      if (r < rows && k0 + c < a.K) xv[i] = load_x<VEC>(a.x + (long long)(m0 + r) * a.x_ld + k0 + c);
+      if (r < rows && k0 + c < a.K) {
+        const long long at = (long long)(m0 + r) * a.x_ld + k0 + c;
+        if constexpr (SPLIT)
+#pragma unroll
+          for (int k = 0; k < PARTS; ++k) xv[i][k] = ((const u32x4 *)((const float *)a.x + at))[k];
+        else
+          xv[i][0] = load_x<VEC>((const uint16_t *)a.x + at);
+      }
     }
   };
   f32x4 tot[NN][MT];
@@ -151,7 +176,15 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
 #pragma unroll
     for (int i = 0; i < XQ; ++i) {
       const int e = i * NTH + tid, r = e / (KC / 8);
-      if (r < rows) *(u32x4 *)&lds.c.x[r][e % (KC / 8) * 8] = permuted(xv[i]);
+      if (r < rows) {
+        u32x4 part[PARTS];
+        if constexpr (SPLIT)
+          split_x(xv[i][0], xv[i][1], part[0], part[1]);
+        else
+          part[0] = permuted(xv[i][0]);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) *(u32x4 *)&lds.c.x[k][r][e % (KC / 8) * 8] = part[k];
+      }
     }
     __syncthreads();
     if (k0 + KC < a.K) fetch(k0 + KC);
@@ -180,14 +213,16 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
         // rows without a token hold anything (or another's): they reach only their own rows of the result
         f32x4 acc[NN] = {};
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-          const bf16x8 xf = *(const bf16x8 *)&lds.c.x[(m * 16 + col) % XR][kb * KB + kq * WORDS * 8 + i * 8];
+        for (int i = 0; i < WORDS; ++i)
 #pragma unroll
-          for (int t = 0; t < NN; ++t) {
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[t][i]), acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus[t], acc[t], 0, 0, 0);
+          for (int k = 0; k < PARTS; ++k) {
+            const bf16x8 xf = *(const bf16x8 *)&lds.c.x[k][(m * 16 + col) % XR][kb * KB + kq * WORDS * 8 + i * 8];
+#pragma unroll
+            for (int t = 0; t < NN; ++t) {
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, unpack(wq[t][i]), acc[t], 0, 0, 0);
+              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, minus[t], acc[t], 0, 0, 0);
+            }
           }
-        }
 #pragma unroll
         for (int t = 0; t < NN; ++t)
 #pragma unroll
@@ -217,19 +252,27 @@ __global__ __launch_bounds__(KS * 64, NN * MT > 2 || (KC > 1024 && XR > 4) ? 2 :
   }
 }
 
+enum XKind { BF16_ROWS, BF16_WIDE, F32_PARTS };  // x by elements or by 16 bytes, or fp32 in two parts
+
 template <int NN, int MT, int XR, int KC, int WORDS>
-hipError_t launch_w(const W4Args &a, bool vec, hipStream_t st) {
+hipError_t launch_w(const W4Args &a, XKind x, hipStream_t st) {
   const dim3 grid((unsigned)rec_cdiv(a.N, 16 * NN), (unsigned)rec_cdiv(a.M, MT * 16));
-  if (vec)
-    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, true>), grid, dim3(KS * 64), 0, st, a);
-  else
-    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, false>), grid, dim3(KS * 64), 0, st, a);
+  if (x == F32_PARTS) {
+    if constexpr (NN * MT <= 2)
+      hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, true, true>), grid, dim3(KS * 64), 0, st, a);
+    else
+      return hipErrorInvalidValue;  // both parts of the larger tile do not fit LDS
+  } else if (x == BF16_WIDE) {
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, true, false>), grid, dim3(KS * 64), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((w4_kernel<NN, MT, XR, KC, WORDS, false, false>), grid, dim3(KS * 64), 0, st, a);
+  }
   return hipGetLastError();
 }
 template <int NN, int MT, int KC, int XR = 16 * MT>
-hipError_t launch_mt(const W4Args &a, bool vec, hipStream_t st) {
-  if (a.group % 128 == 0) return launch_w<NN, MT, XR, KC, 4>(a, vec, st);
-  return a.group == 64 ? launch_w<NN, MT, XR, KC, 2>(a, vec, st) : launch_w<NN, MT, XR, KC, 1>(a, vec, st);
+hipError_t launch_mt(const W4Args &a, XKind x, hipStream_t st) {
+  if (a.group % 128 == 0) return launch_w<NN, MT, XR, KC, 4>(a, x, st);
+  return a.group == 64 ? launch_w<NN, MT, XR, KC, 2>(a, x, st) : launch_w<NN, MT, XR, KC, 1>(a, x, st);
 }
 
 }  // namespace
@@ -251,10 +294,10 @@ const char *w4_refusal(const void *q, const void *scale, int N, int K, int group
 }
 
 hipError_t launch_w4(const void *x, const void *q, const void *scale, const void *zero, void *out, int M, int N, int K,
-                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos) {
+                     int group, long long x_ld, bool out_bf16, hipStream_t st, int *pos, bool x_f32) {
   W4Args a;
   a.pos = pos;
-  a.x = (const uint16_t *)x;
+  a.x = x;
   a.q = (const uint32_t *)q;
   a.scale = (const uint16_t *)scale;
   a.zero = (const uint8_t *)zero;
@@ -265,20 +308,20 @@ hipError_t launch_w4(const void *x, const void *q, const void *scale, const void
   a.K = K;
   a.group = group;
   a.out_bf16 = out_bf16;
-  const bool vec = x_ld % 8 == 0 && rec_aligned(x, 16);
+  const XKind kind = x_f32 ? F32_PARTS : x_ld % 8 == 0 && rec_aligned(x, 16) ? BF16_WIDE : BF16_ROWS;
   // A larger tile reads x and W fewer times from L2, a smaller one gives more workgroups.
   // Measured, us, for tiles of 16 x 16, 32 x 16, 64 x 32 (rows of W x tokens): M 16, N 2048,
   // K 4096: 6.9, 7.9, 14.6; M 64, N 2048, K 4096: 10.2, 8.2, 14.7; M 16, N 12288, K 2048: 9.4,
   // 7.3, 8.5; M 32: 15.5, 10.9, 9.3; M 64, N 16384, K 8192: 126, 75, 58.  So the larger one
   // as soon as it still gives about a workgroup per CU.
-  if (M <= 4) return launch_mt<1, 1, 2048, 4>(a, vec, st);
-  if (M > 16 && rec_cdiv(N, 64) * rec_cdiv(M, 32) >= 192) return launch_mt<4, 2, 1024>(a, vec, st);
-  if (rec_cdiv(N, 32) * rec_cdiv(M, 16) >= 192) return launch_mt<2, 1, 1024>(a, vec, st);
+  if (M <= 4) return launch_mt<1, 1, 2048, 4>(a, kind, st);
+  if (!x_f32 && M > 16 && rec_cdiv(N, 64) * rec_cdiv(M, 32) >= 192) return launch_mt<4, 2, 1024>(a, kind, st);
+  if (rec_cdiv(N, 32) * rec_cdiv(M, 16) >= 192) return launch_mt<2, 1, 1024>(a, kind, st);
   // Chunks twice as long, whose LDS leaves a CU one workgroup, where there are no more than that:
   // M 16, N 2048, K 4096, groups of 64: 7.3 -> 6.4 us, K 2048: 4.8 -> 4.3 us.  For 32 rows of W they
   // took longer from K 4096 on (M 64, N 2048: 8.3 -> 8.9 us).
-  if (rec_cdiv(N, 16) * rec_cdiv(M, 16) <= 256 && K > 1024) return launch_mt<1, 1, 2048>(a, vec, st);
-  return launch_mt<1, 1, 1024>(a, vec, st);
+  if (rec_cdiv(N, 16) * rec_cdiv(M, 16) <= 256 && K > 1024) return launch_mt<1, 1, 2048>(a, kind, st);
+  return launch_mt<1, 1, 1024>(a, kind, st);
 }
 
 }  // namespace ret

@@ -1,0 +1,94 @@
+"""GPU parity of the recurrent-layer operators at further edges: the 4-bit decode step against 64 bits."""
+import pytest
+import torch
+
+import retentive_network_scale_amd as rn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+# ------------------------------------------------------------------------------ 4-bit decode step
+def _w4_matrix(gen, n, k, g, lo, hi, zeros=True):
+    """(packed, scales, zeros) and the weights in 64 bits; scales are powers of two, 2^-lo .. 2^-hi."""
+    q = torch.randint(0, 16, (n, k), generator=gen, dtype=torch.uint8)
+    s = torch.exp2(-torch.randint(lo, hi + 1, (n, k // g), generator=gen).float()).to(BF)
+    z = torch.randint(5, 12, (n, k // g), generator=gen, dtype=torch.uint8) if zeros else None
+    off = z.double().repeat_interleave(g, 1) if zeros else 8.0
+    return (rn.pack_w4(q), s, z), (q.double() - off) * s.double().repeat_interleave(g, 1)
+
+
+def _to(w):
+    return tuple(None if t is None else t.to(DEV) for t in w)
+
+
+def _msr_step64(x, w_in, w_o, state, pos, H, dk, dv, gamma, theta, eps=1e-5):
+    """The decode step in 64 bits on the CPU: (y by heads [B, H, d_model], gated heads, new state)."""
+    B = x.shape[0]
+    p = x.double() @ w_in.T
+    q, k, v, gate = p.split([H * dk, H * dk, H * dv, H * dv], 1)
+    q, k = q.reshape(B, H, dk // 2, 2), k.reshape(B, H, dk // 2, 2)
+    if theta is not None:
+        turn = torch.polar(torch.ones(B, 1, dk // 2, dtype=torch.float64), (pos.double()[:, None] * theta.double())[:, None])
+        q, k = (torch.view_as_real(torch.view_as_complex(r.contiguous()) * turn) for r in (q, k))
+    q, k, v = q.reshape(B, H, dk, 1), k.reshape(B, H, dk, 1), v.reshape(B, H, 1, dv)
+    h = gamma.double()[:, None, None] * state.double() + k * v
+    o = (q * h).sum(2)
+    o = o - o.mean(-1, keepdim=True)
+    z = o / torch.sqrt((o * o).mean(-1, keepdim=True) + eps) * (gate * torch.sigmoid(gate)).reshape(B, H, dv)
+    y = torch.stack([z[:, i] @ w_o[:, i * dv:(i + 1) * dv].T for i in range(H)], 1)
+    return y, z, h
+
+
+def test_msr_step_w4_gated_heads_keep_their_bits():
+    """y is the 64-bit value rounded once to bf16, whatever the gated heads' own roundings to fewer bits would be.
+
+    Tokens that pick one column of the weights, scales and decays of powers of two, no rotation: projections, states
+    and the retention output are exact in fp32 (whole multiples of 2^-9 below 2^15), so only what follows is rounded,
+    in units of 2^-24: the deviation's sum of squares (dv / 2 + 8, the same for a head), the gate and the products
+    around it (16) and two bf16 parts of the gated heads (2^-16, 256); a block of 128 runs 16 matrix steps of at most
+    31 |z| scale, two roundings each (992), then scale and joins (16).  Then half a step of bf16 of the sum."""
+    B, dm, H, dk, dv, g = 16, 256, 8, 32, 512, 128
+    gen = torch.Generator().manual_seed(101)
+    w_in, d_in = _w4_matrix(gen, 2 * H * dk + 2 * H * dv, dm, g, 3, 3)
+    w_o, d_o = _w4_matrix(gen, dm, H * dv, g, 7, 9)
+    x = torch.zeros(B, dm)
+    x[torch.arange(B), torch.randint(0, dm, (B,), generator=gen)] = 1.0
+    x = x.to(BF)
+    state = torch.randint(-64, 65, (B, H, dk, dv), generator=gen) / 32.0
+    gamma, pos = torch.full((H,), 0.5), torch.zeros(B, dtype=torch.int32)
+    by_head, z, h = _msr_step64(x, d_in, d_o, state, pos, H, dk, dv, gamma, None)
+    st = state.to(DEV)
+    y = rn.msr_layer_step_w4(x.to(DEV), _to(w_in), _to(w_o), st, pos.to(DEV), H, dk, dv, gamma)
+    assert torch.equal(st.cpu().double(), h)
+    y64, az = by_head.sum(1), z.flatten(1).abs()
+    scale = w_o[1].double().repeat_interleave(g, 1)
+    off = 2.0 ** -24 * ((dv / 2 + 8) * by_head.abs().sum(1) + (256 + 16 + 16) * (az @ d_o.abs().T) + 992 * (az @ scale.T))
+    step = torch.exp2(torch.floor(torch.log2(y64.abs() + off)) - 7)  # of bf16 at that magnitude
+    worst = ((y.cpu().double() - y64).abs() / (step / 2 + off)).max().item()
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("B,dm,H,dk,dv,g,zeros,rot", [(3, 2048, 4, 64, 512, 64, True, True), (16, 2048, 4, 64, 512, 128, False, True),
+                                                      (20, 1152, 4, 64, 576, 32, True, True), (40, 1408, 2, 128, 704, 64, True, False),
+                                                      (64, 2048, 4, 64, 512, 64, True, True)])
+def test_msr_step_w4_against_64_bits(B, dm, H, dk, dv, g, zeros, rot):
+    """Sizes whose products walk several chunks of K, in each of their tiles.  y's rounding to bf16 is at most 2^-8 of
+    every value, 0.45 of that in the norm; the rest is room for the fp32 steps."""
+    gen = torch.Generator().manual_seed(102)
+    w_in, d_in = _w4_matrix(gen, 2 * H * dk + 2 * H * dv, dm, g, 7, 9, zeros)
+    w_o, d_o = _w4_matrix(gen, dm, H * dv, g, 7, 9, zeros)
+    gamma = torch.tensor([1 - 2.0 ** (-5 - i) for i in range(H)])
+    theta = torch.tensor([10000.0 ** (-2 * i / dk) for i in range(dk // 2)]) if rot else None
+    state = torch.randn(B, H, dk, dv, generator=gen)
+    pos = torch.randint(0, 5000, (B,), generator=gen, dtype=torch.int32)
+    x = torch.randn(B, dm, generator=gen).to(BF)
+    by_head, _, h = _msr_step64(x, d_in, d_o, state, pos, H, dk, dv, gamma, theta)
+    st, p = state.to(DEV), pos.to(DEV)
+    y = rn.msr_layer_step_w4(x.to(DEV), _to(w_in), _to(w_o), st, p, H, dk, dv, gamma, theta)
+    assert torch.equal(p.cpu(), pos + 1)
+    torch.testing.assert_close(st.cpu().double(), h, rtol=1e-4, atol=1e-4)
+    y64 = by_head.sum(1)
+    off = ((y.cpu().double() - y64).norm() / y64.norm()).item()
+    assert off <= 2.0 ** -8, off
