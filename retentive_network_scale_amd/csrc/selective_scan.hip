@@ -859,7 +859,10 @@ __global__ __launch_bounds__(64 * BWD_WAVES, NS >= 16 ? 1 : 2) void scan_bwd_ker
         }
         du[c] = gB[c] * dt[c] + dy * Dsk[c];
         dd[c] = sA[c] + gB[c] * u[c];
-        if (a.softplus) dd[c] *= sigmoid(x[c] + bias[c]);
+        if (a.softplus) {  // no slope (a masked token): 0, also where a rate of the lowest value made the sum overflow
+          const float slope = sigmoid(x[c] + bias[c]);
+          dd[c] = slope == 0.0f ? 0.0f : dd[c] * slope;
+        }
         const bool live = t0 + k < w.t_hi && c < nc;
         sD[c] += live ? dy * u[c] : 0.0f;
         sb[c] += live ? dd[c] : 0.0f;

@@ -1,8 +1,10 @@
-"""GPU parity of the recurrent-layer operators at further edges: the 4-bit decode step against 64 bits."""
+"""GPU parity of the recurrent-layer operators at further edges: the 4-bit decode step against 64 bits,
+masked tokens in the gradients."""
 import pytest
 import torch
 
 import retentive_network_scale_amd as rn
+from tests.test_gpu_recurrent import _bwd, _check_bwd, _scan_inputs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -92,3 +94,22 @@ def test_msr_step_w4_against_64_bits(B, dm, H, dk, dv, g, zeros, rot):
     y64 = by_head.sum(1)
     off = ((y.cpu().double() - y64).norm() / y64.norm()).item()
     assert off <= 2.0 ** -8, off
+
+
+# ------------------------------------------------------------------------------ masked tokens
+@pytest.mark.parametrize("L", [40, 300])
+def test_scan_bwd_masked_tokens_beside_rates_of_the_lowest_value(L):
+    """A token without a time step has no gradient for it, also where a state's rate is the lowest value: the sum over
+    states may overflow there, and softplus has no slope.  A rate of -inf (which the formula does not cover at such
+    a token) leaves every gradient finite too."""
+    v = _scan_inputs(2, L, 64, 8, 1, F32, 103, state=True)
+    v["A"][:, 1], v["A"][:, 2] = torch.finfo(F32).min, -3e38
+    v["h0"] = 4 * v["h0"]
+    v["delta"][0, :9] = v["delta"][1, 3:40:2] = float("-inf")
+    v["delta"][1, 4:30:2, ::3] = torch.finfo(F32).min
+    g = torch.Generator().manual_seed(104)
+    d_o, dhT = 4 * torch.randn(2, L, 64, generator=g), torch.randn(2, 64, 8, generator=g)
+    for lengths in (None, [L, L - 23]):
+        _check_bwd(v, d_o, dhT, True, lengths, _bwd(v, d_o, dhT, lengths=lengths), "masked, lowest")
+    v["A"][:, 3] = float("-inf")
+    assert all(bool(torch.isfinite(t).all()) for t in _bwd(v, d_o, dhT))
