@@ -1394,13 +1394,15 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   const void *fs[] = {dA, dD, ddelta_bias, d_state_in, d_state_out};
   for (const void *q : fs)
     if (!rec_aligned(q, 4)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  ScanPlan p = {};
+  if (L > 0) p = scan_plan(B, L, D, N, G, true);
   const RecSpan dho = {"d_state_out", d_state_out, d_state_out ? ns : 0};
   const RecSpan outs[] = {{"du", du, (size_t)rows * D * oe}, {"ddelta", ddelta, (size_t)rows * D * oe},
                           {"dA", dA, (size_t)D * N * 4}, {"dB", dB, (size_t)rows * bc * oe},
                           {"dC", dC, (size_t)rows * bc * oe}, {"dD", dD, (size_t)D * 4},
                           {"dz", dz, (size_t)rows * D * oe}, {"ddelta_bias", ddelta_bias, (size_t)D * 4},
                           {"d_state_in", d_state_in, d_state_in ? ns : 0},
-                          {"the workspace", L ? workspace : nullptr, workspace_bytes}};
+                          {"the workspace", workspace, p.total}};
   const RecSpan ins[] = {rec_rows("u", u, rows, u_ld, D, e), rec_rows("delta", delta, rows, delta_ld, D, e),
                          rec_rows("z", z, rows, z_ld, D, e), rec_rows("Bm", Bm, rows, b_ld, bc, e),
                          rec_rows("Cm", Cm, rows, c_ld, bc, e), {"A", A, (size_t)D * N * 4},
@@ -1422,7 +1424,6 @@ ret_status_t selective_scan_bwd(const void *u, const void *delta, const float *A
   const void *os[] = {du, ddelta, dB, dC, dz};
   for (const void *q : os)
     if (!rec_aligned(q, oe)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  const ScanPlan p = scan_plan(B, L, D, N, G, true);
   if (!workspace || workspace_bytes < p.total)
     return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.total, workspace_bytes);
   if (!rec_aligned(workspace, 16)) return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
