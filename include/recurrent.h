@@ -23,6 +23,8 @@
  *     one after the last token.
  *   - Accumulators and states are fp32; results are rounded once to out_dtype.
  *   - L == 0: nothing to compute; a final state is the initial one (or zero).
+ *   - A workspace query's size serves every call of at most that L with the same
+ *     other sizes (not of other B: more sequences can need less).
  *   - Outputs must not overlap inputs, the workspace or each other, except where
  *     a call says so.  Calls sharing a workspace must not overlap in time; two
  *     captured graphs that may run at once need two workspaces.

@@ -1063,6 +1063,32 @@ struct ScanPlan {
   size_t seg, sdt, gseg, ck, ckdt, bcpart, dApart, dDpart, dbpart, total;
 };
 
+// The parts of a workspace for nseg segments of in all subs sub-tiles per sequence, in nspan spans.
+void scan_layout(ScanPlan &p, int B, int L, int D, int N, int G, bool bwd, size_t nseg, size_t subs, size_t nspan) {
+  size_t off = 0;
+  auto take = [&off](size_t floats) {
+    const size_t at = off;
+    off += rec_align(floats * 4);
+    return at;
+  };
+  const size_t DN = (size_t)D * N;
+  p.seg = p.sdt = p.gseg = p.ck = p.ckdt = p.bcpart = p.dApart = p.dDpart = p.dbpart = 0;
+  if (bwd || nseg > 1) {
+    p.seg = take(B * nseg * DN);
+    p.sdt = take(B * nseg * D);
+  }
+  if (bwd) {
+    p.gseg = take(B * nseg * DN);
+    p.ck = take(B * subs * DN);
+    p.ckdt = take(B * subs * D);
+    p.bcpart = take((size_t)p.bwd_tiles * B * L * G * 2 * N);
+    p.dApart = take(B * nspan * DN);
+    p.dDpart = take(B * nspan * D);
+    p.dbpart = take(B * nspan * D);
+  }
+  p.total = off;
+}
+
 // How a call is cut.  Waves of 16 wide_cj channels share a token's LDS reads and sums
 // among up to 16 elements per lane; waves of 16 channels are more.  The wide ones are taken
 // where they still give three waves per SIMD: 24 sequences of 2048 tokens, D 2048, N 16
@@ -1108,29 +1134,39 @@ ScanPlan scan_plan(int B, int L, int D, int N, int G, bool bwd) {
     p.span = 1;
   }
   p.subs = p.seg_len / SUB;
-  size_t off = 0;
-  auto take = [&off](size_t floats) {
-    const size_t at = off;
-    off += rec_align(floats * 4);
-    return at;
-  };
-  const size_t bs = (size_t)B * p.nseg, DN = (size_t)D * N;
-  p.seg = p.sdt = p.gseg = p.ck = p.ckdt = p.bcpart = p.dApart = p.dDpart = p.dbpart = 0;
-  if (bwd || p.nseg > 1) {
-    p.seg = take(bs * DN);
-    p.sdt = take(bs * D);
-  }
-  if (bwd) {
-    p.gseg = take(bs * DN);
-    p.ck = take(bs * p.subs * DN);
-    p.ckdt = take(bs * p.subs * D);
-    p.bcpart = take((size_t)p.bwd_tiles * B * L * G * 2 * N);
-    p.dApart = take((size_t)B * p.nspan * DN);
-    p.dDpart = take((size_t)B * p.nspan * D);
-    p.dbpart = take((size_t)B * p.nspan * D);
-  }
-  p.total = off;
+  scan_layout(p, B, L, D, N, G, bwd, p.nseg, (size_t)p.nseg * p.subs, p.nspan);
   return p;
+}
+
+// Bytes that serve every call of at most L tokens: the plan's counts of segments and spans rise
+// and fall with L, so each is replaced by a bound that only rises.
+size_t scan_bytes(int B, int L, int D, int N, int G, bool bwd) {
+  ScanPlan p;
+  const int NS = state_regs(N), Dg = D / G, wide = wide_cj(NS);
+  const long long groups = (long long)B * G, ww = groups * rec_cdiv(Dg, 16 * wide), w16 = groups * rec_cdiv(Dg, 16);
+  if (!bwd) {
+    if (w16 >= SIMDS || L <= 256) return 0;
+    // the most segments by their length, of four tiles or (up to `fine` tokens) two; more of them
+    // never turn wide waves narrow again
+    const long long fine = NS >= 8 ? 4 * TT * ((2 * SIMDS - 1) / w16) : 0;
+    const long long most = std::max(rec_cdiv(L, 4 * TT), rec_cdiv(std::min<long long>(L, fine), 2 * TT));
+    scan_layout(p, B, L, D, N, G, false, std::min(most, rec_cdiv(8192, ww * most >= 3 * SIMDS ? ww : w16)), 0, 0);
+    return p.total;
+  }
+  const int cw = 16 * bwd_cj(NS);
+  p.bwd_waves = (int)std::min<long long>(BWD_WAVES, rec_cdiv(Dg, cw));
+  p.bwd_tiles = (int)rec_cdiv(Dg, (long long)cw * p.bwd_waves);
+  // In tiles.  s spans of n = ceil(tiles / s) cover at most tiles + min(n, s) - 1.  A span in c
+  // segments adds at most min(ceil(n / c), c) - 1: over all spans no more than there are segments
+  // (at most `cut`), and where c > 1 no more than half of what they cover.
+  const long long tiles = rec_cdiv(L, TT), cap = rec_cdiv(2048, groups * p.bwd_tiles * p.bwd_waves);
+  const long long spans = std::min(cap, rec_cdiv(tiles, 2));
+  const long long cover = tiles + (rec_cdiv(tiles, 2) <= cap ? 1 : std::min(rec_cdiv(tiles, cap), cap));
+  const long long cut = 4096 / (ww * rec_cdiv(L, 2 * TT) >= 3 * SIMDS ? ww : w16);
+  const long long all = cover + std::min(cut, cover / 2);
+  scan_layout(p, B, L, D, N, G, true, std::min(std::max(cut, spans), std::max(all / 2, 1LL)),
+              (size_t)all * (TT / bwd_sub(NS)), spans);
+  return p.total;
 }
 
 // Sizes a call takes, the header's limits.  They keep every grid below 2^32 threads: 64
@@ -1306,11 +1342,11 @@ ret_status_t check_inputs(const ScanArgs &a, size_t e) {
 extern "C" {
 
 size_t selective_scan_workspace_bytes(int B, int L, int D, int N, int G) {
-  return plan_ok(B, L, D, N, G) ? scan_plan(B, L, D, N, G, false).total : 0;
+  return plan_ok(B, L, D, N, G) ? scan_bytes(B, L, D, N, G, false) : 0;
 }
 
 size_t selective_scan_bwd_workspace_bytes(int B, int L, int D, int N, int G) {
-  return plan_ok(B, L, D, N, G) ? scan_plan(B, L, D, N, G, true).total : 0;
+  return plan_ok(B, L, D, N, G) ? scan_bytes(B, L, D, N, G, true) : 0;
 }
 
 ret_status_t selective_scan(const void *u, const void *delta, const float *A, const void *Bm, const void *Cm,
