@@ -406,17 +406,16 @@ void set_runs(ConvArgs &a, int vc, int most) {
 }
 constexpr int FWD_RUN = 64, BWD_RUN = 64;
 
-// Partial sums of the backward: workgroups along the tokens, of the kernel that has the most.
+// Partial sums of the backward for at most L tokens: workgroups along the tokens, of the kernel that
+// has the most.  Runs are halved where 64-token ones give less than 1024 NT threads, so that fewer
+// tokens can have more runs: at most the twice as many that were too few before the last halving.
 long long bwd_parts(int B, int L, int D) {
-  ConvArgs a = {};
-  a.B = B;
-  a.L = L;
-  a.D = D;
   long long most = 0;
   for (int vc : {1, 4})
     if (D % vc == 0) {
-      set_runs(a, vc, BWD_RUN);
-      most = std::max(most, B * rec_cdiv(a.runs, WAVES));
+      const long long enough = (1024LL * NT - 1) / ((long long)B * (D / vc));
+      const long long runs = std::max(rec_cdiv(L, BWD_RUN), std::min(rec_cdiv(L, STEP), 2 * enough));
+      most = std::max(most, B * rec_cdiv(runs, WAVES));
     }
   return most;
 }
@@ -490,7 +489,14 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
   for (const void *p : fs)
     if (!rec_aligned(p, 4)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   const long long rows = (long long)B * L;
-  const size_t need = causal_conv1d_bwd_workspace_bytes(B, L, D, K);
+  const int vc = channels(ps, 6, D, x_ld, e);
+  ConvArgs a = {};
+  a.B = B;
+  a.L = L;
+  a.D = D;
+  if (L > 0) set_runs(a, vc, BWD_RUN);
+  const long long parts = L > 0 ? B * rec_cdiv(a.runs, WAVES) : 0;
+  const size_t need = rec_align((size_t)parts * D * (K + 1) * 4);
   const RecSpan ins[] = {rec_rows("x", x, rows, x_ld, D, e), {"w", w, (size_t)D * K * e}, {"bias", bias, (size_t)D * e},
                          {"d_o", d_o, (size_t)rows * D * e}, {"state_in", state_in, ns},
                          {"d_state_out", d_state_out, ns}, {"lengths", lengths, (size_t)B * 4}};
@@ -501,7 +507,6 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
   if (L > 0 && (!workspace || workspace_bytes < need))
     return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
   if (!rec_aligned(workspace, 16)) return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  ConvArgs a = {};
   a.x = x;
   a.w = w;
   a.bias = bias;
@@ -512,9 +517,6 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
   a.dx = dx;
   a.dh0 = d_state_in;
   a.part = (float *)workspace;
-  a.B = B;
-  a.L = L;
-  a.D = D;
   a.K = K;
   a.x_ld = x_ld;
   a.silu = silu != 0;
@@ -530,19 +532,17 @@ ret_status_t causal_conv1d_bwd(const void *x, const void *w, const void *bias, c
       c.h0 = d_state_out;
       c.hT = d_state_in;
       const void *qs[] = {d_state_out, d_state_in};
-      const int vc = channels(qs, 2, D, 0, e);
-      err = launch<FWD>(c, bf, vc, (long long)B * (K - 1) * (D / vc), st);
+      const int sv = channels(qs, 2, D, 0, e);
+      err = launch<FWD>(c, bf, sv, (long long)B * (K - 1) * (D / sv), st);
     }
     if (err == hipSuccess) err = conv_sum(nullptr, dw, dbias, 0, D, K, st);
     return rec_status(err);
   }
-  const int vc = channels(ps, 6, D, x_ld, e);
-  set_runs(a, vc, BWD_RUN);
   if (!rec_grid_ok((double)rec_cdiv(D / vc, 64) * rec_cdiv(a.runs, WAVES) * B, NT))
     return rec_fail(RET_ERR_UNSUPPORTED, "too many tokens (B=%d L=%d D=%d)", B, L, D);
   hipError_t err = launch<BWD>(a, bf, vc, a.main_threads, st);
   if (err != hipSuccess) return rec_status(err);
-  return rec_status(conv_sum(a.part, dw, dbias, B * rec_cdiv(a.runs, WAVES), D, K, st));
+  return rec_status(conv_sum(a.part, dw, dbias, parts, D, K, st));
 }
 
 ret_status_t causal_conv1d_step(const void *x, const void *w, const void *bias, void *out, void *state, int B, int D,

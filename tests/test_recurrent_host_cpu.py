@@ -3,7 +3,7 @@ refusals themselves.  No call here reaches a kernel."""
 import pytest
 
 import retentive_network_scale_amd as rn
-from tests.test_recurrent_abi_cpu import INVALID, P, _bwd, _scan
+from tests.test_recurrent_abi_cpu import INVALID, P, _bwd, _conv_bwd, _scan
 
 
 def test_scan_bwd_workspace_is_what_the_call_needs():
@@ -38,4 +38,17 @@ def test_scan_workspace_holds_for_shorter_sequences(B, D, N, G):
             assert b"16-byte aligned" in lib.retention_last_error()
         grads = {k: P(i << 24) for i, k in enumerate(("d_o", "du", "dd", "dA", "dB", "dC", "dD", "dz", "db"), 20)}
         assert _bwd(**big, **at, **grads, h0=None, dhT=None, dh0=None, ws=P(40 << 24, 8), wb=need[1]) == INVALID
+        assert b"16-byte aligned" in lib.retention_last_error()
+
+
+@pytest.mark.parametrize("B,D", [(1, 4096), (1, 1), (3, 1000), (4, 4096), (16, 67), (2, 64)])
+def test_conv_workspace_holds_for_shorter_sequences(B, D):
+    lib = rn.lib()
+    before = 0
+    for L in (n for n in LENGTHS if B * n <= 1 << 24):
+        need = lib.causal_conv1d_bwd_workspace_bytes(B, L, D, 4)
+        assert need >= before, (L, before, need)
+        before = need
+        at = {k: P(i << 24) for i, k in enumerate(("x", "w", "bias", "d_o", "dx", "dw", "db"), 1)}
+        assert _conv_bwd(**at, s0=None, dsT=None, ds0=None, bt=B, L=L, d=D, xld=D, ws=P(20 << 24, 8), wb=need) == INVALID
         assert b"16-byte aligned" in lib.retention_last_error()
