@@ -20,8 +20,8 @@ CausalConvGrads = namedtuple("CausalConvGrads", "dx dw dbias d_state_in")
 
 
 # The calls here are short (a decode step's kernels take a few microseconds), so what
-# every call does on the host is kept to a few comparisons per tensor.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# every call does on the host is kept to a few comparisons per tensor.  Stream and device
+# come from torch._C at the call: a torch built without a GPU runtime has no such names.
 
 
 def _bad(t, name, shape, dtype, index):
@@ -86,7 +86,7 @@ class _Call:
             raise TypeError(f"{name} must be a GPU tensor")
         self.index, self.device, self.stream = t.get_device(), t.device, stream
         if stream is None:
-            self.raw = _raw_stream(self.index)
+            self.raw = torch._C._cuda_getCurrentRawStream(self.index)
         else:
             if stream.device != self.device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
@@ -112,7 +112,7 @@ class _Call:
         return t, _dense(t, "workspace", None, None, self.index), t.numel() * t.element_size()
 
     def run(self, fn, *args):
-        if _current_device() == self.index:
+        if torch._C._cuda_getDevice() == self.index:
             status = fn(*args, self.raw)
         else:
             with torch.cuda.device(self.index):

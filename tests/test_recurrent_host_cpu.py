@@ -1,6 +1,9 @@
 """Host side of the recurrent-layer operators on the CPU: what their argument checks compare, beside the
 refusals themselves.  No call here reaches a kernel."""
+import importlib.util
+
 import pytest
+import torch
 
 import retentive_network_scale_amd as rn
 from tests.test_recurrent_abi_cpu import INVALID, P, _bwd, _conv_bwd, _scan
@@ -52,3 +55,14 @@ def test_conv_workspace_holds_for_shorter_sequences(B, D):
         at = {k: P(i << 24) for i, k in enumerate(("x", "w", "bias", "d_o", "dx", "dw", "db"), 1)}
         assert _conv_bwd(**at, s0=None, dsT=None, ds0=None, bt=B, L=L, d=D, xld=D, ws=P(20 << 24, 8), wb=need) == INVALID
         assert b"16-byte aligned" in lib.retention_last_error()
+
+
+def test_binding_imports_without_a_gpu_runtime(monkeypatch):
+    """torch built for the CPU alone lacks the stream and device queries: that shows at a call, not at import."""
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name)
+    spec = importlib.util.spec_from_file_location(rn.__name__ + ".recurrent_again", rn.recurrent.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    with pytest.raises(TypeError):
+        module.linear_w4(torch.zeros(1, 32), torch.zeros(1, 16), torch.zeros(1, 1))
