@@ -92,6 +92,17 @@ __device__ __forceinline__ void load_taps(const ConvArgs &a, int d, float (&w)[K
   }
 }
 
+// bias + sum_j w_j x_{i+j}, the products added in their order and each fused with its sum: written
+// out, so that a token has the same bits in a prompt and as a step (left to the compiler, two taps
+// were fused the one way here and the other way there).
+template <int K, int VC, int W>
+__device__ __forceinline__ float taps_at(const float (&w)[K][VC], const float (&x)[W][VC], float bias, int i, int c) {
+  float s = w[0][c] * x[i][c];
+#pragma unroll
+  for (int j = 1; j < K; ++j) s = fmaf(w[j][c], x[i + j][c], s);
+  return s + bias;
+}
+
 __device__ __forceinline__ int length_of(const ConvArgs &a, long long b) {
   return a.lengths ? min(max(a.lengths[b], 0), a.L) : a.L;
 }
@@ -135,10 +146,7 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
       float y[VC];
 #pragma unroll
       for (int c = 0; c < VC; ++c) {
-        float s = w[0][c] * win[i][c];
-#pragma unroll
-        for (int j = 1; j < K; ++j) s += w[j][c] * win[i + j][c];
-        s += bias[c];
+        const float s = taps_at(w, win, bias[c], i, c);
         y[c] = a.silu ? silu(s) : s;
       }
       if (t + i < t1) storec<T, VC>((T *)a.out + (b * a.L + t + i) * a.D + d, y);
@@ -328,10 +336,7 @@ __global__ __launch_bounds__(NT) void conv_step_kernel(ConvArgs a) {
   loadc<T, VC>((const T *)a.x + b * a.x_ld + d, x[K - 1]);
 #pragma unroll
   for (int c = 0; c < VC; ++c) {
-    float s = w[0][c] * x[0][c];
-#pragma unroll
-    for (int j = 1; j < K; ++j) s += w[j][c] * x[j][c];
-    s += bias[c];
+    const float s = taps_at(w, x, bias[c], 0, c);
     y[c] = a.silu ? silu(s) : s;
   }
   storec<T, VC>((T *)a.out + b * a.D + d, y);

@@ -1,10 +1,10 @@
 """GPU parity of the recurrent-layer operators at further edges: the 4-bit decode step against 64 bits,
-masked tokens in the gradients."""
+masked tokens in the gradients, every number of the convolution's taps."""
 import pytest
 import torch
 
 import retentive_network_scale_amd as rn
-from tests.test_gpu_recurrent import _bwd, _check_bwd, _scan_inputs
+from tests.test_gpu_recurrent import _bwd, _check_bwd, _check_conv, _check_conv_bwd, _conv_inputs, _scan_inputs
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -74,9 +74,11 @@ def test_msr_step_w4_gated_heads_keep_their_bits():
 
 @pytest.mark.parametrize("B,dm,H,dk,dv,g,zeros,rot", [(3, 2048, 4, 64, 512, 64, True, True), (16, 2048, 4, 64, 512, 128, False, True),
                                                       (20, 1152, 4, 64, 576, 32, True, True), (40, 1408, 2, 128, 704, 64, True, False),
-                                                      (64, 2048, 4, 64, 512, 64, True, True)])
+                                                      (64, 2048, 4, 64, 512, 64, True, True), (64, 2048, 2, 64, 640, 32, False, True),
+                                                      (64, 2048, 4, 64, 512, 128, True, True), (16, 1280, 4, 64, 544, 64, True, True),
+                                                      (6, 256, 2, 64, 128, 32, True, True), (7, 256, 2, 64, 192, 128, True, True)])
 def test_msr_step_w4_against_64_bits(B, dm, H, dk, dv, g, zeros, rot):
-    """Sizes whose products walk several chunks of K, in each of their tiles.  y's rounding to bf16 is at most 2^-8 of
+    """Sizes whose products walk several chunks of K, and short ones, in each of their tiles.  y's rounding to bf16 is at most 2^-8 of
     every value, 0.45 of that in the norm; the rest is room for the fp32 steps."""
     gen = torch.Generator().manual_seed(102)
     w_in, d_in = _w4_matrix(gen, 2 * H * dk + 2 * H * dv, dm, g, 7, 9, zeros)
@@ -113,3 +115,20 @@ def test_scan_bwd_masked_tokens_beside_rates_of_the_lowest_value(L):
         _check_bwd(v, d_o, dhT, True, lengths, _bwd(v, d_o, dhT, lengths=lengths), "masked, lowest")
     v["A"][:, 3] = float("-inf")
     assert all(bool(torch.isfinite(t).all()) for t in _bwd(v, d_o, dhT))
+
+
+# ------------------------------------------------------------------------------ taps
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("d", [26, 28])
+@pytest.mark.parametrize("k", [2, 3, 4, 5, 6, 7, 8])
+def test_conv_taps(k, d, dt):
+    """Every number of taps, by one channel and by four: the whole, its gradients, and the last token as a step."""
+    v = _conv_inputs(2, 37, d, k, dt, 215)
+    dev = {n: t.to(DEV) for n, t in v.items()}
+    out, st = rn.causal_conv1d(dev["x"], dev["w"], dev["bias"], state_in=dev["s0"], state_out=True)
+    _check_conv(v, True, None, out, st, f"{k} {d}")
+    got = rn.causal_conv1d_bwd(dev["x"], dev["w"], dev["d_o"], dev["bias"], state_in=dev["s0"], d_state_out=dev["dsT"])
+    _check_conv_bwd(v, True, None, got, f"{k} {d}")
+    _, h = rn.causal_conv1d(dev["x"][:, :-1].contiguous(), dev["w"], dev["bias"], state_in=dev["s0"], state_out=True)
+    one = rn.causal_conv1d_step(dev["x"][:, -1].contiguous(), h, dev["w"], dev["bias"])
+    assert torch.equal(one, out[:, -1]) and torch.equal(h, st)
