@@ -236,7 +236,7 @@ struct Quad<float, VEC> {
   }
 };
 
-// The CJ neighbouring values of a lane in a row of LDS.
+// The CJ neighbouring values of a lane in a row of LDS (four where it staged them, one or two channels in a pass).
 template <int CJ>
 __device__ __forceinline__ void get_lane(const float *p, float (&r)[CJ]) {
   if constexpr (CJ == 4) {
@@ -255,9 +255,7 @@ __device__ __forceinline__ void get_lane(const float *p, float (&r)[CJ]) {
 }
 template <int CJ>
 __device__ __forceinline__ void put_lane(float *p, const float (&r)[CJ]) {
-  if constexpr (CJ == 4)
-    *(float4 *)p = make_float4(r[0], r[1], r[2], r[3]);
-  else if constexpr (CJ == 2)
+  if constexpr (CJ == 2)
     *(float2 *)p = make_float2(r[0], r[1]);
   else
     p[0] = r[0];
