@@ -90,8 +90,11 @@ def test_scan_two_channels_a_lane_in_segments(d, n, G, dt):
 @pytest.mark.parametrize("d,n,G", [(4100, 4, 1), (4104, 8, 2), (4100, 16, 1), (4104, 24, 2), (4100, 32, 1)])
 def test_scan_bwd_two_channels_a_lane(d, n, G, dt):
     """Checkpoints of 32 channels a wave, spans of several segments; ends inside a segment."""
-    bt, L = 2, 380
+    bt, L = 2, 400
     assert _waves(bt, d, G, 32) * _cdiv(L, 32) >= 3 * SIMDS
+    four = 4 * 16 * (1 if n > 16 else 2)  # channels of the main pass's workgroups
+    span = 16 * _cdiv(_cdiv(L, min(_cdiv(2048, 4 * _waves(bt, d, G, four)), _cdiv(L, 32))), 16)
+    assert span > 32 and 4096 // (_waves(bt, d, G, 32) * _cdiv(L, span)) >= 2
     lengths = [L, 211]
     v = _scan_big(bt, L, d, n, G, dt, 204, lengths)
     args, kw = _args(v)
