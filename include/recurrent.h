@@ -82,6 +82,9 @@ ret_status_t selective_scan(const void *u, const void *delta, const float *A, co
  *   dA = sum_t g_t dt_t exp(dt_t A) h_{t-1}   dD = sum_t dy_t u_t   ddelta_bias = sum_t ddelta_t
  *   d_state_in = exp(dt_0 A) g_0
  * The states are computed again from the inputs; nothing of the forward call is kept.
+ * The workspace holds a state every 16 tokens (N <= 16), 8 (N <= 32) or 4: some 4 B L D N / 16,
+ * / 8 or / 4 bytes, 9.9 GB at B 8, L 4096, D 4096, N 64.  A token whose time step softplus
+ * makes 0 has ddelta 0, whatever the rates.
  *   du, ddelta, dz : [B, L, D] out_dtype, dense (dz NULL exactly where z is)
  *   dB, dC : [B, L, G, N] out_dtype, dense
  *   dA : [D, N] fp32    dD, ddelta_bias : [D] fp32, or NULL where not wanted

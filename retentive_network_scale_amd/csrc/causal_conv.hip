@@ -5,7 +5,7 @@
 // aligned to them), their taps and a window of the last K inputs in registers and walks
 // a run of tokens, so each input is read once but for the K - 1 in front of a run.  The
 // loads of a step's tokens go out together.  Bound by the bytes, each moved once: the forward
-// takes 59 us for 268 MB (4.5 TB/s) at B 4, L 4096, D 4096, bf16 (the vector unit is busy 82 %); runs of 128 tokens and
+// takes 63 us for 268 MB (4.2 TB/s) at B 4, L 4096, D 4096, bf16 (the vector unit is busy 81 %); runs of 128 tokens and
 // steps of four were no faster.
 #include <algorithm>
 #include <type_traits>
@@ -163,8 +163,8 @@ __global__ __launch_bounds__(NT) void conv_fwd_kernel(ConvArgs a) {
 // g the last inputs of the run need; the first run also covers the K - 1 inputs of the
 // state in front.  The workgroup's waves take neighbouring runs of the same channels and
 // add up their dw and dbias.  Bound by its three streams of memory; four waves per SIMD
-// (128 registers, where the taps allow it) instead of three took it from 111 to 92 us at B 4, L 4096, D 4096, bf16,
-// 403 MB, 4.4 TB/s.
+// (128 registers, where the taps allow it) instead of three took it from 111 to 92 us at best at B 4, L 4096, D 4096,
+// bf16 (96 on average: 403 MB, 4.2 TB/s).
 template <typename T, int K, int VC>
 __global__ __launch_bounds__(NT, K <= 3 || (K == 4 && sizeof(T) == 2) ? 4 : 2) void conv_bwd_kernel(ConvArgs a) {
   constexpr int S = 4;

@@ -86,9 +86,11 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w) {
 // for at most four tokens, which leaves room for chunks twice as long (K = 2048 is one: 7.8 ->
 // 5.4 us for one token, N 12288).  Bound by the latency of the launch and one dependent chain
 // (load, LDS, matrix steps, the join), until N K is some 2^27 (M 16, N 8192, K 8192: 14 us for
-// 35 MB; M 64, N 16384, K 8192: 58 us for 67 MB and 34 GFLOP with both steps).
+// 35 MB; M 64, N 16384, K 8192: 58 us for 67 MB and 34 GFLOP with both steps).  The tile of 64 rows
+// and 32 tokens is bound by no unit (matrix cores busy 21 %, vector unit 35 %, LDS 18 %): its 104 KB of
+// LDS leave a CU one workgroup, whose loads and matrix steps take turns around a chunk's barriers.
 // SPLIT: x is fp32 (16-byte aligned, VEC) and multiplied in its two parts, whose rows of LDS and
-// matrix steps are twice as many: 9.0 us instead of 6.4 (M 16, N 2048, K 4096), 13.8 instead of 9.6
+// matrix steps are twice as many: 9.2 us instead of 6.4 (M 16, N 2048, K 4096), 13.8 instead of 9.6
 // (M 64).  An accumulator for each part, or shorter chunks, were no faster.
 template <int NN, int MT, int XR, int KC, int WORDS, bool VEC, bool SPLIT>
 __global__ __launch_bounds__(KS * 64, NN * MT > 2 || SPLIT || (KC > 1024 && XR > 4) ? 2 : 4) void w4_kernel(W4Args a) {
