@@ -11,6 +11,9 @@ Functions (same names as the C ABI):
 and, declared in include/recurrent.h and bound in recurrent.py,
     selective_scan, selective_scan_bwd, selective_scan_step, causal_conv1d,
     causal_conv1d_bwd, causal_conv1d_step, linear_w4
+and, declared in include/language.h and bound in language.py,
+    embedding, embedding_bwd, group_norm_gate, group_norm_gate_bwd, linear, linear_bwd,
+    beam_select, beam_reorder
 """
 import ctypes
 import os
@@ -31,6 +34,10 @@ __all__ = [
     "selective_scan_step", "SelectiveScanGrads", "causal_conv1d", "causal_conv1d_bwd",
     "causal_conv1d_bwd_workspace_bytes", "causal_conv1d_step", "CausalConvGrads", "linear_w4", "pack_w4",
     "RECURRENT_SYMBOLS",
+    "embedding", "embedding_bwd", "embedding_bwd_workspace_bytes", "group_norm_gate", "group_norm_gate_bwd",
+    "group_norm_gate_bwd_workspace_bytes", "GroupNormGateGrads", "linear", "linear_workspace_bytes", "linear_bwd",
+    "linear_bwd_workspace_bytes", "LinearGrads", "beam_select", "beam_select_workspace_bytes", "BeamSelection",
+    "beam_reorder", "LANGUAGE_SYMBOLS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libretention.so")
@@ -89,6 +96,24 @@ _RECURRENT_SIGS = {
 }
 RECURRENT_SYMBOLS = tuple(_RECURRENT_SIGS)
 
+# the same, mirroring include/language.h
+_LANGUAGE_SIGS = {
+    "embedding": (_i, [_vp] * 3 + [_ll, _i, _i, _f, _i, _i, _vp]),
+    "embedding_bwd_workspace_bytes": (_sz, [_ll, _i, _i]),
+    "embedding_bwd": (_i, [_vp] * 3 + [_ll, _i, _i, _ll, _f, _i, _i, _vp, _sz, _vp]),
+    "group_norm_gate": (_i, [_vp] * 6 + [_i] * 4 + [_ll] * 4 + [_i, _f, _i, _i, _vp]),
+    "group_norm_gate_bwd_workspace_bytes": (_sz, [_i] * 4),
+    "group_norm_gate_bwd": (_i, [_vp] * 10 + [_i] * 4 + [_ll] * 4 + [_i, _f, _i, _i, _vp, _sz, _vp]),
+    "linear_workspace_bytes": (_sz, [_ll, _i, _i]),
+    "linear": (_i, [_vp] * 6 + [_ll, _i, _i, _ll, _i, _i, _i, _vp, _sz, _vp]),
+    "linear_bwd_workspace_bytes": (_sz, [_ll, _i, _i]),
+    "linear_bwd": (_i, [_vp] * 7 + [_ll, _i, _i, _ll, _i, _i, _vp, _sz, _vp]),
+    "beam_select_workspace_bytes": (_sz, [_i] * 4),
+    "beam_select": (_i, [_vp] * 6 + [_i] * 4 + [_ll, _i, _i, _vp, _sz, _vp]),
+    "beam_reorder": (_i, [ctypes.POINTER(_vp), ctypes.POINTER(_ll), _i, _vp, _i, _i, _vp]),
+}
+LANGUAGE_SYMBOLS = tuple(_LANGUAGE_SIGS)
+
 _lib = None
 
 
@@ -106,7 +131,7 @@ def lib():
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m retentive_network_scale_amd.build`")
         L = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in (*_SIGS.items(), *_RECURRENT_SIGS.items()):
+        for name, (res, args) in (*_SIGS.items(), *_RECURRENT_SIGS.items(), *_LANGUAGE_SIGS.items()):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = res, args
         _lib = L
@@ -373,3 +398,7 @@ from .recurrent import (  # noqa: E402  (needs the helpers above)
     CausalConvGrads, SelectiveScanGrads, causal_conv1d, causal_conv1d_bwd, causal_conv1d_bwd_workspace_bytes,
     causal_conv1d_step, linear_w4, msr_layer_step_w4, msr_layer_step_w4_workspace_bytes, pack_w4, selective_scan,
     selective_scan_bwd, selective_scan_bwd_workspace_bytes, selective_scan_step, selective_scan_workspace_bytes)
+from .language import (  # noqa: E402  (on recurrent's helpers)
+    BeamSelection, GroupNormGateGrads, LinearGrads, beam_reorder, beam_select, beam_select_workspace_bytes, embedding,
+    embedding_bwd, embedding_bwd_workspace_bytes, group_norm_gate, group_norm_gate_bwd,
+    group_norm_gate_bwd_workspace_bytes, linear, linear_bwd, linear_bwd_workspace_bytes, linear_workspace_bytes)

@@ -1,0 +1,422 @@
+// A step of a beam search: the selection of the K best continuations of every request, and the
+// reordering of the beams' states (language.h).
+//
+// Selection takes two launches.  The first reads the logits once: a workgroup keeps a slice of one
+// beam's row in registers, leaves the slice's maximum and sum of exponentials, and its K best
+// logits in order.  To find those, every thread's best value is ranked among the workgroup's; the
+// K-th of them is a bound that at least K elements reach and few pass, and those that
+// reach it are ranked by counting.  Values are ordered together with their indices, as one whole
+// number, so that none are equal.  The second launch, a workgroup a request, joins the slices'
+// sums to the beams' log-sums and does the same with the lists' heads and the lists.
+#include <math.h>
+
+#include <algorithm>
+
+#include "language.hpp"
+
+using namespace ret;
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int MAXK = LANGUAGE_MAX_BEAMS;
+typedef unsigned long long u64;
+
+struct Cand {
+  float value;
+  int index;  // in the row; -1: none
+};
+
+struct SelectArgs {
+  const void *logits;
+  const float *scores;
+  const uint8_t *ended;
+  int *tokens, *parents;
+  float *out_scores;
+  float2 *sums;  // [B W][slices]: maximum, sum of exp(x - maximum)
+  Cand *cands;   // [B W][slices][K], best first
+  long long ld;
+  int B, W, V, K, eos, slices;
+};
+
+// Whole numbers in the order of the values (NaN of either sign at the ends).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ u64 ordered(double v) {
+  const u64 b = (u64)__double_as_longlong(v);
+  return b ^ ((u64)((long long)b >> 63) | 0x8000000000000000ull);
+}
+// -0 is 0: the two compare equal, and the index has to decide.
+__device__ __forceinline__ u64 key_of(float v, int index) { return (u64)ordered(v + 0.0f) << 32 | (uint32_t)~index; }
+
+// E elements of a row a thread, in E / 8 chunks.
+template <typename T, int E>
+__global__ __launch_bounds__(NT) void slice_kernel(SelectArgs a) {
+  constexpr int CAP = MAXK * E;  // elements that can reach the bound: of the K - 1 threads with a better one, and one more
+  __shared__ u64 best[NT];
+  __shared__ u64 list[CAP];
+  __shared__ float red[NT / 64];
+  __shared__ u64 bound;
+  __shared__ int count;
+  const int tid = threadIdx.x, slice = blockIdx.x;
+  const long long row = blockIdx.y + (long long)blockIdx.z * 65535;
+  if (row >= (long long)a.B * a.W) return;
+  // an ended beam and one without a score offer nothing of their logits
+  if ((a.ended && a.ended[row]) || !isfinite(a.scores[row])) return;
+  const int first = slice * (NT * E);
+  const T *src = (const T *)a.logits + row * a.ld;
+  float x[E / 8][8];
+#pragma unroll
+  for (int c = 0; c < E / 8; ++c) {
+    const int at = first + (c * NT + tid) * 8;
+    load8(src + at, a.V - at, x[c]);
+  }
+  u64 mine = 0;
+  float m = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = first + (c * NT + tid) * 8 + i;
+      if (at < a.V) {
+        const u64 k = key_of(x[c][i], at);
+        mine = k > mine ? k : mine;
+        m = fmaxf(m, x[c][i]);
+      }
+    }
+  best[tid] = mine;
+  if (tid == 0) bound = 0, count = 0;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+  m = red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[w]);
+  // the rank of the thread's best
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < NT; ++j) rank += best[j] > mine;
+  if (mine && rank == a.K - 1) bound = mine;
+  // sum of exponentials; a maximum that is not finite (or a NaN, which fmaxf passes over) shows in the sum
+  float s = 0.0f;
+#pragma unroll
+  for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = first + (c * NT + tid) * 8 + i;
+      if (at < a.V) s += m == -INFINITY ? (x[c][i] == x[c][i] ? 0.0f : x[c][i]) : expf(x[c][i] - m);
+    }
+  __syncthreads();  // red is read, bound written
+  s = block_sum<NT>(s, red);
+  const u64 least = bound;
+#pragma unroll
+  for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = first + (c * NT + tid) * 8 + i;
+      if (at < a.V) {
+        const u64 k = key_of(x[c][i], at);
+        if (k >= least) {
+          const int to = atomicAdd(&count, 1);
+          if (to < CAP) list[to] = k;
+        }
+      }
+    }
+  __syncthreads();
+  const int n = min(count, CAP);
+  Cand *out = a.cands + (row * a.slices + slice) * a.K;
+  for (int e = tid; e < n; e += NT) {
+    const u64 k = list[e];
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += list[j] > k;
+    if (r < a.K) {
+      const uint32_t o = (uint32_t)(k >> 32);
+      out[r] = {__uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu)), (int)~(uint32_t)k};
+    }
+  }
+  for (int e = n + tid; e < a.K; e += NT) out[e] = {0.0f, -1};
+  if (tid == 0) a.sums[row * a.slices + slice] = make_float2(m, s);
+}
+
+struct Key {
+  u64 score;
+  uint32_t index;  // ~ flat index
+  __device__ __forceinline__ bool above(const Key &o) const {
+    return score > o.score || (score == o.score && index > o.index);
+  }
+};
+
+constexpr int MAX_LISTS = LANGUAGE_MAX_BEAM_LISTS;
+constexpr int CAP2 = MAXK * MAXK;
+
+__global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
+  __shared__ double lse[MAXK];
+  __shared__ int kind[MAXK];  // 0: an ordinary beam, 1: ended, 2: nothing to offer
+  __shared__ u64 head_score[MAX_LISTS];
+  __shared__ uint32_t head_index[MAX_LISTS];
+  __shared__ u64 list_score[CAP2];
+  __shared__ uint32_t list_index[CAP2];
+  __shared__ Key bound;
+  __shared__ int count;
+  const int tid = threadIdx.x;
+  const long long b = blockIdx.x;
+  if (tid < a.W) {
+    const long long row = b * a.W + tid;
+    const float own = a.scores[row];
+    float m = -INFINITY;
+    for (int i = 0; i < a.slices; ++i) m = fmaxf(m, a.sums[row * a.slices + i].x);
+    double s = 0.0;
+    for (int i = 0; i < a.slices; ++i) {
+      const float2 v = a.sums[row * a.slices + i];
+      // a slice of nothing but -inf adds its sum, 0 or NaN
+      s += v.x == -INFINITY ? (double)v.y : (double)v.y * exp((double)v.x - (double)m);
+    }
+    const double l = (double)m + log(s);
+    lse[tid] = l;
+    kind[tid] = !isfinite(own) ? 2 : a.ended && a.ended[row] ? 1 : isfinite(l) ? 0 : 2;
+  }
+  if (tid == 0) bound = {0, 0}, count = 0;
+  __syncthreads();
+  const int lists = a.W * a.slices;
+  // Candidate j of a list as a key; {0, 0}: none
+  auto key_at = [&](int list, int j) -> Key {
+    const int w = list / a.slices, slice = list - w * a.slices;
+    const long long row = b * a.W + w;
+    int v;
+    double score;
+    if (kind[w] == 0) {
+      const Cand c = a.cands[(row * a.slices + slice) * a.K + j];
+      if (c.index < 0) return {0, 0};
+      v = c.index;
+      score = (double)a.scores[row] + ((double)c.value - lse[w]);
+    } else {
+      // the tokens in their order, after the end token where the beam has ended: in the first list
+      if (slice) return {0, 0};
+      const bool end = kind[w] == 1 && a.eos >= 0 && a.eos < a.V;
+      v = !end ? j : j == 0 ? a.eos : j - 1 < a.eos ? j - 1 : j;
+      if (v >= a.V) return {0, 0};
+      score = end && j == 0 ? (double)a.scores[row] : -INFINITY;
+    }
+    return {ordered(score + 0.0), ~(uint32_t)(w * a.V + v)};
+  };
+  for (int l = tid; l < lists; l += NT) {
+    const Key k = key_at(l, 0);
+    head_score[l] = k.score;
+    head_index[l] = k.index;
+  }
+  __syncthreads();
+  for (int l = tid; l < lists; l += NT) {
+    const Key k = {head_score[l], head_index[l]};
+    if (!k.score) continue;
+    int r = 0;
+    for (int j = 0; j < lists; ++j) r += Key{head_score[j], head_index[j]}.above(k);
+    if (r == a.K - 1) bound = k;
+  }
+  __syncthreads();
+  // what reaches the bound: prefixes of at most K lists
+  for (int l = tid; l < lists; l += NT) {
+    for (int j = 0; j < a.K; ++j) {
+      const Key k = key_at(l, j);
+      if (!k.score || bound.above(k)) break;
+      const int to = atomicAdd(&count, 1);
+      if (to < CAP2) list_score[to] = k.score, list_index[to] = k.index;
+    }
+  }
+  __syncthreads();
+  const int n = min(count, CAP2);
+  for (int e = tid; e < n; e += NT) {
+    const Key k = {list_score[e], list_index[e]};
+    int r = 0;
+    for (int j = 0; j < n; ++j) r += Key{list_score[j], list_index[j]}.above(k);
+    if (r < a.K) {
+      const uint32_t flat = ~k.index;
+      const u64 o = k.score;
+      a.tokens[b * a.K + r] = (int)(flat % (uint32_t)a.V);
+      a.parents[b * a.K + r] = (int)(flat / (uint32_t)a.V);
+      a.out_scores[b * a.K + r] =
+          (float)__longlong_as_double((long long)(o ^ (o >> 63 ? 0x8000000000000000ull : ~0ull)));
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- reorder
+struct ReorderArgs {
+  void *states[LANGUAGE_MAX_REORDERED];
+  long long bytes[LANGUAGE_MAX_REORDERED];
+  unsigned first[LANGUAGE_MAX_REORDERED + 1];  // workgroups of a request in front of tensor i
+  const int *parents;
+  int count, W;
+};
+
+// A thread holds the same few bytes of every beam of a request: it reads the parents' before it
+// writes, so the exchange needs no second buffer.  WM beams at most, T at a time.
+template <typename T, int WM>
+__device__ __forceinline__ void reorder_at(char *base, long long bytes, long long off, const int (&parent)[WM], int W) {
+  T v[WM];
+#pragma unroll
+  for (int w = 0; w < WM; ++w)
+    if (w < W && parent[w] != w) v[w] = *(const T *)(base + parent[w] * bytes + off);
+#pragma unroll
+  for (int w = 0; w < WM; ++w)
+    if (w < W && parent[w] != w) *(T *)(base + w * bytes + off) = v[w];
+}
+
+template <int WM>
+__global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs a) {
+  using Wide = std::conditional_t<(WM <= 16), uint4, std::conditional_t<(WM <= 32), uint2, uint32_t>>;
+  int i = 0;
+  while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) ++i;
+  const long long bytes = a.bytes[i], b = blockIdx.y;
+  char *base = (char *)a.states[i] + b * a.W * bytes;
+  int parent[WM];
+#pragma unroll
+  for (int w = 0; w < WM; ++w) {
+    parent[w] = w;
+    if (w < a.W) {
+      const int p = a.parents[b * a.W + w];
+      parent[w] = (unsigned)p < (unsigned)a.W ? p : w;
+    }
+  }
+  const long long at = (long long)(blockIdx.x - a.first[i]) * NT + threadIdx.x,
+                  step = (long long)(a.first[i + 1] - a.first[i]) * NT;
+  const unsigned low = (unsigned)(uintptr_t)a.states[i] | (unsigned)bytes;
+  if (low % sizeof(Wide) == 0)
+    for (long long e = at * sizeof(Wide); e < bytes; e += step * sizeof(Wide))
+      reorder_at<Wide, WM>(base, bytes, e, parent, a.W);
+  else if (low % 4 == 0)
+    for (long long e = at * 4; e < bytes; e += step * 4) reorder_at<uint32_t, WM>(base, bytes, e, parent, a.W);
+  else
+    for (long long e = at; e < bytes; e += step) reorder_at<uint8_t, WM>(base, bytes, e, parent, a.W);
+}
+
+// Elements of a row a thread keeps: 32 where that gives enough workgroups, else 8.
+int per_thread(long long rows, int V) { return rows * rec_cdiv(V, NT * 32) >= 256 ? 32 : 8; }
+
+struct SelectWs {
+  int slices;
+  size_t cands, bytes;
+};
+SelectWs select_ws(long long rows, int V, int K) {
+  SelectWs w;
+  w.slices = (int)rec_cdiv(V, NT * per_thread(rows, V));
+  w.cands = rec_align((size_t)rows * w.slices * sizeof(float2));
+  w.bytes = w.cands + rec_align((size_t)rows * w.slices * K * sizeof(Cand));
+  return w;
+}
+
+ret_status_t check_sizes(int B, int W, int V, int K) {
+  if (B < 0 || W <= 0 || V <= 0 || K <= 0) return rec_fail(RET_ERR_INVALID_ARG, "sizes must be positive");
+  if ((long long)W * V < K) return rec_fail(RET_ERR_INVALID_ARG, "K above W V");
+  if (W > LANGUAGE_MAX_BEAMS || K > LANGUAGE_MAX_BEAMS || V > LANGUAGE_MAX_VOCAB || (long long)B * W > (1LL << 24) ||
+      W * rec_cdiv(V, NT * 8) > LANGUAGE_MAX_BEAM_LISTS)
+    return rec_fail(RET_ERR_UNSUPPORTED, "B, W, V or K too large");
+  return RET_OK;
+}
+
+}  // namespace
+
+extern "C" size_t beam_select_workspace_bytes(int B, int W, int V, int K) {
+  if (check_sizes(B, W, V, K) != RET_OK || B == 0) return 0;
+  return select_ws((long long)B * W, V, K).bytes;
+}
+
+extern "C" ret_status_t beam_select(const void *logits, const float *scores, const unsigned char *ended, int *tokens,
+                                    int *parents, float *out_scores, int B, int W, int V, int K, long long logits_ld,
+                                    int eos, ret_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                    void *hip_stream) {
+  ret_status_t s = check_sizes(B, W, V, K);
+  if (s != RET_OK) return s;
+  if (!rec_dtype_ok(dtype)) return rec_fail(RET_ERR_INVALID_ARG, "unknown dtype");
+  if (logits_ld < V) return rec_fail(RET_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  if (ended && (eos < 0 || eos >= V)) return rec_fail(RET_ERR_INVALID_ARG, "eos outside 0..V-1");
+  if (logits_ld > (1LL << 31)) return rec_fail(RET_ERR_UNSUPPORTED, "logits_ld too large");
+  if (B == 0) return rec_status(hipSuccess);
+  if (!logits || !scores || !tokens || !parents || !out_scores)
+    return rec_fail(RET_ERR_INVALID_ARG, "NULL tensor pointer");
+  const long long rows = (long long)B * W;
+  const size_t e = rec_esize(dtype), picked = (size_t)B * K * 4;
+  if (!rec_aligned(logits, e) || !rec_aligned(scores, 4) || !rec_aligned(tokens, 4) || !rec_aligned(parents, 4) ||
+      !rec_aligned(out_scores, 4))
+    return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  const SelectWs w = select_ws(rows, V, K);
+  if (!workspace || workspace_bytes < w.bytes)
+    return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed", w.bytes);
+  const RecSpan ins[] = {rec_rows("logits", logits, rows, logits_ld, V, e), {"scores", scores, (size_t)rows * 4},
+                         {"ended", ended, (size_t)rows}};
+  const RecSpan outs[] = {{"tokens", tokens, picked}, {"parents", parents, picked}, {"out_scores", out_scores, picked},
+                          {"workspace", workspace, w.bytes}};
+  if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
+  if (!rec_aligned(workspace, 16)) return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  SelectArgs a = {};
+  a.logits = logits, a.scores = scores, a.ended = ended, a.tokens = tokens, a.parents = parents;
+  a.out_scores = out_scores, a.ld = logits_ld;
+  a.B = B, a.W = W, a.V = V, a.K = K, a.eos = eos, a.slices = w.slices;
+  a.sums = (float2 *)workspace;
+  a.cands = (Cand *)((char *)workspace + w.cands);
+  const dim3 grid((unsigned)w.slices, (unsigned)std::min<long long>(rows, 65535), (unsigned)rec_cdiv(rows, 65535));
+  hipStream_t st = (hipStream_t)hip_stream;
+  const bool many = per_thread(rows, V) == 32;
+  if (dtype == RET_BF16) {
+    if (many)
+      hipLaunchKernelGGL((slice_kernel<uint16_t, 32>), grid, dim3(NT), 0, st, a);
+    else
+      hipLaunchKernelGGL((slice_kernel<uint16_t, 8>), grid, dim3(NT), 0, st, a);
+  } else {
+    if (many)
+      hipLaunchKernelGGL((slice_kernel<float, 32>), grid, dim3(NT), 0, st, a);
+    else
+      hipLaunchKernelGGL((slice_kernel<float, 8>), grid, dim3(NT), 0, st, a);
+  }
+  hipLaunchKernelGGL(join_kernel, dim3((unsigned)B), dim3(NT), 0, st, a);
+  return rec_status(hipGetLastError());
+}
+
+extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes, int count, const int *parents, int B,
+                                     int W, void *hip_stream) {
+  if (count < 0 || B < 0 || W <= 0) return rec_fail(RET_ERR_INVALID_ARG, "sizes must be positive");
+  if (count > LANGUAGE_MAX_REORDERED || W > LANGUAGE_MAX_BEAMS || B > LANGUAGE_MAX_REORDER_BATCH)
+    return rec_fail(RET_ERR_UNSUPPORTED, "too many tensors, requests or beams");
+  if (count == 0 || B == 0) return rec_status(hipSuccess);
+  if (!states || !bytes || !parents) return rec_fail(RET_ERR_INVALID_ARG, "NULL pointer");
+  if (!rec_aligned(parents, 4)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  ReorderArgs a = {};
+  a.parents = parents, a.count = 0, a.W = W;
+  const RecSpan par = {"parents", parents, (size_t)B * W * 4};
+  RecSpan all[LANGUAGE_MAX_REORDERED];
+  unsigned blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    if (bytes[i] < 0) return rec_fail(RET_ERR_INVALID_ARG, "sizes must be positive");
+    if (bytes[i] > (1LL << 40) || (double)bytes[i] * B * W > (double)(1LL << 44))
+      return rec_fail(RET_ERR_UNSUPPORTED, "a tensor is too large");
+    if (bytes[i] == 0) continue;
+    if (!states[i]) return rec_fail(RET_ERR_INVALID_ARG, "NULL tensor pointer");
+    const int n = a.count++;
+    all[n] = {"a tensor", states[i], (size_t)bytes[i] * B * W};
+    if (rec_overlap(all[n], par)) return rec_fail(RET_ERR_INVALID_ARG, "a tensor overlaps parents");
+    for (int j = 0; j < n; ++j)
+      if (rec_overlap(all[n], all[j])) return rec_fail(RET_ERR_INVALID_ARG, "two tensors overlap");
+    a.states[n] = states[i];
+    a.bytes[n] = bytes[i];
+    a.first[n] = blocks;
+    blocks += (unsigned)std::min<long long>(4096, rec_cdiv(bytes[i], NT * 16));
+    a.first[n + 1] = blocks;
+  }
+  if (a.count == 0) return rec_status(hipSuccess);
+  if (!rec_grid_ok((double)blocks * B, NT)) return rec_fail(RET_ERR_UNSUPPORTED, "too many workgroups for one launch");
+  const dim3 grid(blocks, (unsigned)B);
+  hipStream_t st = (hipStream_t)hip_stream;
+  if (W <= 4)
+    hipLaunchKernelGGL((reorder_kernel<4>), grid, dim3(NT), 0, st, a);
+  else if (W <= 8)
+    hipLaunchKernelGGL((reorder_kernel<8>), grid, dim3(NT), 0, st, a);
+  else if (W <= 16)
+    hipLaunchKernelGGL((reorder_kernel<16>), grid, dim3(NT), 0, st, a);
+  else if (W <= 32)
+    hipLaunchKernelGGL((reorder_kernel<32>), grid, dim3(NT), 0, st, a);
+  else
+    hipLaunchKernelGGL((reorder_kernel<64>), grid, dim3(NT), 0, st, a);
+  return rec_status(hipGetLastError());
+}

@@ -1,0 +1,294 @@
+// Scaled embedding and its gradient by sorted tokens (language.h).
+//
+// The lookup streams: eight elements a thread, each moved once.
+//
+// The gradient of a row is a sum over the tokens that name it, in their order.  Three launches:
+//   1. Sort.  Each workgroup owns a range of ids and reads all tokens twice: once to count, once to
+//      place.  What lies below its range tells where its part of the order begins, so the
+//      workgroups need nothing from each other.
+//   2. Long runs.  Tokens come with the frequencies of words, so one id can have a tenth of them.  The
+//      order is cut into pieces of `piece` tokens, and runs longer than one are summed piece by piece.
+//   3. Rows.  Every row of the table's gradient is written once: the sum of a short run's tokens or of
+//      a long run's pieces, or zero.
+#include <algorithm>
+
+#include "language.hpp"
+
+using namespace ret;
+
+namespace {
+
+constexpr int NT = 256;
+
+// ------------------------------------------------------------------------------ lookup
+// Threads of a row: tpr (a power of two up to NT); a workgroup takes NT / tpr rows at a time.
+template <typename TI, typename TO>
+__global__ __launch_bounds__(NT) void lookup_kernel(const int *ids, const TI *table, TO *out, long long n, int V, int D,
+                                                    int tpr, float scale) {
+  const int col = threadIdx.x & (tpr - 1), rows = NT / tpr;
+  const long long t = (long long)blockIdx.x * rows + threadIdx.x / tpr;
+  if (t >= n) return;
+  const int id = ids[t];
+  const bool in = (unsigned)id < (unsigned)V;
+  const TI *src = table + (long long)(in ? id : 0) * D;
+  TO *dst = out + t * D;
+  for (int c = col * 8; c < D; c += tpr * 8) {
+    float r[8];
+    load8(src + c, in ? D - c : 0, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = in ? r[i] * scale : 0.0f;
+    store8(dst + c, D - c, r);
+  }
+}
+
+// -------------------------------------------------------------------------------- sort
+constexpr int SORT_NT = 1024, SORT_WAVES = SORT_NT / 64;
+constexpr int MAX_RANGE = 512;  // ids of a workgroup: 32 KB of counters
+
+// order[j]: the token at place j of the order by (id, token); start[v]: the place of v's first
+// token, start[V] their number.  Wave w of a workgroup reads the w-th part of the tokens.
+__global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *order, int *start, int n, int V, int range) {
+  __shared__ int at[SORT_WAVES][MAX_RANGE];  // tokens of a wave for an id, then where its next one goes
+  __shared__ int red[SORT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int v0 = blockIdx.x * range, mine = min(range, V - v0);
+  const int part = ((n + SORT_WAVES * 64 - 1) / (SORT_WAVES * 64)) * 64;
+  const long long lo = (long long)wave * part, hi = lo + part < n ? lo + part : n;
+  for (int i = tid; i < SORT_WAVES * MAX_RANGE; i += SORT_NT) (&at[0][0])[i] = 0;
+  __syncthreads();
+  int below = 0;
+  for (long long t = lo + lane; t < hi; t += 64) {
+    const int id = ids[t];
+    below += id >= 0 && id < v0;
+    if (id >= v0 && id < v0 + mine) atomicAdd(&at[wave][id - v0], 1);
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off, 64);
+  if (lane == 0) red[wave] = below;
+  __syncthreads();
+  // wave 0: the counts' running sum over (id, wave), from the tokens below the range on
+  if (wave == 0) {
+    int base = 0;
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) base += red[w];
+    for (int i0 = 0; i0 < mine; i0 += 64) {
+      const int i = i0 + lane;
+      int sum = 0;
+      if (i < mine)
+#pragma unroll
+        for (int w = 0; w < SORT_WAVES; ++w) sum += at[w][i];
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int up = __shfl_up(incl, off, 64);
+        if (lane >= off) incl += up;
+      }
+      int p = base + incl - sum;
+      if (i < mine) {
+        start[v0 + i] = p;
+#pragma unroll
+        for (int w = 0; w < SORT_WAVES; ++w) {
+          const int c = at[w][i];
+          at[w][i] = p;
+          p += c;
+        }
+      }
+      base += __shfl(incl, 63, 64);
+    }
+    if (v0 + mine == V && lane == 0) start[V] = base;
+  }
+  __syncthreads();
+  for (long long t0 = lo; t0 < hi; t0 += 64) {
+    const long long t = t0 + lane;
+    const int id = t < hi ? ids[t] : -1;
+    unsigned long long todo = __ballot(id >= v0 && id < v0 + mine);
+    while (todo) {  // each different id of these tokens: its lanes in order
+      const int leader = __ffsll((long long)todo) - 1, v = __shfl(id, leader, 64);
+      const unsigned long long same = __ballot(id == v);
+      int to = 0;
+      if (lane == leader) to = atomicAdd(&at[wave][v - v0], __popcll(same));
+      to = __shfl(to, leader, 64);
+      if (id == v) order[to + __popcll(same & ((1ull << lane) - 1))] = (int)t;
+      todo &= ~same;
+    }
+  }
+}
+
+// -------------------------------------------------------------------------------- sums
+template <typename TI>
+__device__ __forceinline__ void add_tokens(const TI *d_o, const int *order, int from, int to, long long ld, int c, int n,
+                                           float (&sum)[8]) {
+  int j = from;
+  for (; j + 4 <= to; j += 4) {
+    float r[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) load8(d_o + order[j + u] * ld + c, n, r[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += r[u][i];
+  }
+  for (; j < to; ++j) {
+    float r[8];
+    load8(d_o + order[j] * ld + c, n, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += r[i];
+  }
+}
+
+// Piece blockIdx.x of the order: the part of the run that its first place belongs to, and of the run
+// that its last place belongs to where that is another, each only if the run is longer than a piece.
+template <typename TI>
+__global__ __launch_bounds__(NT) void piece_kernel(const int *ids, const TI *d_o, const int *order, const int *start,
+                                                   float *part, int V, int D, long long ld, int piece) {
+  const int total = start[V], j0 = blockIdx.x * piece, j1 = min(j0 + piece, total);
+  if (j0 >= j1) return;
+  const int c = (blockIdx.y * NT + threadIdx.x) * 8;
+  const int a = ids[order[j0]], z = ids[order[j1 - 1]];
+#pragma unroll
+  for (int slot = 0; slot < 2; ++slot) {
+    if (slot == 1 && z == a) break;
+    const int v = slot ? z : a, s = start[v], e = start[v + 1];
+    if (e - s <= piece || c >= D) continue;
+    float sum[8] = {};
+    add_tokens(d_o, order, max(s, j0), min(e, j1), ld, c, D - c, sum);
+    store8(part + (2LL * blockIdx.x + slot) * D + c, D - c, sum);
+  }
+}
+
+template <typename TI, typename TO>
+__global__ __launch_bounds__(NT) void rows_kernel(const TI *d_o, const int *order, const int *start, const float *part,
+                                                  TO *dtable, int V, int D, long long ld, int piece, int tpr,
+                                                  float scale) {
+  const int col = threadIdx.x & (tpr - 1), rows = NT / tpr;
+  const int v = blockIdx.x * rows + threadIdx.x / tpr;
+  if (v >= V) return;
+  const int s = start ? start[v] : 0, e = start ? start[v + 1] : 0;
+  for (int c = col * 8; c < D; c += tpr * 8) {
+    float sum[8] = {};
+    if (e - s <= piece) {
+      add_tokens(d_o, order, s, e, ld, c, D - c, sum);
+    } else {
+      // a run that begins inside its first piece is that piece's second slot
+      const int p0 = s / piece, p1 = (e - 1) / piece;
+      for (int p = p0; p <= p1; ++p) {
+        float r[8];
+        load8(part + (2LL * p + (p == p0 && s % piece != 0)) * D + c, D - c, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += r[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] *= scale;
+    store8(dtable + (long long)v * D + c, D - c, sum);
+  }
+}
+
+int threads_per_row(int D) {
+  int t = 1;
+  while (t < NT && t * 8 < D) t *= 2;
+  return t;
+}
+
+// Tokens of a piece: about the square root of their number, so that neither a piece nor the list of
+// pieces of one id is long.
+int piece_of(long long n) {
+  int p = 32;
+  while ((long long)p * p < n) p *= 2;
+  return p;
+}
+
+struct EmbedWs {
+  size_t order, start, part, bytes;
+};
+EmbedWs embed_ws(long long n, int V, int D) {
+  EmbedWs w;
+  w.order = 0;
+  w.start = rec_align((size_t)n * 4);
+  w.part = w.start + rec_align(((size_t)V + 1) * 4);
+  w.bytes = w.part + rec_align((size_t)rec_cdiv(n, piece_of(n)) * 2 * D * 4);
+  return w;
+}
+
+ret_status_t check_sizes(long long n, int V, int D, ret_dtype_t in, ret_dtype_t out) {
+  if (n < 0 || V <= 0 || D <= 0) return rec_fail(RET_ERR_INVALID_ARG, "sizes must be positive");
+  if (!rec_dtype_ok(in) || !rec_dtype_ok(out)) return rec_fail(RET_ERR_INVALID_ARG, "unknown dtype");
+  if (n > LANGUAGE_MAX_TOKENS || V > LANGUAGE_MAX_VOCAB || D > LANGUAGE_MAX_CHANNELS ||
+      n * D > LANGUAGE_MAX_ELEMENTS || (long long)V * D > LANGUAGE_MAX_ELEMENTS)
+    return rec_fail(RET_ERR_UNSUPPORTED, "n, V or D too large");
+  const int rows = NT / threads_per_row(D);
+  if (!rec_grid_ok((double)rec_cdiv(std::max<long long>(n, V), rows), NT))
+    return rec_fail(RET_ERR_UNSUPPORTED, "too many rows for one launch");
+  return RET_OK;
+}
+
+}  // namespace
+
+extern "C" ret_status_t embedding(const int *ids, const void *table, void *out, long long n, int V, int D, float scale,
+                                  ret_dtype_t in_dtype, ret_dtype_t out_dtype, void *hip_stream) {
+  ret_status_t s = check_sizes(n, V, D, in_dtype, out_dtype);
+  if (s != RET_OK) return s;
+  if (n == 0) return rec_status(hipSuccess);
+  if (!ids || !table || !out) return rec_fail(RET_ERR_INVALID_ARG, "NULL tensor pointer");
+  const size_t ie = rec_esize(in_dtype), oe = rec_esize(out_dtype);
+  if (!rec_aligned(ids, 4) || !rec_aligned(table, ie) || !rec_aligned(out, oe))
+    return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  const RecSpan ins[] = {{"ids", ids, (size_t)n * 4}, {"table", table, (size_t)V * D * ie}};
+  const RecSpan outs[] = {{"out", out, (size_t)n * D * oe}};
+  if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
+  const int tpr = threads_per_row(D);
+  const unsigned grid = (unsigned)rec_cdiv(n, NT / tpr);
+  return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
+    hipLaunchKernelGGL((lookup_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>>),
+                       dim3(grid), dim3(NT), 0, (hipStream_t)hip_stream, ids, (decltype(ti))table, (decltype(to))out, n,
+                       V, D, tpr, scale);
+    return hipGetLastError();
+  }));
+}
+
+extern "C" size_t embedding_bwd_workspace_bytes(long long n, int V, int D) {
+  if (check_sizes(n, V, D, RET_F32, RET_F32) != RET_OK || n == 0) return 0;
+  return embed_ws(n, V, D).bytes;
+}
+
+extern "C" ret_status_t embedding_bwd(const int *ids, const void *d_o, void *dtable, long long n, int V, int D,
+                                      long long o_ld, float scale, ret_dtype_t in_dtype, ret_dtype_t out_dtype,
+                                      void *workspace, size_t workspace_bytes, void *hip_stream) {
+  ret_status_t s = check_sizes(n, V, D, in_dtype, out_dtype);
+  if (s != RET_OK) return s;
+  if (o_ld < D) return rec_fail(RET_ERR_INVALID_ARG, "a row stride is shorter than its row");
+  if (o_ld > (1LL << 31)) return rec_fail(RET_ERR_UNSUPPORTED, "o_ld too large");
+  if (!dtable || (n > 0 && (!ids || !d_o))) return rec_fail(RET_ERR_INVALID_ARG, "NULL tensor pointer");
+  const size_t ie = rec_esize(in_dtype), oe = rec_esize(out_dtype);
+  if (!rec_aligned(ids, 4) || !rec_aligned(d_o, ie) || !rec_aligned(dtable, oe))
+    return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
+  const EmbedWs w = embed_ws(n, V, D);
+  if (n > 0) {
+    if (!workspace || workspace_bytes < w.bytes)
+      return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed", w.bytes);
+    const RecSpan ins[] = {{"ids", ids, (size_t)n * 4}, rec_rows("d_o", d_o, n, o_ld, D, ie)};
+    const RecSpan outs[] = {{"dtable", dtable, (size_t)V * D * oe}, {"workspace", workspace, w.bytes}};
+    if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
+    if (!rec_aligned(workspace, 16)) return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  }
+  hipStream_t st = (hipStream_t)hip_stream;
+  char *ws = (char *)workspace;
+  int *order = n ? (int *)(ws + w.order) : nullptr, *start = n ? (int *)(ws + w.start) : nullptr;
+  float *part = n ? (float *)(ws + w.part) : nullptr;
+  const int piece = piece_of(n), tpr = threads_per_row(D);
+  if (n > 0) {
+    const int range = (int)std::min<long long>(MAX_RANGE, std::max<long long>(1, rec_cdiv(V, 256)));
+    hipLaunchKernelGGL(sort_kernel, dim3((unsigned)rec_cdiv(V, range)), dim3(SORT_NT), 0, st, ids, order, start, (int)n,
+                       V, range);
+  }
+  return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
+    using TI = std::remove_pointer_t<decltype(ti)>;
+    using TO = std::remove_pointer_t<decltype(to)>;
+    if (n > piece)
+      hipLaunchKernelGGL((piece_kernel<TI>), dim3((unsigned)rec_cdiv(n, piece), (unsigned)rec_cdiv(D, NT * 8)), dim3(NT),
+                         0, st, ids, (const TI *)d_o, order, start, part, V, D, o_ld, piece);
+    hipLaunchKernelGGL((rows_kernel<TI, TO>), dim3((unsigned)rec_cdiv(V, NT / tpr)), dim3(NT), 0, st, (const TI *)d_o,
+                       order, start, part, (TO *)dtable, V, D, o_ld, piece, tpr, scale);
+    return hipGetLastError();
+  }));
+}
