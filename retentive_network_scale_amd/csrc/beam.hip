@@ -3,11 +3,15 @@
 //
 // Selection takes two launches.  The first reads the logits once: a workgroup keeps a slice of one
 // beam's row in registers, leaves the slice's maximum and sum of exponentials, and its K best
-// logits in order.  To find those, every thread's best value is ranked among the workgroup's; the
-// K-th of them is a bound that at least K elements reach and few pass, and those that
-// reach it are ranked by counting.  Values are ordered together with their indices, as one whole
-// number, so that none are equal.  The second launch, a workgroup a request, joins the slices'
-// sums to the beams' log-sums and does the same with the lists' heads and the lists.
+// logits in order.  To find those, each wave takes the K-th best of its lanes' best values, found bit by
+// bit, and the workgroup the largest of these as a bound: at least K elements reach it and few others.
+// Those are gathered and ranked by counting, ordered by value and index as one whole number, so that none
+// are equal.  Where more reach it than there is room for (rows of equal values), the bound is found again
+// from the lanes' best as such whole numbers, which at most K lanes reach.
+// The second launch, a workgroup a request, joins the slices' sums to the beams' log-sums and does the
+// same with the lists' heads and the lists.
+// Bound by the vector unit's work on an element (exponential, two comparisons): ranking all 256 lanes' best by
+// counting took three times as long (64 requests, 8 beams, 32000 bf16 logits: 29 us).
 #include <math.h>
 
 #include <algorithm>
@@ -51,13 +55,28 @@ __device__ __forceinline__ u64 ordered(double v) {
 // -0 is 0: the two compare equal, and the index has to decide.
 __device__ __forceinline__ u64 key_of(float v, int index) { return (u64)ordered(v + 0.0f) << 32 | (uint32_t)~index; }
 
+// The K-th largest of the lanes' values (K <= 64) as a whole number in their order.
+__device__ __forceinline__ uint32_t kth_of_wave(uint32_t mine, int K) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | 1u << bit;
+    if (__popcll(__ballot(mine >= c)) >= K) t = c;
+  }
+  return t;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu));
+}
+
 // E elements of a row a thread, in E / 8 chunks.
 template <typename T, int E>
 __global__ __launch_bounds__(NT) void slice_kernel(SelectArgs a) {
-  constexpr int CAP = MAXK * E;  // elements that can reach the bound: of the K - 1 threads with a better one, and one more
-  __shared__ u64 best[NT];
+  constexpr int CAP = MAXK * E;  // elements that can reach an exact bound: of K - 1 threads with a better one, and one more
   __shared__ u64 list[CAP];
+  __shared__ u64 best[NT];
   __shared__ float red[NT / 64];
+  __shared__ uint32_t kth[NT / 64];
   __shared__ u64 bound;
   __shared__ int count;
   const int tid = threadIdx.x, slice = blockIdx.x;
@@ -67,75 +86,99 @@ __global__ __launch_bounds__(NT) void slice_kernel(SelectArgs a) {
   if ((a.ended && a.ended[row]) || !isfinite(a.scores[row])) return;
   const int first = slice * (NT * E);
   const T *src = (const T *)a.logits + row * a.ld;
-  float x[E / 8][8];
+  float x[E / 8][8];  // -inf behind the row's end
+  if (first + NT * E <= a.V) {
 #pragma unroll
-  for (int c = 0; c < E / 8; ++c) {
-    const int at = first + (c * NT + tid) * 8;
-    load8(src + at, a.V - at, x[c]);
+    for (int c = 0; c < E / 8; ++c) load8(src + first + (c * NT + tid) * 8, x[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c) {
+      const int left = a.V - first - (c * NT + tid) * 8;
+      load8(src + first + (c * NT + tid) * 8, left, x[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[c][i] = i < left ? x[c][i] : -INFINITY;
+    }
   }
-  u64 mine = 0;
-  float m = -INFINITY;
+  float top = -INFINITY;  // of the thread; passes over NaN, which spoils the sum
 #pragma unroll
   for (int c = 0; c < E / 8; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = first + (c * NT + tid) * 8 + i;
-      if (at < a.V) {
-        const u64 k = key_of(x[c][i], at);
-        mine = k > mine ? k : mine;
-        m = fmaxf(m, x[c][i]);
-      }
-    }
-  best[tid] = mine;
-  if (tid == 0) bound = 0, count = 0;
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, x[c][i]);
+  const uint32_t t = kth_of_wave(ordered(top + 0.0f), a.K);
+  float m = top;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if ((tid & 63) == 0) red[tid >> 6] = m;
+  if ((tid & 63) == 0) red[tid >> 6] = m, kth[tid >> 6] = t;
+  if (tid == 0) bound = 0, count = 0;
   __syncthreads();
   m = red[0];
+  uint32_t most = kth[0];
 #pragma unroll
-  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[w]);
-  // the rank of the thread's best
-  int rank = 0;
-#pragma unroll 8
-  for (int j = 0; j < NT; ++j) rank += best[j] > mine;
-  if (mine && rank == a.K - 1) bound = mine;
-  // sum of exponentials; a maximum that is not finite (or a NaN, which fmaxf passes over) shows in the sum
-  float s = 0.0f;
+  for (int w = 1; w < NT / 64; ++w) m = fmaxf(m, red[w]), most = max(most, kth[w]);
+  const float least = value_of(most);
+  // gather what reaches the bound
+  auto put = [&](u64 k) {
+    const int to = atomicAdd(&count, 1);
+    if (to < CAP) list[to] = k;
+  };
+  if (top >= least)
 #pragma unroll
-  for (int c = 0; c < E / 8; ++c)
+    for (int c = 0; c < E / 8; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = first + (c * NT + tid) * 8 + i;
-      if (at < a.V) s += m == -INFINITY ? (x[c][i] == x[c][i] ? 0.0f : x[c][i]) : expf(x[c][i] - m);
-    }
-  __syncthreads();  // red is read, bound written
-  s = block_sum<NT>(s, red);
-  const u64 least = bound;
-#pragma unroll
-  for (int c = 0; c < E / 8; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = first + (c * NT + tid) * 8 + i;
-      if (at < a.V) {
-        const u64 k = key_of(x[c][i], at);
-        if (k >= least) {
-          const int to = atomicAdd(&count, 1);
-          if (to < CAP) list[to] = k;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int at = first + (c * NT + tid) * 8 + i;
+        if (x[c][i] >= least && at < a.V) put(key_of(x[c][i], at));
       }
-    }
-  __syncthreads();
-  const int n = min(count, CAP);
+  // sum of exponentials; a maximum that is not finite, or a NaN, shows in the sum
+  float s = 0.0f;
+  if (m == -INFINITY) {
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[c][i] == x[c][i] ? 0.0f : x[c][i];
+  } else {
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += __builtin_amdgcn_exp2f((x[c][i] - m) * kLog2e);
+  }
+  __syncthreads();  // red is read, the list written
+  s = block_sum<NT>(s, red);
+  int n = count;
+  if (n > CAP) {  // the same for all threads
+    u64 mine = 0;
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = first + (c * NT + tid) * 8 + i;
+        const u64 k = at < a.V ? key_of(x[c][i], at) : 0;
+        mine = k > mine ? k : mine;
+      }
+    best[tid] = mine;
+    __syncthreads();
+    if (tid == 0) count = 0;
+    int rank = 0;
+    for (int j = 0; j < NT; ++j) rank += best[j] > mine;
+    if (mine && rank == a.K - 1) bound = mine;
+    __syncthreads();
+    const u64 b = bound;
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = first + (c * NT + tid) * 8 + i;
+        if (at < a.V && key_of(x[c][i], at) >= b) put(key_of(x[c][i], at));
+      }
+    __syncthreads();
+    n = count;
+  }
   Cand *out = a.cands + (row * a.slices + slice) * a.K;
   for (int e = tid; e < n; e += NT) {
     const u64 k = list[e];
     int r = 0;
     for (int j = 0; j < n; ++j) r += list[j] > k;
-    if (r < a.K) {
-      const uint32_t o = (uint32_t)(k >> 32);
-      out[r] = {__uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xffffffffu)), (int)~(uint32_t)k};
-    }
+    if (r < a.K) out[r] = {value_of((uint32_t)(k >> 32)), (int)~(uint32_t)k};
   }
   for (int e = n + tid; e < a.K; e += NT) out[e] = {0.0f, -1};
   if (tid == 0) a.sums[row * a.slices + slice] = make_float2(m, s);
@@ -163,20 +206,30 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
   __shared__ int count;
   const int tid = threadIdx.x;
   const long long b = blockIdx.x;
-  if (tid < a.W) {
-    const long long row = b * a.W + tid;
+  // a beam's log-sum by a wave, its slices by the lanes
+  for (int w = tid >> 6; w < a.W; w += NT / 64) {
+    const long long row = b * a.W + w;
     const float own = a.scores[row];
+    const bool end = a.ended && a.ended[row];
     float m = -INFINITY;
-    for (int i = 0; i < a.slices; ++i) m = fmaxf(m, a.sums[row * a.slices + i].x);
     double s = 0.0;
-    for (int i = 0; i < a.slices; ++i) {
-      const float2 v = a.sums[row * a.slices + i];
-      // a slice of nothing but -inf adds its sum, 0 or NaN
-      s += v.x == -INFINITY ? (double)v.y : (double)v.y * exp((double)v.x - (double)m);
+    if (!end && isfinite(own)) {
+      for (int i = tid & 63; i < a.slices; i += 64) m = fmaxf(m, a.sums[row * a.slices + i].x);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+      for (int i = tid & 63; i < a.slices; i += 64) {
+        const float2 v = a.sums[row * a.slices + i];
+        // a slice of nothing but -inf adds its sum, 0 or NaN
+        s += v.x == -INFINITY ? (double)v.y : (double)v.y * exp((double)v.x - (double)m);
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
     }
-    const double l = (double)m + log(s);
-    lse[tid] = l;
-    kind[tid] = !isfinite(own) ? 2 : a.ended && a.ended[row] ? 1 : isfinite(l) ? 0 : 2;
+    if ((tid & 63) == 0) {
+      const double l = (double)m + log(s);
+      lse[w] = l;
+      kind[w] = !isfinite(own) ? 2 : end ? 1 : isfinite(l) ? 0 : 2;
+    }
   }
   if (tid == 0) bound = {0, 0}, count = 0;
   __syncthreads();
@@ -243,10 +296,13 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
 }
 
 // ----------------------------------------------------------------------------- reorder
+// MT tensors at most: of few all arguments are read at once, in one trip to the memory they lie in (two tensors
+// of 131 KB a beam: 8.8 us with arguments for 64, read one after the other).
+template <int MT>
 struct ReorderArgs {
-  void *states[LANGUAGE_MAX_REORDERED];
-  long long bytes[LANGUAGE_MAX_REORDERED];
-  unsigned first[LANGUAGE_MAX_REORDERED + 1];  // workgroups of a request in front of tensor i
+  void *states[MT];
+  long long bytes[MT];
+  unsigned first[MT + 1];  // workgroups of a request in front of tensor i
   const int *parents;
   int count, W;
 };
@@ -264,13 +320,24 @@ __device__ __forceinline__ void reorder_at(char *base, long long bytes, long lon
     if (w < W && parent[w] != w) *(T *)(base + w * bytes + off) = v[w];
 }
 
-template <int WM>
-__global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs a) {
+template <int WM, int MT>
+__global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs<MT> a) {
   using Wide = std::conditional_t<(WM <= 16), uint4, std::conditional_t<(WM <= 32), uint2, uint32_t>>;
-  int i = 0;
-  while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) ++i;
-  const long long bytes = a.bytes[i], b = blockIdx.y;
-  char *base = (char *)a.states[i] + b * a.W * bytes;
+  const long long b = blockIdx.y;
+  long long bytes = a.bytes[0];
+  char *tensor = (char *)a.states[0];
+  unsigned from = 0, to = a.first[1];
+  if constexpr (MT <= 4) {
+#pragma unroll
+    for (int i = 1; i < MT; ++i)
+      if (i < a.count && blockIdx.x >= a.first[i])
+        bytes = a.bytes[i], tensor = (char *)a.states[i], from = a.first[i], to = a.first[i + 1];
+  } else {
+    int i = 0;
+    while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) ++i;
+    bytes = a.bytes[i], tensor = (char *)a.states[i], from = a.first[i], to = a.first[i + 1];
+  }
+  char *base = tensor + b * a.W * bytes;
   int parent[WM];
 #pragma unroll
   for (int w = 0; w < WM; ++w) {
@@ -280,9 +347,8 @@ __global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs a) {
       parent[w] = (unsigned)p < (unsigned)a.W ? p : w;
     }
   }
-  const long long at = (long long)(blockIdx.x - a.first[i]) * NT + threadIdx.x,
-                  step = (long long)(a.first[i + 1] - a.first[i]) * NT;
-  const unsigned low = (unsigned)(uintptr_t)a.states[i] | (unsigned)bytes;
+  const long long at = (long long)(blockIdx.x - from) * NT + threadIdx.x, step = (long long)(to - from) * NT;
+  const unsigned low = (unsigned)(uintptr_t)tensor | (unsigned)bytes;
   if (low % sizeof(Wide) == 0)
     for (long long e = at * sizeof(Wide); e < bytes; e += step * sizeof(Wide))
       reorder_at<Wide, WM>(base, bytes, e, parent, a.W);
@@ -290,6 +356,21 @@ __global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs a) {
     for (long long e = at * 4; e < bytes; e += step * 4) reorder_at<uint32_t, WM>(base, bytes, e, parent, a.W);
   else
     for (long long e = at; e < bytes; e += step) reorder_at<uint8_t, WM>(base, bytes, e, parent, a.W);
+}
+
+template <int MT>
+hipError_t launch_reorder(const ReorderArgs<MT> &a, dim3 grid, hipStream_t st) {
+  if (a.W <= 4)
+    hipLaunchKernelGGL((reorder_kernel<4, MT>), grid, dim3(NT), 0, st, a);
+  else if (a.W <= 8)
+    hipLaunchKernelGGL((reorder_kernel<8, MT>), grid, dim3(NT), 0, st, a);
+  else if (a.W <= 16)
+    hipLaunchKernelGGL((reorder_kernel<16, MT>), grid, dim3(NT), 0, st, a);
+  else if (a.W <= 32)
+    hipLaunchKernelGGL((reorder_kernel<32, MT>), grid, dim3(NT), 0, st, a);
+  else
+    hipLaunchKernelGGL((reorder_kernel<64, MT>), grid, dim3(NT), 0, st, a);
+  return hipGetLastError();
 }
 
 // Elements of a row a thread keeps: 32 where that gives enough workgroups, else 8.
@@ -382,7 +463,7 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
   if (count == 0 || B == 0) return rec_status(hipSuccess);
   if (!states || !bytes || !parents) return rec_fail(RET_ERR_INVALID_ARG, "NULL pointer");
   if (!rec_aligned(parents, 4)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  ReorderArgs a = {};
+  ReorderArgs<LANGUAGE_MAX_REORDERED> a = {};
   a.parents = parents, a.count = 0, a.W = W;
   const RecSpan par = {"parents", parents, (size_t)B * W * 4};
   RecSpan all[LANGUAGE_MAX_REORDERED];
@@ -408,15 +489,9 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
   if (!rec_grid_ok((double)blocks * B, NT)) return rec_fail(RET_ERR_UNSUPPORTED, "too many workgroups for one launch");
   const dim3 grid(blocks, (unsigned)B);
   hipStream_t st = (hipStream_t)hip_stream;
-  if (W <= 4)
-    hipLaunchKernelGGL((reorder_kernel<4>), grid, dim3(NT), 0, st, a);
-  else if (W <= 8)
-    hipLaunchKernelGGL((reorder_kernel<8>), grid, dim3(NT), 0, st, a);
-  else if (W <= 16)
-    hipLaunchKernelGGL((reorder_kernel<16>), grid, dim3(NT), 0, st, a);
-  else if (W <= 32)
-    hipLaunchKernelGGL((reorder_kernel<32>), grid, dim3(NT), 0, st, a);
-  else
-    hipLaunchKernelGGL((reorder_kernel<64>), grid, dim3(NT), 0, st, a);
-  return rec_status(hipGetLastError());
+  if (a.count > 4) return rec_status(launch_reorder(a, grid, st));
+  ReorderArgs<4> few = {};
+  for (int i = 0; i < a.count; ++i) few.states[i] = a.states[i], few.bytes[i] = a.bytes[i], few.first[i + 1] = a.first[i + 1];
+  few.parents = parents, few.count = a.count, few.W = W;
+  return rec_status(launch_reorder(few, grid, st));
 }

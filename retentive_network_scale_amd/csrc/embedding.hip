@@ -11,6 +11,7 @@
 //   3. Rows.  Every row of the table's gradient is written once: the sum of a short run's tokens or of
 //      a long run's pieces, or zero.
 #include <algorithm>
+#include <type_traits>
 
 #include "language.hpp"
 
@@ -46,15 +47,17 @@ constexpr int SORT_NT = 1024, SORT_WAVES = SORT_NT / 64;
 constexpr int MAX_RANGE = 512;  // ids of a workgroup: 32 KB of counters
 
 // order[j]: the token at place j of the order by (id, token); start[v]: the place of v's first
-// token, start[V] their number.  Wave w of a workgroup reads the w-th part of the tokens.
-__global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *order, int *start, int n, int V, int range) {
+// token, start[V] their number.  Wave w of a workgroup reads the w-th part of the tokens; `bits` is the
+// width of an id within the range.
+__global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *order, int *start, int n, int V, int range,
+                                                       int bits) {
   __shared__ int at[SORT_WAVES][MAX_RANGE];  // tokens of a wave for an id, then where its next one goes
   __shared__ int red[SORT_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int v0 = blockIdx.x * range, mine = min(range, V - v0);
   const int part = ((n + SORT_WAVES * 64 - 1) / (SORT_WAVES * 64)) * 64;
   const long long lo = (long long)wave * part, hi = lo + part < n ? lo + part : n;
-  for (int i = tid; i < SORT_WAVES * MAX_RANGE; i += SORT_NT) (&at[0][0])[i] = 0;
+  for (int i = lane; i < mine; i += 64) at[wave][i] = 0;
   __syncthreads();
   int below = 0;
   for (long long t = lo + lane; t < hi; t += 64) {
@@ -101,38 +104,53 @@ __global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *orde
   for (long long t0 = lo; t0 < hi; t0 += 64) {
     const long long t = t0 + lane;
     const int id = t < hi ? ids[t] : -1;
-    unsigned long long todo = __ballot(id >= v0 && id < v0 + mine);
-    while (todo) {  // each different id of these tokens: its lanes in order
-      const int leader = __ffsll((long long)todo) - 1, v = __shfl(id, leader, 64);
-      const unsigned long long same = __ballot(id == v);
-      int to = 0;
-      if (lane == leader) to = atomicAdd(&at[wave][v - v0], __popcll(same));
-      to = __shfl(to, leader, 64);
-      if (id == v) order[to + __popcll(same & ((1ull << lane) - 1))] = (int)t;
-      todo &= ~same;
+    const bool in = id >= v0 && id < v0 + mine;
+    unsigned long long same = __ballot(in);  // the lanes of the same id, from one comparison a bit
+    if (!same) continue;
+    for (int bit = 0; bit < bits; ++bit) {
+      const bool one = (unsigned)(id - v0) >> bit & 1u;
+      const unsigned long long set = __ballot(one);
+      same &= one ? set : ~set;
     }
+    // the first lane of an id takes the places of all of them
+    const int leader = __ffsll((long long)same) - 1;
+    int to = 0;
+    if (in && lane == leader) to = atomicAdd(&at[wave][id - v0], __popcll(same));
+    to = __shfl(to, leader, 64);
+    if (in) order[to + __popcll(same & ((1ull << lane) - 1))] = (int)t;
   }
 }
 
 // -------------------------------------------------------------------------------- sums
-template <typename TI>
-__device__ __forceinline__ void add_tokens(const TI *d_o, const int *order, int from, int to, long long ld, int c, int n,
-                                           float (&sum)[8]) {
+// Adds the tokens order[from .. to) to CH chunks of eight columns, the first at c, chunk k `step` further on.
+template <typename TI, int CH, int AHEAD>
+__device__ __forceinline__ void add_tokens(const TI *d_o, const int *order, int from, int to, long long ld, int c,
+                                           int step, int D, float (&sum)[CH][8]) {
   int j = from;
-  for (; j + 4 <= to; j += 4) {
-    float r[4][8];
+  for (; j + AHEAD <= to; j += AHEAD) {
+    float r[AHEAD][CH][8];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) load8(d_o + order[j + u] * ld + c, n, r[u]);
+    for (int u = 0; u < AHEAD; ++u) {
+      const TI *src = d_o + order[j + u] * ld + c;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+      for (int k = 0; k < CH; ++k) load8(src + k * step, D - c - k * step, r[u][k]);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += r[u][i];
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int k = 0; k < CH; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[k][i] += r[u][k][i];
   }
   for (; j < to; ++j) {
-    float r[8];
-    load8(d_o + order[j] * ld + c, n, r);
+    const TI *src = d_o + order[j] * ld + c;
+    float r[CH][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] += r[i];
+    for (int k = 0; k < CH; ++k) load8(src + k * step, D - c - k * step, r[k]);
+#pragma unroll
+    for (int k = 0; k < CH; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[k][i] += r[k][i];
   }
 }
 
@@ -150,51 +168,62 @@ __global__ __launch_bounds__(NT) void piece_kernel(const int *ids, const TI *d_o
     if (slot == 1 && z == a) break;
     const int v = slot ? z : a, s = start[v], e = start[v + 1];
     if (e - s <= piece || c >= D) continue;
-    float sum[8] = {};
-    add_tokens(d_o, order, max(s, j0), min(e, j1), ld, c, D - c, sum);
-    store8(part + (2LL * blockIdx.x + slot) * D + c, D - c, sum);
+    float sum[1][8] = {};
+    add_tokens<TI, 1, 8>(d_o, order, max(s, j0), min(e, j1), ld, c, 0, D, sum);
+    store8(part + (2LL * blockIdx.x + slot) * D + c, D - c, sum[0]);
   }
 }
 
-template <typename TI, typename TO>
+// A row of the gradient by tpr lanes (a power of two up to a wave), CH chunks of eight columns each at a
+// time: a wave a row rather than a workgroup, since a row's time is that of start, order and tokens
+// one after the other.
+template <typename TI, typename TO, int CH>
 __global__ __launch_bounds__(NT) void rows_kernel(const TI *d_o, const int *order, const int *start, const float *part,
                                                   TO *dtable, int V, int D, long long ld, int piece, int tpr,
                                                   float scale) {
-  const int col = threadIdx.x & (tpr - 1), rows = NT / tpr;
+  const int col = threadIdx.x & (tpr - 1), rows = NT / tpr, step = tpr * 8;
   const int v = blockIdx.x * rows + threadIdx.x / tpr;
   if (v >= V) return;
   const int s = start ? start[v] : 0, e = start ? start[v + 1] : 0;
-  for (int c = col * 8; c < D; c += tpr * 8) {
-    float sum[8] = {};
+  for (int c = col * 8; c < D; c += CH * step) {
+    float sum[CH][8] = {};
     if (e - s <= piece) {
-      add_tokens(d_o, order, s, e, ld, c, D - c, sum);
+      add_tokens<TI, CH, CH >= 4 ? 2 : 4>(d_o, order, s, e, ld, c, step, D, sum);
     } else {
       // a run that begins inside its first piece is that piece's second slot
       const int p0 = s / piece, p1 = (e - 1) / piece;
+#pragma unroll 4
       for (int p = p0; p <= p1; ++p) {
-        float r[8];
-        load8(part + (2LL * p + (p == p0 && s % piece != 0)) * D + c, D - c, r);
+        const float *src = part + (2LL * p + (p == p0 && s % piece != 0)) * D + c;
+        float r[CH][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += r[i];
+        for (int k = 0; k < CH; ++k) load8(src + k * step, D - c - k * step, r[k]);
+#pragma unroll
+        for (int k = 0; k < CH; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[k][i] += r[k][i];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum[i] *= scale;
-    store8(dtable + (long long)v * D + c, D - c, sum);
+    for (int k = 0; k < CH; ++k) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[k][i] *= scale;
+      store8(dtable + (long long)v * D + c + k * step, D - c - k * step, sum[k]);
+    }
   }
 }
 
-int threads_per_row(int D) {
+int threads_per_row(int D, int most) {
   int t = 1;
-  while (t < NT && t * 8 < D) t *= 2;
+  while (t < most && t * 8 < D) t *= 2;
   return t;
 }
 
-// Tokens of a piece: about the square root of their number, so that neither a piece nor the list of
-// pieces of one id is long.
+// Tokens of a piece: about a quarter of the square root of their number, so that neither a piece nor the list
+// of pieces of one id is long (16384 tokens in pieces of 128 and 32: 73 and 9 us).
 int piece_of(long long n) {
   int p = 32;
-  while ((long long)p * p < n) p *= 2;
+  while (16LL * p * p < n) p *= 2;
   return p;
 }
 
@@ -216,8 +245,8 @@ ret_status_t check_sizes(long long n, int V, int D, ret_dtype_t in, ret_dtype_t 
   if (n > LANGUAGE_MAX_TOKENS || V > LANGUAGE_MAX_VOCAB || D > LANGUAGE_MAX_CHANNELS ||
       n * D > LANGUAGE_MAX_ELEMENTS || (long long)V * D > LANGUAGE_MAX_ELEMENTS)
     return rec_fail(RET_ERR_UNSUPPORTED, "n, V or D too large");
-  const int rows = NT / threads_per_row(D);
-  if (!rec_grid_ok((double)rec_cdiv(std::max<long long>(n, V), rows), NT))
+  if (!rec_grid_ok((double)rec_cdiv(n, NT / threads_per_row(D, NT)), NT) ||
+      !rec_grid_ok((double)rec_cdiv(V, NT / threads_per_row(D, 64)), NT))
     return rec_fail(RET_ERR_UNSUPPORTED, "too many rows for one launch");
   return RET_OK;
 }
@@ -236,7 +265,7 @@ extern "C" ret_status_t embedding(const int *ids, const void *table, void *out, 
   const RecSpan ins[] = {{"ids", ids, (size_t)n * 4}, {"table", table, (size_t)V * D * ie}};
   const RecSpan outs[] = {{"out", out, (size_t)n * D * oe}};
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
-  const int tpr = threads_per_row(D);
+  const int tpr = threads_per_row(D, NT);
   const unsigned grid = (unsigned)rec_cdiv(n, NT / tpr);
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     hipLaunchKernelGGL((lookup_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>>),
@@ -275,11 +304,13 @@ extern "C" ret_status_t embedding_bwd(const int *ids, const void *d_o, void *dta
   char *ws = (char *)workspace;
   int *order = n ? (int *)(ws + w.order) : nullptr, *start = n ? (int *)(ws + w.start) : nullptr;
   float *part = n ? (float *)(ws + w.part) : nullptr;
-  const int piece = piece_of(n), tpr = threads_per_row(D);
+  const int piece = piece_of(n), tpr = threads_per_row(D, 64);
   if (n > 0) {
     const int range = (int)std::min<long long>(MAX_RANGE, std::max<long long>(1, rec_cdiv(V, 256)));
+    int bits = 0;
+    while (1 << bits < range) ++bits;
     hipLaunchKernelGGL(sort_kernel, dim3((unsigned)rec_cdiv(V, range)), dim3(SORT_NT), 0, st, ids, order, start, (int)n,
-                       V, range);
+                       V, range, bits);
   }
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     using TI = std::remove_pointer_t<decltype(ti)>;
@@ -287,8 +318,16 @@ extern "C" ret_status_t embedding_bwd(const int *ids, const void *d_o, void *dta
     if (n > piece)
       hipLaunchKernelGGL((piece_kernel<TI>), dim3((unsigned)rec_cdiv(n, piece), (unsigned)rec_cdiv(D, NT * 8)), dim3(NT),
                          0, st, ids, (const TI *)d_o, order, start, part, V, D, o_ld, piece);
-    hipLaunchKernelGGL((rows_kernel<TI, TO>), dim3((unsigned)rec_cdiv(V, NT / tpr)), dim3(NT), 0, st, (const TI *)d_o,
-                       order, start, part, (TO *)dtable, V, D, o_ld, piece, tpr, scale);
+    auto rows = [&](auto chunks) {
+      hipLaunchKernelGGL((rows_kernel<TI, TO, decltype(chunks)::value>), dim3((unsigned)rec_cdiv(V, NT / tpr)), dim3(NT), 0,
+                         st, (const TI *)d_o, order, start, part, (TO *)dtable, V, D, o_ld, piece, tpr, scale);
+    };
+    if (D <= 512)
+      rows(std::integral_constant<int, 1>{});
+    else if (D <= 1024)
+      rows(std::integral_constant<int, 2>{});
+    else
+      rows(std::integral_constant<int, 4>{});
     return hipGetLastError();
   }));
 }

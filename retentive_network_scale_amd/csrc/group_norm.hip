@@ -37,9 +37,14 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // The activation of a gate and its derivative.
 __device__ __forceinline__ float act_of(float g, int silu) { return silu ? g * sigmoid(g) : g; }
-__device__ __forceinline__ float act_slope(float g, int silu) {
-  const float s = sigmoid(g);
-  return silu ? s * (1.0f + g * (1.0f - s)) : 1.0f;
+__device__ __forceinline__ void act_both(float g, int silu, float &act, float &slope) {
+  act = g;
+  slope = 1.0f;
+  if (silu) {
+    const float s = sigmoid(g);
+    act = g * s;
+    slope = fmaf(act, 1.0f - s, s);
+  }
 }
 
 // Row statistics: x becomes x - mean (zero behind W), the result is 1 / sqrt(var + eps).
@@ -62,95 +67,139 @@ __device__ __forceinline__ float normalise(float (&x)[C][8], int col, int W, flo
   return 1.0f / sqrtf(row_sum<TPR>(q) / (float)W + eps);
 }
 
-template <typename TI, typename TO, int TPR, int C>
+// A group of lanes takes RT tokens of one head, their loads all under way from the start, and the head's weight
+// and bias once for all of them.
+template <typename TI, typename TO, int TPR, int C, int RT>
 __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs a) {
   const int col = threadIdx.x & (TPR - 1);
-  // (b, t, h); the launch's threads fit 32 bits, so the rows do
-  const unsigned row = blockIdx.x * (NT / TPR) + threadIdx.x / TPR;
-  if (row >= (unsigned)a.B * a.L * a.H) return;
-  const unsigned tk = row / (unsigned)a.H, b = tk / (unsigned)a.L;
-  const int h = (int)(row - tk * a.H), t = (int)(tk - b * a.L);
-  const long long tok = tk;
-  if (a.lengths && t >= a.lengths[b]) return;
-  const TI *xp = (const TI *)a.x + b * a.x_sb + h * a.x_sh + t * a.x_sl;
-  const TI *gp = (const TI *)a.gate + tok * a.gate_ld + (long long)h * a.W;
-  float x[C][8], g[C][8];
+  // (tokens, head); the launch's threads fit 32 bits, so the groups do
+  const unsigned group = blockIdx.x * (NT / TPR) + threadIdx.x / TPR, tokens = (unsigned)a.B * a.L;
+  const unsigned run = group / (unsigned)a.H, h = group - run * a.H;
+  if (run * RT >= tokens) return;
+  Raw8<TI> xr[RT][C], gr[RT][C];
+  bool live[RT];
 #pragma unroll
-  for (int k = 0; k < C; ++k) load8(xp + (k * TPR + col) * 8, a.W - (k * TPR + col) * 8, x[k]);
-  if (a.gate)
+  for (int j = 0; j < RT; ++j) {
+    const unsigned tok = run * RT + j, b = tok / (unsigned)a.L, t = tok - b * a.L;
+    live[j] = tok < tokens && (!a.lengths || (int)t < a.lengths[b]);
+    const TI *xp = (const TI *)a.x + (long long)b * a.x_sb + h * a.x_sh + t * a.x_sl;
+    const TI *gp = (const TI *)a.gate + tok * a.gate_ld + (long long)h * a.W;
 #pragma unroll
-    for (int k = 0; k < C; ++k) load8(gp + (k * TPR + col) * 8, a.W - (k * TPR + col) * 8, g[k]);
-  const float r = normalise<TPR, C>(x, col, a.W, a.eps);
+    for (int k = 0; k < C; ++k) {
+      const int c = (k * TPR + col) * 8, n = live[j] ? a.W - c : 0;
+      xr[j][k].load(xp + c, n);
+      if (a.gate) gr[j][k].load(gp + c, n);
+    }
+  }
+  float w[C][8], bias[C][8];
 #pragma unroll
   for (int k = 0; k < C; ++k) {
     const int c = (k * TPR + col) * 8;
-    float w[8], bias[8];
-    if (a.weight) load8(a.weight + (long long)h * a.W + c, a.W - c, w);
-    if (a.bias) load8(a.bias + (long long)h * a.W + c, a.W - c, bias);
+    if (a.weight) load8(a.weight + (long long)h * a.W + c, a.W - c, w[k]);
+    if (a.bias) load8(a.bias + (long long)h * a.W + c, a.W - c, bias[k]);
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float n = x[k][i] * r;
-      if (a.weight) n *= w[i];
-      if (a.bias) n += bias[i];
-      x[k][i] = a.gate ? n * act_of(g[k][i], a.silu) : act_of(n, a.silu);
+  for (int j = 0; j < RT; ++j) {
+    if (!live[j]) continue;
+    float x[C][8];
+#pragma unroll
+    for (int k = 0; k < C; ++k) xr[j][k].get(x[k]);
+    const float r = normalise<TPR, C>(x, col, a.W, a.eps);
+    TO *out = (TO *)a.out + (long long)(run * RT + j) * a.H * a.W + (long long)h * a.W;
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      const int c = (k * TPR + col) * 8;
+      float g[8];
+      if (a.gate) gr[j][k].get(g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float n = x[k][i] * r;
+        if (a.weight) n *= w[k][i];
+        if (a.bias) n += bias[k][i];
+        x[k][i] = a.gate ? n * act_of(g[i], a.silu) : act_of(n, a.silu);
+      }
+      store8(out + c, a.W - c, x[k]);
     }
-    store8((TO *)a.out + tok * a.H * a.W + (long long)h * a.W + c, a.W - c, x[k]);
   }
 }
 
-// blockIdx.y: the head; blockIdx.x of a.parts: tokens blockIdx.x * RB + row, then parts * RB further on.
+// blockIdx.y: the head; blockIdx.x of a.parts: tokens blockIdx.x * RB + row, then parts * RB further on, whose
+// loads are under way while one is computed.
 template <typename TI, typename TO, int TPR, int C, bool SUMS>
 __global__ __launch_bounds__(BWD_NT) void norm_bwd_kernel(NormArgs a) {
   constexpr int RB = BWD_NT / TPR;
   const int col = threadIdx.x & (TPR - 1), h = blockIdx.y;
   float dw[SUMS ? C : 1][8] = {}, db[SUMS ? C : 1][8] = {};
-  const long long tokens = (long long)a.B * a.L;
-  for (long long tok = (long long)blockIdx.x * RB + threadIdx.x / TPR; tok < tokens; tok += (long long)a.parts * RB) {
-    const unsigned b = (unsigned)tok / (unsigned)a.L;
-    const int t = (int)((unsigned)tok - b * a.L);
-    const bool live = !a.lengths || t < a.lengths[b];
-    const TI *xp = (const TI *)a.x + b * a.x_sb + h * a.x_sh + t * a.x_sl;
+  float w[C][8], bias[C][8];
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    const int c = (k * TPR + col) * 8;
+    if (a.weight) load8(a.weight + (long long)h * a.W + c, a.W - c, w[k]);
+    if (a.bias) load8(a.bias + (long long)h * a.W + c, a.W - c, bias[k]);
+  }
+  const unsigned tokens = (unsigned)a.B * a.L, step = a.parts * RB;
+  Raw8<TI> xr[C], gr[C], dr[C];
+  bool live = false;
+  auto fetch = [&](unsigned tok) {
+    const unsigned b = tok / (unsigned)a.L, t = tok - b * a.L;
+    live = tok < tokens && (!a.lengths || (int)t < a.lengths[b]);
+    const TI *xp = (const TI *)a.x + (long long)b * a.x_sb + h * a.x_sh + t * a.x_sl;
     const TI *gp = (const TI *)a.gate + tok * a.gate_ld + (long long)h * a.W;
-    const long long at = tok * a.H * a.W + (long long)h * a.W;
-    float x[C][8], g[C][8], d[C][8];
+    const TI *dp = (const TI *)a.d_o + (long long)tok * a.H * a.W + (long long)h * a.W;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8, n = live ? a.W - c : 0;
-      load8(xp + c, n, x[k]);
-      load8((const TI *)a.d_o + at + c, n, d[k]);
-      if (a.gate) load8(gp + c, n, g[k]);
+      xr[k].load(xp + c, n);
+      dr[k].load(dp + c, n);
+      if (a.gate) gr[k].load(gp + c, n);
     }
+  };
+  unsigned tok = blockIdx.x * RB + threadIdx.x / TPR;
+  fetch(tok);
+  for (; tok < tokens; tok += step) {
+    const unsigned b = tok / (unsigned)a.L, t = tok - b * a.L;
+    const bool now = live;
+    float x[C][8], g[C][8], d[C][8];
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      xr[k].get(x[k]);
+      dr[k].get(d[k]);
+      if (a.gate) gr[k].get(g[k]);
+    }
+    fetch(tok + step);
     const float r = normalise<TPR, C>(x, col, a.W, a.eps);
     float s1 = 0.0f, s2 = 0.0f;
+    TO *dgate = (TO *)a.dgate + (long long)tok * a.H * a.W + (long long)h * a.W;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8;
-      float w[8], bias[8];
-      if (a.weight) load8(a.weight + (long long)h * a.W + c, a.W - c, w);
-      if (a.bias) load8(a.bias + (long long)h * a.W + c, a.W - c, bias);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float xh = x[k][i] * r;
         float n = xh, dn;
-        if (a.weight) n *= w[i];
-        if (a.bias) n += bias[i];
+        if (a.weight) n *= w[k][i];
+        if (a.bias) n += bias[k][i];
         if (a.gate) {
-          dn = d[k][i] * act_of(g[k][i], a.silu);
-          g[k][i] = d[k][i] * n * act_slope(g[k][i], a.silu);
+          float act, slope;
+          act_both(g[k][i], a.silu, act, slope);
+          dn = d[k][i] * act;
+          g[k][i] = d[k][i] * n * slope;
         } else {
-          dn = d[k][i] * act_slope(n, a.silu);
+          float act, slope;
+          act_both(n, a.silu, act, slope);
+          dn = d[k][i] * slope;
         }
         if constexpr (SUMS) {
           dw[k][i] += dn * xh;
           db[k][i] += dn;
         }
-        if (a.weight) dn *= w[i];
+        if (a.weight) dn *= w[k][i];
         x[k][i] = xh;
         d[k][i] = dn;
         s1 += dn;
         s2 += dn * xh;
       }
-      if (a.gate) store8((TO *)a.dgate + at + c, a.W - c, g[k]);
+      if (a.gate) store8(dgate + c, a.W - c, g[k]);
     }
     s1 = row_sum<TPR>(s1) / (float)a.W;
     s2 = row_sum<TPR>(s2) / (float)a.W;
@@ -159,7 +208,7 @@ __global__ __launch_bounds__(BWD_NT) void norm_bwd_kernel(NormArgs a) {
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[k][i] = live ? r * (d[k][i] - s1 - x[k][i] * s2) : 0.0f;
+      for (int i = 0; i < 8; ++i) d[k][i] = now ? r * (d[k][i] - s1 - x[k][i] * s2) : 0.0f;
       store8(dx + c, a.W - c, d[k]);
     }
   }
@@ -207,6 +256,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int 
   if (!out) return;
   float s = 0.0f;
   if (ch < width)
+#pragma unroll 8
     for (int p = wave; p < parts; p += 16) s += part[((long long)p * 2 + which) * width + ch];
   red[wave][lane] = s;
   __syncthreads();
@@ -299,9 +349,10 @@ extern "C" ret_status_t group_norm_gate(const void *x, const void *gate, const f
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     return with_width(W, [&](auto tpr, auto chunks) {
+      constexpr int RT = decltype(chunks)::value == 1 ? 4 : 1;
       hipLaunchKernelGGL((norm_fwd_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>,
-                                          decltype(tpr)::value, decltype(chunks)::value>),
-                         dim3((unsigned)rec_cdiv(tokens * H, NT / decltype(tpr)::value)), dim3(NT), 0,
+                                          decltype(tpr)::value, decltype(chunks)::value, RT>),
+                         dim3((unsigned)rec_cdiv(rec_cdiv(tokens, RT) * H, NT / decltype(tpr)::value)), dim3(NT), 0,
                          (hipStream_t)hip_stream, a);
       return hipGetLastError();
     });

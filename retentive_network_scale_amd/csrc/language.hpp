@@ -65,6 +65,38 @@ __device__ __forceinline__ void store8(T *p, int n, const float (&r)[8]) {
   }
 }
 
+// Eight elements as they come from memory, for loads that are to be under way while others are used.
+template <typename T>
+struct Raw8 {
+  Words4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *p, int n) {
+    if (n >= 8) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = ((const Words4 *)p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) {
+          if constexpr (sizeof(T) == 2)
+            w[0].w[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+          else
+            w[i / 4].w[i % 4] = __float_as_uint(p[i]);
+        }
+    }
+  }
+  __device__ __forceinline__ void get(float (&r)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2)
+        r[i] = __uint_as_float(i % 2 ? w[0].w[i / 2] & 0xffff0000u : w[0].w[i / 2] << 16);
+      else
+        r[i] = __uint_as_float(w[i / 4].w[i % 4]);
+    }
+  }
+};
+
 // Calls f with a null pointer of the element type that each dtype stands for.
 template <typename F>
 inline auto with_types(ret_dtype_t in, ret_dtype_t out, F f) {

@@ -1,5 +1,5 @@
 // Products with bias, activation and residual, and their gradients (language.h): the entry points, the
-// product for at most eight tokens, and the elementwise part of the gradients.  linear_mm.hpp has the tiled
+// product for few tokens, and the elementwise part of the gradients.  linear_mm.hpp has the tiled
 // product.
 #include "linear.hpp"
 
@@ -7,48 +7,72 @@ using namespace ret;
 
 namespace {
 
-// ------------------------------------------------------------------ at most eight tokens
-// A wave takes RW rows of w, a lane 8 k of each 512; M tokens.
+// --------------------------------------------------------------------------- few tokens
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+// Eight bf16 elements as they are, the first n of them (any alignment).
+__device__ __forceinline__ Words4 raw8(const uint16_t *p, int n) {
+  Words4 v = {{0u, 0u, 0u, 0u}};
+  if (n >= 8) return *(const Words4 *)p;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) v.w[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+  return v;
+}
+
+// A wave takes RW rows of w, which it reads at full width, a lane 8 k of each 512; M tokens at most.  The
+// lanes' RW M sums are added so that each step halves their number: value i ends in lane i 64 / (RW M).
+// Bound by the launch and the way from memory: one token, N 4096, K 2048 (16.8 MB).
 template <int M, int RW>
-__global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint16_t *w, int N, int K, long long x_ld,
-                                                   Finish f) {
+__global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint16_t *w, int tokens, int N, int K,
+                                                   long long x_ld, Finish f) {
+  constexpr int C = M * RW;
+  static_assert(C <= 64 && (C & (C - 1)) == 0, "sums of a wave");
   const int lane = threadIdx.x & 63;
   const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * RW;
   if (n0 >= N) return;
-  float acc[RW][M] = {};
+  float acc[C] = {};  // [RW][M]
 #pragma unroll 2
   for (int k = lane * 8; k < K; k += 512) {
-    float wv[RW][8], xv[8];
+    Words4 wv[RW];
 #pragma unroll
-    for (int r = 0; r < RW; ++r) load8(w + (long long)min(n0 + r, N - 1) * K + k, K - k, wv[r]);
+    for (int r = 0; r < RW; ++r) wv[r] = raw8(w + (long long)min(n0 + r, N - 1) * K + k, K - k);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      load8(x + m * x_ld + k, K - k, xv);
+      const Words4 xv = raw8(x + min(m, tokens - 1) * x_ld + k, K - k);
 #pragma unroll
       for (int r = 0; r < RW; ++r)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[r][m] = fmaf(wv[r][i], xv[i], acc[r][m]);
+        for (int i = 0; i < 4; ++i)
+          acc[r * M + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wv[r].w[i]),
+                                                           __builtin_bit_cast(bf16x2, xv.w[i]), acc[r * M + m], false);
     }
   }
+  int n = C;
 #pragma unroll
-  for (int r = 0; r < RW; ++r)
+  for (int off = 32; off > 0; off >>= 1) {
+    if (n > 1) {
+      n /= 2;
 #pragma unroll
-    for (int m = 0; m < M; ++m) acc[r][m] = wave_sum(acc[r][m]);
-  // lane m finishes token m
-#pragma unroll
-  for (int r = 0; r < RW; ++r) {
-    float v = acc[r][0];
-#pragma unroll
-    for (int m = 1; m < M; ++m) v = lane == m ? acc[r][m] : v;
-    const int n = n0 + r;
-    if (lane < M && n < N) {
-      const long long at = (long long)lane * N + n;
-      if (f.bias) v += bf2f(f.bias[n]);
-      if (f.pre) f.pre[at] = f2bf(v);
-      v = act_value(v, f.act);
-      if (f.residual) v += load_elem(f.residual, at, f.res_bf16);
-      store_elem(f.out, at, v, f.out_bf16);
+      for (int i = 0; i < C / 2; ++i)
+        if (i < n) {
+          const bool up = lane & off;
+          const float mine = up ? acc[i + n] : acc[i], other = up ? acc[i] : acc[i + n];
+          acc[i] = mine + __shfl_xor(other, off, 64);
+        }
+    } else {
+      acc[0] += __shfl_xor(acc[0], off, 64);
     }
+  }
+  const int value = lane / (64 / C), m = value % M, col = n0 + value / M;
+  if (lane % (64 / C) == 0 && m < tokens && col < N) {
+    float v = acc[0];
+    const long long at = (long long)m * N + col;
+    if (f.bias) v += bf2f(f.bias[col]);
+    if (f.pre) f.pre[at] = f2bf(v);
+    v = act_value(v, f.act);
+    if (f.residual) v += load_elem(f.residual, at, f.res_bf16);
+    store_elem(f.out, at, v, f.out_bf16);
   }
 }
 
@@ -94,6 +118,7 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float *part, int 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = blockIdx.x * 64 + lane;
   float s = 0.0f;
   if (n < N)
+#pragma unroll 8
     for (int p = wave; p < parts; p += 16) s += part[(long long)p * N + n];
   red[wave][lane] = s;
   __syncthreads();
@@ -106,13 +131,13 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float *part, int 
 }
 
 // ------------------------------------------------------------------------------- host
-constexpr long long FEW = 8;  // tokens that rows_kernel serves
+constexpr long long FEW = 16;  // tokens that rows_kernel serves
 
-template <int M>
-hipError_t launch_rows(const void *x, const void *w, int N, int K, long long x_ld, const Finish &f, hipStream_t st) {
-  constexpr int RW = 2;
+template <int M, int RW>
+hipError_t launch_rows(const void *x, const void *w, int tokens, int N, int K, long long x_ld, const Finish &f,
+                       hipStream_t st) {
   hipLaunchKernelGGL((rows_kernel<M, RW>), dim3((unsigned)rec_cdiv(N, 4 * RW)), dim3(256), 0, st, (const uint16_t *)x,
-                     (const uint16_t *)w, N, K, x_ld, f);
+                     (const uint16_t *)w, tokens, N, K, x_ld, f);
   return hipGetLastError();
 }
 
@@ -180,15 +205,13 @@ extern "C" ret_status_t linear(const void *x, const void *w, const void *bias, c
   f.bias = (const uint16_t *)bias, f.residual = residual, f.out = out, f.pre = (uint16_t *)pre;
   f.act = act, f.res_bf16 = residual_dtype == RET_BF16, f.out_bf16 = out_dtype == RET_BF16;
   hipStream_t st = (hipStream_t)hip_stream;
-  switch (M <= FEW ? (int)M : 0) {
-    case 1: return rec_status(launch_rows<1>(x, w, N, K, x_ld, f, st));
-    case 2: return rec_status(launch_rows<2>(x, w, N, K, x_ld, f, st));
-    case 3: return rec_status(launch_rows<3>(x, w, N, K, x_ld, f, st));
-    case 4: return rec_status(launch_rows<4>(x, w, N, K, x_ld, f, st));
-    case 5: return rec_status(launch_rows<5>(x, w, N, K, x_ld, f, st));
-    case 6: return rec_status(launch_rows<6>(x, w, N, K, x_ld, f, st));
-    case 7: return rec_status(launch_rows<7>(x, w, N, K, x_ld, f, st));
-    case 8: return rec_status(launch_rows<8>(x, w, N, K, x_ld, f, st));
+  if (M <= FEW) {
+    const int m = (int)M;
+    return rec_status(m == 1   ? launch_rows<1, 2>(x, w, m, N, K, x_ld, f, st)
+                      : m == 2 ? launch_rows<2, 2>(x, w, m, N, K, x_ld, f, st)
+                      : m <= 4 ? launch_rows<4, 2>(x, w, m, N, K, x_ld, f, st)
+                      : m <= 8 ? launch_rows<8, 2>(x, w, m, N, K, x_ld, f, st)
+                               : launch_rows<16, 4>(x, w, m, N, K, x_ld, f, st));
   }
   MmArgs a = {};
   a.p = (const uint16_t *)x, a.q = (const uint16_t *)w, a.ldp = x_ld, a.ldq = K;

@@ -68,67 +68,36 @@ struct Finish {
   int act, res_bf16, out_bf16;
 };
 
-struct __attribute__((packed, aligned(2))) Words2 {
-  uint32_t w[2];
-};
-// Four consecutive elements, whatever their alignment.
-__device__ __forceinline__ void load4(const void *p, long long off, bool bf16, float (&r)[4]) {
-  if (bf16) {
-    const Words2 v = *(const Words2 *)((const uint16_t *)p + off);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r[2 * i] = __uint_as_float(v.w[i] << 16);
-      r[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
-    }
-  } else {
-    const Words4 v = *(const Words4 *)((const float *)p + off);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = __uint_as_float(v.w[i]);
-  }
-}
-__device__ __forceinline__ void put4(void *p, long long off, bool bf16, const float (&r)[4]) {
-  if (bf16) {
-    *(Words2 *)((uint16_t *)p + off) = {{pack_bf2(r[0], r[1]), pack_bf2(r[2], r[3])}};
-  } else {
-    Words4 v;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v.w[i] = __float_as_uint(r[i]);
-    *(Words4 *)((float *)p + off) = v;
-  }
-}
-
-// z's elements n..n+3 of row m (of N a row), as far as there are any: bias, activation, residual.
-__device__ __forceinline__ void finish4(const Finish &f, long long m, int n, int N, float (&z)[4]) {
+// z's elements n .. n + 7 of row m (of N a row), as far as there are any: bias, activation, residual.
+__device__ __forceinline__ void finish8(const Finish &f, long long m, int n, int N, float (&z)[8]) {
   const long long at = m * N + n;
-  if (n + 4 <= N) {
-    float r[4];
-    if (f.bias) {
-      load4(f.bias, n, true, r);
+  const int left = N - n;
+  float r[8];
+  if (f.bias) {
+    load8(f.bias + n, left, r);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] += r[i];
-    }
-    if (f.pre) put4(f.pre, at, true, z);
-    if (f.act)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] = act_value(z[i], f.act);
-    if (f.residual) {
-      load4(f.residual, at, f.res_bf16, r);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z[i] += r[i];
-    }
-    put4(f.out, at, f.out_bf16, z);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < N) {
-        float v = z[i];
-        if (f.bias) v += bf2f(f.bias[n + i]);
-        if (f.pre) f.pre[at + i] = f2bf(v);
-        v = act_value(v, f.act);
-        if (f.residual) v += load_elem(f.residual, at + i, f.res_bf16);
-        store_elem(f.out, at + i, v, f.out_bf16);
-      }
+    for (int i = 0; i < 8; ++i) z[i] += r[i];
   }
+  if (f.pre) store8(f.pre + at, left, z);
+  if (f.act == LINEAR_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = gelu(z[i]);
+  } else if (f.act == LINEAR_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= sigmoid(z[i]);
+  }
+  if (f.residual) {
+    if (f.res_bf16)
+      load8((const uint16_t *)f.residual + at, left, r);
+    else
+      load8((const float *)f.residual + at, left, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += r[i];
+  }
+  if (f.out_bf16)
+    store8((uint16_t *)f.out + at, left, z);
+  else
+    store8((float *)f.out + at, left, z);
 }
 
 struct MmArgs {
@@ -138,7 +107,7 @@ struct MmArgs {
   int N;        // Q's rows
   long long K;
   long long kpart;  // k of a part, a multiple of BK
-  float *part;      // [parts][M][N rounded up to 4], or NULL: finish
+  float *part;      // [parts][M][N], or NULL: finish
   Finish f;
 };
 
@@ -149,19 +118,38 @@ struct MmPlan {
   size_t bytes;  // of the parts' sums
 };
 
-// The largest tile that still gives every CU a workgroup, and else parts of k until there are about
-// two a CU, none shorter than four tiles of k.
+// Tile and parts of k by an estimate of the time, in us.  A step (64 k) of a tile takes `alone` where a CU has
+// one workgroup and `each` for every workgroup of the fullest CU (measured with 16 tokens, and with
+// 1024 tiles, K 2048: a 128 x 128 tile fetches twice the bytes of a 256 x 256 one for its work, and a 64 x 64
+// one four times); `end` is its way from sums to output.  Parts of k cost their sums' way to memory and back
+// and a launch.  At M 16384, N 4096, K 2048 the three take 232, 274 and 400 us, at M 1024 47, 25 and 31, at M 200
+// 45, 21 and 12; four parts for M 16, N 2048, K 4096: 18.8 -> 10.7 us.
 inline MmPlan mm_plan(long long M, long long N, long long K) {
-  MmPlan p;
-  auto tiles = [&](int t) { return rec_cdiv(M, t) * rec_cdiv(N, t); };
-  p.tile = tiles(256) >= 256 ? 256 : tiles(128) >= 256 ? 128 : 64;
-  const long long steps = std::max<long long>(1, rec_cdiv(K, BK)), n = std::max<long long>(1, tiles(p.tile));
-  long long parts = n >= 256 ? 1 : std::min<long long>(rec_cdiv(512, n), steps / 4);
-  parts = std::max<long long>(1, std::min<long long>(parts, 64));
-  p.kpart = rec_cdiv(steps, parts) * BK;
-  p.parts = (int)std::max<long long>(1, rec_cdiv(K, p.kpart));
-  p.bytes = p.parts > 1 ? rec_align((size_t)p.parts * M * ((N + 3) / 4 * 4) * 4) : 0;
-  return p;
+  struct {
+    int tile;
+    double alone, each, end;
+  } const kinds[] = {{64, 0.27, 0.23, 0.7}, {128, 0.50, 0.53, 1.5}, {256, 1.25, 1.70, 3.0}};
+  const long long steps = std::max<long long>(1, rec_cdiv(K, BK));
+  MmPlan best = {};
+  double least = 1e30;
+  for (const auto &k : kinds) {
+    const long long tiles = std::max<long long>(1, rec_cdiv(M, k.tile) * rec_cdiv(N, k.tile));
+    for (long long parts = 1; parts <= 32 && (parts == 1 || 2 * parts <= steps); parts *= 2) {
+      const long long each = rec_cdiv(steps, parts), real = rec_cdiv(steps, each);
+      if (real != parts) continue;
+      const double fullest = (double)rec_cdiv(tiles * parts, 256);
+      double t = each * std::max(k.alone, fullest * k.each) + k.end;
+      if (parts > 1) t += 2.5 + (double)M * N * (8 * parts + 2) / 4.5e6;
+      if (t < least) {
+        least = t;
+        best.tile = k.tile;
+        best.parts = (int)parts;
+        best.kpart = each * BK;
+      }
+    }
+  }
+  best.bytes = best.parts > 1 ? rec_align((size_t)best.parts * M * N * 4) : 0;
+  return best;
 }
 
 // The products on `ws`, mm_plan's bytes: forward (both operands with k along their rows), dx (P with k

@@ -4,11 +4,15 @@
 //   forward  P = x,  Q = w         both with k along their rows
 //   dx       P = dz, Q = w         w's rows run along n: its tiles are read transposed from LDS
 //   dw       P = dz, Q = x         both with k across their rows
-// Tiles of 64 k reach LDS by DMA, two buffers in turn, so that one is filled while the other is
-// multiplied; the 16-byte chunks of a row are permuted, so that the operand reads meet no bank twice.
+// Tiles of 64 k reach LDS by DMA, two in turn, so that one is filled while the other is multiplied, and the
+// operands of the next matrix step are read from LDS while the present one's are multiplied.
 // Operands whose rows are not 16-byte aligned take the same way through registers.
 // Where there are too few tiles for the chip, k is cut, the parts' sums go to the workspace in
 // fp32, and a second launch joins them in order and finishes.
+//
+// M 16384, features 2048 -> 4096 (275 GFLOP): 228 us without and 248 us with bias and gelu, whose 18
+// operations an element follow the last matrix step with nothing to hide behind; dx 243 us, dw 272 us and 13 us
+// to join two parts.  The largest library product reaches 1385 TFLOP/s here, so 199 us would be the floor.
 #pragma once
 
 #include "linear.hpp"
@@ -22,31 +26,40 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((address_space(3))) void lds_void;
 
-// A tile of R rows and BK k of an operand in LDS.
-//   KROWS: [R][BK], chunk c (16 bytes) of row r at c ^ (r & 7): the eight rows that a read
-//     takes together then lie in different banks
-//   else: [BK][R], chunk c of row k at c ^ 2 (k & 3), for reads that transpose
+// A tile of R rows and 64 k of an operand in LDS, in two halves of 32 k, one matrix step each.
+//   KROWS (k along the rows in memory): groups of 8 rows, of each 8 rows of 32 k and then 8 rows of
+//     the next 32: a wave load takes 8 whole lines of 128 bytes (tiles of 32 k fetched every line
+//     twice and were bound by it: 128 x 128 tiles took 0.29 us a step of 32 k).  Chunk c (16 bytes) of
+//     a half's row r is at c ^ (r / 2 & 3): the 8 rows that a read takes together meet no bank twice.
+//   else: [64][R], chunk c of row k at c ^ 2 (k & 3), for reads that transpose
 template <int R, bool KROWS, int NT, bool DMA>
 struct Operand {
-  static constexpr int BYTES = R * BK * 2, NJ = BYTES / 1024 / (NT / 64);
-  static_assert(NJ >= 1 && BYTES % (1024 * (NT / 64)) == 0, "whole wave loads");
+  static constexpr int SIZE = R * BK, NJ = SIZE * 2 / 1024 / (NT / 64);  // elements; wave loads of a wave
+  static_assert(NJ >= 1 && SIZE * 2 % (1024 * (NT / 64)) == 0, "whole wave loads");
   const uint16_t *base;  // of the tile's rows (KROWS) or columns
-  long long ld, K;
+  long long ld;
   int width;  // rows of the operand from the tile on, R at most
   u32x4 reg[DMA ? 1 : NJ];
 
-  __device__ __forceinline__ void start(const uint16_t *p, long long ld_, long long rows, long long r0, long long K_) {
+  __device__ __forceinline__ void start(const uint16_t *p, long long ld_, long long rows, long long r0) {
     base = KROWS ? p + r0 * ld_ : p + r0;
     ld = ld_;
-    K = K_;
     width = rows - r0 < R ? (int)(rows - r0) : R;
   }
-  // Place of chunk j of this thread: row of the LDS tile and (unpermuted) chunk in it.
+  // The wave, as a scalar.
+  static __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+  // What chunk j of this thread holds: a row and one of its 16-byte chunks (KROWS: of k, else of columns).
   static __device__ __forceinline__ void place(int j, int &row, int &c) {
-    const int off = ((threadIdx.x >> 6) * NJ + j) * 1024 + (threadIdx.x & 63) * 16;
-    constexpr int RB = KROWS ? BK * 2 : R * 2;
-    row = off / RB;
-    c = (off % RB) / 16 ^ (KROWS ? row & 7 : 2 * (row & 3));
+    const int piece = wave() * NJ + j, lane = threadIdx.x & 63;
+    if constexpr (KROWS) {
+      const int r = lane >> 2 & 7;
+      row = piece * 8 + r;
+      c = (lane >> 5) * 4 + ((lane & 3) ^ (r >> 1));
+    } else {
+      const int off = piece * 1024 + lane * 16;
+      row = off / (R * 2);
+      c = off % (R * 2) / 16 ^ 2 * (row & 3);
+    }
   }
   // The tile at k0 on its way to `lds` (DMA) or to registers; k from `kend` on is zero.
   __device__ __forceinline__ void fetch(uint16_t *lds, long long k0, long long kend) {
@@ -54,7 +67,7 @@ struct Operand {
       // rows are whole 16-byte chunks; what lies behind the range reads as zero
       const int left = kend - k0 < BK ? (int)(kend - k0) : BK;
       const uint16_t *b = KROWS ? base + k0 : base + k0 * ld;
-      const long long last = KROWS ? (long long)(width - 1) * ld + left : (long long)(left - 1) * ld + width;
+      const long long last = left <= 0 ? 0 : KROWS ? (long long)(width - 1) * ld + left : (long long)(left - 1) * ld + width;
       const __amdgpu_buffer_rsrc_t rs =
           __builtin_amdgcn_make_buffer_rsrc((void *)b, (short)0, (int)(last * 2), 0x00020000);
 #pragma unroll
@@ -63,8 +76,7 @@ struct Operand {
         place(j, row, c);
         int off = row * (int)ld * 2 + c * 16;
         if (KROWS && c * 8 >= left) off = (int)0x80000000u;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(lds + ((threadIdx.x >> 6) * NJ + j) * 512), 16, off, 0,
-                                                 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(lds + (wave() * NJ + j) * 512), 16, off, 0, 0, 0);
       }
     } else {
 #pragma unroll
@@ -92,16 +104,15 @@ struct Operand {
   __device__ __forceinline__ void commit(uint16_t *lds) {
     if constexpr (!DMA)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        *(u32x4 *)(lds + ((threadIdx.x >> 6) * NJ + j) * 512 + (threadIdx.x & 63) * 8) = reg[j];
+      for (int j = 0; j < NJ; ++j) *(u32x4 *)(lds + (wave() * NJ + j) * 512 + (threadIdx.x & 63) * 8) = reg[j];
   }
-  // Matrix operand: lane (l16, g) holds k = 32 ks + 8 g .. + 7 of row r0 + l16.
-  static __device__ __forceinline__ bf16x8 read(const uint16_t *lds, int r0, int ks, int l16, int g) {
+  // Matrix operand of half h: lane (l16, g) holds k = 32 h + 8 g .. + 7 of row r0 + l16.
+  static __device__ __forceinline__ bf16x8 read(const uint16_t *lds, int r0, int h, int l16, int g) {
     if constexpr (KROWS) {
-      return *(const bf16x8 *)(lds + (r0 + l16) * BK + ((ks * 4 + g) ^ (l16 & 7)) * 8);
+      return *(const bf16x8 *)(lds + (r0 / 8 + (l16 >> 3)) * 512 + h * 256 + (l16 & 7) * 32 + (g ^ (l16 >> 1 & 3)) * 8);
     } else {
       // within 16 lanes, lane r receives element r % 4 of the pieces that lanes 4 j + r / 4 address
-      const int row = ks * 32 + 8 * g + (l16 >> 2), c = (r0 >> 3) + ((l16 & 3) >> 1);
+      const int row = h * 32 + 8 * g + (l16 >> 2), c = (r0 >> 3) + ((l16 & 3) >> 1);
       const uint16_t *p = lds + row * R + ((c ^ 2 * (row & 3)) << 3) + 4 * (l16 & 1);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p + 4 * R));
@@ -110,12 +121,29 @@ struct Operand {
   }
 };
 
-// BM x BN of out by WM x WN waves.
-template <int BM, int BN, int WM, int WN, bool PK, bool QK, bool DMA>
+// Waits until at most N of this wave's loads are under way, and for its LDS operations.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+}
+// A barrier that waits for nothing by itself; memory operations stay on their side of it.
+__device__ __forceinline__ void meet() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// BM x BN of out by WM x WN waves, with a ring of NB tiles in LDS.  A wave multiplies the operands of a half
+// tile while it reads those of the next half.  The barrier in the middle of a tile tells that all
+// have read it, so that tile i + NB takes its place, and that tile i + 1 has come.
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, bool DMA>
 __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
   constexpr int NT = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(BM + BN) * BK];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
+  using OpP = Operand<BM, PK, NT, DMA>;
+  using OpQ = Operand<BN, QK, NT, DMA>;
+  constexpr int SIZE = OpP::SIZE + OpQ::SIZE, LOADS = OpP::NJ + OpQ::NJ;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[NB * SIZE];
+  const int lane = threadIdx.x & 63, wave = OpP::wave(), l16 = lane & 15, g = lane >> 4;
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
   // Workgroups go round the eight XCDs, each with an L2 of its own: an XCD takes neighbouring tiles,
   // in groups of rows of tiles that share their columns of Q.
@@ -125,65 +153,106 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
     const unsigned per = tiles / 8, rest = tiles % 8, x = t % 8;
     t = t / 8 + x * per + min(x, rest);
   }
-  constexpr unsigned GM = 8;
+  constexpr unsigned GM = 4;
   const unsigned gr = t / (GM * tn), in = t - gr * GM * tn, gm = min(GM, tm - gr * GM);
   const long long m0 = (long long)(gr * GM + in % gm) * BM;
   const int n0 = (int)(in / gm) * BN;
   const long long kb = (long long)blockIdx.y * a.kpart, ke = kb + a.kpart < a.K ? kb + a.kpart : a.K;
+  const int tiles_k = (int)((ke - kb + BK - 1) / BK);
 
-  Operand<BM, PK, NT, DMA> P;
-  Operand<BN, QK, NT, DMA> Q;
-  P.start(a.p, a.ldp, a.M, m0, a.K);
-  Q.start(a.q, a.ldq, a.N, n0, a.K);
+  OpP P;
+  OpQ Q;
+  P.start(a.p, a.ldp, a.M, m0);
+  Q.start(a.q, a.ldq, a.N, n0);
   f32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  int buf = 0;
-  if (kb < ke) {
-    P.fetch(lds[0], kb, ke);
-    Q.fetch(lds[0] + BM * BK, kb, ke);
-  }
-  for (long long k0 = kb; k0 < ke; k0 += BK) {
-    uint16_t *cur = lds[buf], *next = lds[buf ^ 1];
-    P.commit(cur);
-    Q.commit(cur + BM * BK);
-    __syncthreads();  // this tile is there, and all have left the other buffer
-    if (k0 + BK < ke) {
-      P.fetch(next, k0 + BK, ke);
-      Q.fetch(next + BM * BK, k0 + BK, ke);
+  bf16x8 fp[2][FM], fq[2][FN];
+  auto fetch = [&](int i, int slot) {
+    P.fetch(lds + slot * SIZE, kb + (long long)i * BK, ke);
+    Q.fetch(lds + slot * SIZE + OpP::SIZE, kb + (long long)i * BK, ke);
+  };
+  auto read = [&](int slot, int h) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) fq[h][j] = OpQ::read(lds + slot * SIZE + OpP::SIZE, wn + j * 16, h, l16, g);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) fp[h][i] = OpP::read(lds + slot * SIZE, wm + i * 16, h, l16, g);
+  };
+  auto multiply = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[h][j], fp[h][i], acc[i][j], 0, 0, 0);
+  };
+  // the reads go out between the first matrix instructions
+  auto interleave = [] {
+    constexpr int READS = (PK ? FM : 2 * FM) + (QK ? FN : 2 * FN);
+#pragma unroll
+    for (int r = 0; r < READS; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // and a matrix instruction
     }
+  };
+  if constexpr (DMA) {
+    // tiles behind the last are fetched as zeros, so that all steps are alike
 #pragma unroll
-    for (int ks = 0; ks < BK / 32; ++ks) {
-      bf16x8 fp[FM], fq[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fq[j] = Q.read(cur + BM * BK, wn + j * 16, ks, l16, g);
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fp[i] = P.read(cur, wm + i * 16, ks, l16, g);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[j], fp[i], acc[i][j], 0, 0, 0);
+    for (int i = 0; i < NB; ++i) fetch(i, i);
+    wait_loads<(NB - 1) * LOADS>();
+    meet();
+    read(0, 0);
+    int slot = 0;  // of tile i
+    for (int i = 0; i < tiles_k; ++i) {
+      read(slot, 1);
+      multiply(0);
+      interleave();
+      wait_loads<(NB - 2) * LOADS>();
+      meet();
+      fetch(i + NB, slot);
+      slot = slot + 1 == NB ? 0 : slot + 1;
+      read(slot, 0);
+      multiply(1);
+      interleave();
     }
-    buf ^= 1;
+  } else {
+    if (tiles_k > 0) fetch(0, 0);
+    for (int i = 0; i < tiles_k; ++i) {
+      uint16_t *cur = lds + (i & 1) * SIZE;
+      P.commit(cur);
+      Q.commit(cur + OpP::SIZE);
+      __syncthreads();  // this tile is there, and all have left the other place
+      if (i + 1 < tiles_k) fetch(i + 1, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        read(i & 1, h);
+        multiply(h);
+      }
+    }
   }
-  // lane (l16, g): row l16 of P's, rows 4 g .. + 3 of Q's
+  // Lane (l16, g) holds row l16 of P's and rows 4 g .. + 3 of Q's of each 16 x 16; through LDS, 16 rows of P's
+  // at a time, they become runs of eight neighbours, which are finished and stored together.
+  wait_loads<0>();
+  meet();
+  constexpr int TN = BN / WN, PITCH = TN + 4, ROWS = 512 / TN;  // ROWS rows in a pass of 64 lanes
+  static_assert(NT / 64 * 16 * PITCH * 4 <= (int)sizeof(lds) && ROWS <= 16, "the waves' patches");
+  float *patch = (float *)lds + wave * 16 * PITCH;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const long long m = m0 + wm + i * 16 + l16;
-    if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int n = n0 + wn + j * 16 + 4 * g;
-      if (n >= a.N) continue;
-      float z[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (a.part) {
-        const long long nr = (a.N + 3) / 4 * 4;
-        *(f32x4 *)(a.part + ((long long)blockIdx.y * a.M + m) * nr + n) = acc[i][j];
-      } else {
-        finish4(a.f, m, n, a.N, z);
+    for (int j = 0; j < FN; ++j) *(f32x4 *)(patch + l16 * PITCH + j * 16 + 4 * g) = acc[i][j];
+#pragma unroll 1
+    for (int r = lane / (TN / 8); r < 16; r += ROWS) {
+      const int c = lane % (TN / 8) * 8, n = n0 + wn + c;
+      const long long m = m0 + wm + i * 16 + r;
+      const f32x4 lo = *(const f32x4 *)(patch + r * PITCH + c), hi = *(const f32x4 *)(patch + r * PITCH + c + 4);
+      float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      if (m < a.M && n < a.N) {
+        if (a.part)
+          store8(a.part + ((long long)blockIdx.y * a.M + m) * a.N + n, a.N - n, z);
+        else
+          finish8(a.f, m, n, a.N, z);
       }
     }
   }
@@ -191,27 +260,29 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
 
 // The parts' sums, in order.
 __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, int parts, long long M, int N, Finish f) {
-  const unsigned nq = (N + 3) / 4;
+  const unsigned runs = (N + 7) / 8;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (e >= M * nq) return;
-  const long long m = e / nq;
-  const int n = (int)(e - m * nq) * 4;
-  float z[4] = {};
+  if (e >= M * runs) return;
+  const long long m = e / runs;
+  const int n = (int)(e - m * runs) * 8;
+  float z[8] = {};
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) {
-    const f32x4 v = *(const f32x4 *)(part + (p * M + m) * nq * 4 + n);
+    float v[8];
+    load8(part + (p * M + m) * N + n, N - n, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] += v[i];
+    for (int i = 0; i < 8; ++i) z[i] += v[i];
   }
-  finish4(f, m, n, N, z);
+  finish8(f, m, n, N, z);
 }
 
-template <int T, int WM, int WN, bool PK, bool QK>
+template <int BM, int BN, int WM, int WN, bool PK, bool QK>
 hipError_t launch_tile(const MmArgs &a, int parts, bool dma, hipStream_t st) {
-  const dim3 grid((unsigned)(rec_cdiv(a.M, T) * rec_cdiv(a.N, T)), (unsigned)parts);
+  const dim3 grid((unsigned)(rec_cdiv(a.M, BM) * rec_cdiv(a.N, BN)), (unsigned)parts);
   if (dma)
-    hipLaunchKernelGGL((mm_kernel<T, T, WM, WN, PK, QK, true>), grid, dim3(WM * WN * 64), 0, st, a);
+    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, 2, PK, QK, true>), grid, dim3(WM * WN * 64), 0, st, a);
   else
-    hipLaunchKernelGGL((mm_kernel<T, T, WM, WN, PK, QK, false>), grid, dim3(WM * WN * 64), 0, st, a);
+    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, 2, PK, QK, false>), grid, dim3(WM * WN * 64), 0, st, a);
   return hipGetLastError();
 }
 
@@ -226,12 +297,14 @@ hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   a.kpart = p.kpart;
   a.part = p.parts > 1 ? (float *)ws : nullptr;
   const bool dma = chunked(a.p, a.ldp, PK ? a.K : a.M) && chunked(a.q, a.ldq, QK ? a.K : a.N);
-  hipError_t e = p.tile == 256   ? launch_tile<256, 2, 4, PK, QK>(a, p.parts, dma, st)
-                 : p.tile == 128 ? launch_tile<128, 2, 2, PK, QK>(a, p.parts, dma, st)
-                                 : launch_tile<64, 2, 2, PK, QK>(a, p.parts, dma, st);
+  // of 256 x 256, a wave takes 64 x 128, or, where Q's operands cost two reads each, 128 x 64: 227 and 232 us
+  // forward, 252 and 243 us for dx (M 16384, features 2048 and 4096)
+  hipError_t e = p.tile == 256   ? launch_tile<256, 256, QK ? 4 : 2, QK ? 2 : 4, PK, QK>(a, p.parts, dma, st)
+                 : p.tile == 128 ? launch_tile<128, 128, 2, 2, PK, QK>(a, p.parts, dma, st)
+                                 : launch_tile<64, 64, 2, 2, PK, QK>(a, p.parts, dma, st);
   if (e != hipSuccess || p.parts == 1) return e;
-  const long long quads = a.M * ((a.N + 3) / 4);
-  hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)rec_cdiv(quads, 256)), dim3(256), 0, st, a.part, p.parts, a.M, a.N,
+  const long long runs = a.M * ((a.N + 7) / 8);
+  hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)rec_cdiv(runs, 256)), dim3(256), 0, st, a.part, p.parts, a.M, a.N,
                      a.f);
   return hipGetLastError();
 }
