@@ -206,6 +206,15 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
   __shared__ int count;
   const int tid = threadIdx.x;
   const long long b = blockIdx.x;
+  const int lists = a.W * a.slices;
+  // few candidates are all on their way from the start
+  constexpr int EACH = 4;
+  const bool ahead = lists * a.K <= EACH * NT;
+  Cand own[EACH];
+  if (ahead)
+#pragma unroll
+    for (int u = 0; u < EACH; ++u)
+      if (u * NT + tid < lists * a.K) own[u] = a.cands[b * lists * a.K + u * NT + tid];
   // a beam's log-sum by a wave, its slices by the lanes
   for (int w = tid >> 6; w < a.W; w += NT / 64) {
     const long long row = b * a.W + w;
@@ -233,15 +242,13 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
   }
   if (tid == 0) bound = {0, 0}, count = 0;
   __syncthreads();
-  const int lists = a.W * a.slices;
   // Candidate j of a list as a key; {0, 0}: none
-  auto key_at = [&](int list, int j) -> Key {
+  auto key_of_cand = [&](int list, int j, const Cand &c) -> Key {
     const int w = list / a.slices, slice = list - w * a.slices;
     const long long row = b * a.W + w;
     int v;
     double score;
     if (kind[w] == 0) {
-      const Cand c = a.cands[(row * a.slices + slice) * a.K + j];
       if (c.index < 0) return {0, 0};
       v = c.index;
       score = (double)a.scores[row] + ((double)c.value - lse[w]);
@@ -255,10 +262,24 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
     }
     return {ordered(score + 0.0), ~(uint32_t)(w * a.V + v)};
   };
-  for (int l = tid; l < lists; l += NT) {
-    const Key k = key_at(l, 0);
-    head_score[l] = k.score;
-    head_index[l] = k.index;
+  auto key_at = [&](int list, int j) { return key_of_cand(list, j, a.cands[(b * lists + list) * a.K + j]); };
+  Key mine[EACH];
+  if (ahead) {
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+      const int e = u * NT + tid, l = e / a.K, j = e - l * a.K;
+      mine[u] = {0, 0};
+      if (e < lists * a.K) {
+        mine[u] = key_of_cand(l, j, own[u]);
+        if (j == 0) head_score[l] = mine[u].score, head_index[l] = mine[u].index;
+      }
+    }
+  } else {
+    for (int l = tid; l < lists; l += NT) {
+      const Key k = key_at(l, 0);
+      head_score[l] = k.score;
+      head_index[l] = k.index;
+    }
   }
   __syncthreads();
   for (int l = tid; l < lists; l += NT) {
@@ -270,13 +291,21 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
   }
   __syncthreads();
   // what reaches the bound: prefixes of at most K lists
-  for (int l = tid; l < lists; l += NT) {
-    for (int j = 0; j < a.K; ++j) {
-      const Key k = key_at(l, j);
-      if (!k.score || bound.above(k)) break;
-      const int to = atomicAdd(&count, 1);
-      if (to < CAP2) list_score[to] = k.score, list_index[to] = k.index;
-    }
+  auto put = [&](const Key &k) {
+    const int to = atomicAdd(&count, 1);
+    if (to < CAP2) list_score[to] = k.score, list_index[to] = k.index;
+  };
+  if (ahead) {
+#pragma unroll
+    for (int u = 0; u < EACH; ++u)
+      if (mine[u].score && !bound.above(mine[u])) put(mine[u]);
+  } else {
+    for (int l = tid; l < lists; l += NT)
+      for (int j = 0; j < a.K; ++j) {
+        const Key k = key_at(l, j);
+        if (!k.score || bound.above(k)) break;
+        put(k);
+      }
   }
   __syncthreads();
   const int n = min(count, CAP2);
@@ -310,14 +339,14 @@ struct ReorderArgs {
 // A thread holds the same few bytes of every beam of a request: it reads the parents' before it
 // writes, so the exchange needs no second buffer.  WM beams at most, T at a time.
 template <typename T, int WM>
-__device__ __forceinline__ void reorder_at(char *base, long long bytes, long long off, const int (&parent)[WM], int W) {
+__device__ __forceinline__ void reorder_at(char *base, long long bytes, long long off, const int (&parent)[WM]) {
   T v[WM];
 #pragma unroll
   for (int w = 0; w < WM; ++w)
-    if (w < W && parent[w] != w) v[w] = *(const T *)(base + parent[w] * bytes + off);
+    if (parent[w] != w) v[w] = *(const T *)(base + parent[w] * bytes + off);
 #pragma unroll
   for (int w = 0; w < WM; ++w)
-    if (w < W && parent[w] != w) *(T *)(base + w * bytes + off) = v[w];
+    if (parent[w] != w) *(T *)(base + w * bytes + off) = v[w];
 }
 
 template <int WM, int MT>
@@ -341,21 +370,18 @@ __global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs<MT> a) {
   int parent[WM];
 #pragma unroll
   for (int w = 0; w < WM; ++w) {
-    parent[w] = w;
-    if (w < a.W) {
-      const int p = a.parents[b * a.W + w];
-      parent[w] = (unsigned)p < (unsigned)a.W ? p : w;
-    }
+    const int p = a.parents[b * a.W + min(w, a.W - 1)];  // all read at once
+    parent[w] = w < a.W && (unsigned)p < (unsigned)a.W ? p : w;
   }
   const long long at = (long long)(blockIdx.x - from) * NT + threadIdx.x, step = (long long)(to - from) * NT;
   const unsigned low = (unsigned)(uintptr_t)tensor | (unsigned)bytes;
   if (low % sizeof(Wide) == 0)
     for (long long e = at * sizeof(Wide); e < bytes; e += step * sizeof(Wide))
-      reorder_at<Wide, WM>(base, bytes, e, parent, a.W);
+      reorder_at<Wide, WM>(base, bytes, e, parent);
   else if (low % 4 == 0)
-    for (long long e = at * 4; e < bytes; e += step * 4) reorder_at<uint32_t, WM>(base, bytes, e, parent, a.W);
+    for (long long e = at * 4; e < bytes; e += step * 4) reorder_at<uint32_t, WM>(base, bytes, e, parent);
   else
-    for (long long e = at; e < bytes; e += step) reorder_at<uint8_t, WM>(base, bytes, e, parent, a.W);
+    for (long long e = at; e < bytes; e += step) reorder_at<uint8_t, WM>(base, bytes, e, parent);
 }
 
 template <int MT>

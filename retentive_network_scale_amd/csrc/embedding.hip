@@ -3,9 +3,10 @@
 // The lookup streams: eight elements a thread, each moved once.
 //
 // The gradient of a row is a sum over the tokens that name it, in their order.  Three launches:
-//   1. Sort.  Each workgroup owns a range of ids and reads all tokens twice: once to count, once to
-//      place.  What lies below its range tells where its part of the order begins, so the
-//      workgroups need nothing from each other.
+//   1. Sort.  The tokens are ordered by (id modulo the number of workgroups, id, token).  Each workgroup
+//      owns the ids of one remainder, so that the frequent ones, which come first in a vocabulary, are spread, and
+//      reads all tokens twice: once to count, once to place.  What has a smaller remainder tells
+//      where its part of the order begins, so the workgroups need nothing from each other.
 //   2. Long runs.  Tokens come with the frequencies of words, so one id can have a tenth of them.  The
 //      order is cut into pieces of `piece` tokens, and runs longer than one are summed piece by piece.
 //   3. Rows.  Every row of the table's gradient is written once: the sum of a short run's tokens or of
@@ -45,41 +46,48 @@ __global__ __launch_bounds__(NT) void lookup_kernel(const int *ids, const TI *ta
 // -------------------------------------------------------------------------------- sort
 constexpr int SORT_NT = 1024, SORT_WAVES = SORT_NT / 64;
 constexpr int MAX_RANGE = 512;  // ids of a workgroup: 32 KB of counters
+constexpr int CHUNK = 512;      // tokens that a wave looks through before it places what it found
 
-// order[j]: the token at place j of the order by (id, token); start[v]: the place of v's first
-// token, start[V] their number.  Wave w of a workgroup reads the w-th part of the tokens; `bits` is the
-// width of an id within the range.
-__global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *order, int *start, int n, int V, int range,
-                                                       int bits) {
+// Workgroup b of 2^shift owns the ids b, b + 2^shift, ..: `range` of them at most, `bits` the width of their
+// number.  order[j]: the token at place j; runs[v]: the places of v's tokens, from .x up to .y; *total:
+// the number of tokens with an id in the table.  Wave w of a workgroup reads the w-th part of the tokens.
+__global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *order, int2 *runs, int *total, int n, int V,
+                                                       int shift, int bits) {
   __shared__ int at[SORT_WAVES][MAX_RANGE];  // tokens of a wave for an id, then where its next one goes
+  __shared__ int2 found[SORT_WAVES][CHUNK];
   __shared__ int red[SORT_WAVES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int v0 = blockIdx.x * range, mine = min(range, V - v0);
+  const int own = blockIdx.x, groups = 1 << shift, mine = own < V ? (V - 1 - own) / groups + 1 : 0;
   const int part = ((n + SORT_WAVES * 64 - 1) / (SORT_WAVES * 64)) * 64;
   const long long lo = (long long)wave * part, hi = lo + part < n ? lo + part : n;
   for (int i = lane; i < mine; i += 64) at[wave][i] = 0;
   __syncthreads();
   int below = 0;
+#pragma unroll 4
   for (long long t = lo + lane; t < hi; t += 64) {
     const int id = ids[t];
-    below += id >= 0 && id < v0;
-    if (id >= v0 && id < v0 + mine) atomicAdd(&at[wave][id - v0], 1);
+    if ((unsigned)id < (unsigned)V) {
+      const int rem = id & (groups - 1);
+      below += rem < own;
+      if (rem == own) atomicAdd(&at[wave][id >> shift], 1);
+    }
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off, 64);
   if (lane == 0) red[wave] = below;
   __syncthreads();
-  // wave 0: the counts' running sum over (id, wave), from the tokens below the range on
+  // wave 0: the counts' running sum over (id, wave), from the tokens of smaller remainders on
   if (wave == 0) {
     int base = 0;
 #pragma unroll
     for (int w = 0; w < SORT_WAVES; ++w) base += red[w];
     for (int i0 = 0; i0 < mine; i0 += 64) {
       const int i = i0 + lane;
-      int sum = 0;
-      if (i < mine)
+      int c[SORT_WAVES], sum = 0;
 #pragma unroll
-        for (int w = 0; w < SORT_WAVES; ++w) sum += at[w][i];
+      for (int w = 0; w < SORT_WAVES; ++w) c[w] = i < mine ? at[w][i] : 0;
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) sum += c[w];
       int incl = sum;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -88,107 +96,126 @@ __global__ __launch_bounds__(SORT_NT) void sort_kernel(const int *ids, int *orde
       }
       int p = base + incl - sum;
       if (i < mine) {
-        start[v0 + i] = p;
+        runs[own + (i << shift)] = make_int2(p, p + sum);
 #pragma unroll
         for (int w = 0; w < SORT_WAVES; ++w) {
-          const int c = at[w][i];
           at[w][i] = p;
-          p += c;
+          p += c[w];
         }
       }
       base += __shfl(incl, 63, 64);
     }
-    if (v0 + mine == V && lane == 0) start[V] = base;
+    if (own == groups - 1 && lane == 0) *total = base;
   }
   __syncthreads();
-  for (long long t0 = lo; t0 < hi; t0 += 64) {
-    const long long t = t0 + lane;
-    const int id = t < hi ? ids[t] : -1;
-    const bool in = id >= v0 && id < v0 + mine;
-    unsigned long long same = __ballot(in);  // the lanes of the same id, from one comparison a bit
-    if (!same) continue;
-    for (int bit = 0; bit < bits; ++bit) {
-      const bool one = (unsigned)(id - v0) >> bit & 1u;
-      const unsigned long long set = __ballot(one);
-      same &= one ? set : ~set;
+  for (long long t0 = lo; t0 < hi; t0 += CHUNK) {
+    // the tokens of the workgroup's ids, in order (a wave's LDS operations keep theirs)
+    int many = 0;
+#pragma unroll
+    for (int u = 0; u < CHUNK / 64; ++u) {
+      const long long t = t0 + u * 64 + lane;
+      const int id = t < hi ? ids[t] : -1;
+      const bool in = (unsigned)id < (unsigned)V && (id & (groups - 1)) == own;
+      const unsigned long long some = __ballot(in);
+      if (in) found[wave][many + __popcll(some & ((1ull << lane) - 1))] = make_int2(id >> shift, (int)t);
+      many += __popcll(some);
     }
-    // the first lane of an id takes the places of all of them
-    const int leader = __ffsll((long long)same) - 1;
-    int to = 0;
-    if (in && lane == leader) to = atomicAdd(&at[wave][id - v0], __popcll(same));
-    to = __shfl(to, leader, 64);
-    if (in) order[to + __popcll(same & ((1ull << lane) - 1))] = (int)t;
+    __builtin_amdgcn_wave_barrier();
+    for (int j0 = 0; j0 < many; j0 += 64) {
+      const bool in = j0 + lane < many;
+      const int2 f = in ? found[wave][j0 + lane] : make_int2(0, 0);
+      unsigned long long same = __ballot(in);  // the lanes of the same id, from one comparison a bit
+      for (int bit = 0; bit < bits; ++bit) {
+        const bool one = f.x >> bit & 1;
+        const unsigned long long set = __ballot(one);
+        same &= one ? set : ~set;
+      }
+      // the first lane of an id takes the places of all of them
+      const int leader = __ffsll((long long)same) - 1;
+      int to = 0;
+      if (in && lane == leader) to = atomicAdd(&at[wave][f.x], __popcll(same));
+      to = __shfl(to, leader, 64);
+      if (in) order[to + __popcll(same & ((1ull << lane) - 1))] = f.y;
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
 // -------------------------------------------------------------------------------- sums
-// Adds the tokens order[from .. to) to CH chunks of eight columns, the first at c, chunk k `step` further on.
-template <typename TI, int CH, int AHEAD>
-__device__ __forceinline__ void add_tokens(const TI *d_o, const int *order, int from, int to, long long ld, int c,
-                                           int step, int D, float (&sum)[CH][8]) {
-  int j = from;
-  for (; j + AHEAD <= to; j += AHEAD) {
-    float r[AHEAD][CH][8];
+// Adds tokens to CH chunks of eight columns, the first at c, chunk k `step` further on; AHEAD tokens' loads are
+// under way at a time.  token(j): the j-th of `many`.
+template <typename TI, int CH, int AHEAD, typename F>
+__device__ __forceinline__ void add_tokens(const TI *d_o, F token, int many, long long ld, int c, int step, int D,
+                                           float (&sum)[CH][8]) {
+  for (int j = 0; j < many; j += AHEAD) {
+    Raw8<TI> r[AHEAD][CH];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const TI *src = d_o + order[j + u] * ld + c;
+      const bool in = j + u < many;
+      const TI *src = d_o + token(in ? j + u : j) * ld + c;
 #pragma unroll
-      for (int k = 0; k < CH; ++k) load8(src + k * step, D - c - k * step, r[u][k]);
+      for (int k = 0; k < CH; ++k) r[u][k].load(src + k * step, in ? D - c - k * step : 0);
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
+      for (int k = 0; k < CH; ++k) {
+        float v[8];
+        r[u][k].get(v);
+        if (j + u < many)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[k][i] += r[u][k][i];
-  }
-  for (; j < to; ++j) {
-    const TI *src = d_o + order[j] * ld + c;
-    float r[CH][8];
-#pragma unroll
-    for (int k = 0; k < CH; ++k) load8(src + k * step, D - c - k * step, r[k]);
-#pragma unroll
-    for (int k = 0; k < CH; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[k][i] += r[k][i];
+          for (int i = 0; i < 8; ++i) sum[k][i] += v[i];
+      }
   }
 }
+
+constexpr int MAX_PIECE = 4096;
 
 // Piece blockIdx.x of the order: the part of the run that its first place belongs to, and of the run
 // that its last place belongs to where that is another, each only if the run is longer than a piece.
 template <typename TI>
-__global__ __launch_bounds__(NT) void piece_kernel(const int *ids, const TI *d_o, const int *order, const int *start,
-                                                   float *part, int V, int D, long long ld, int piece) {
-  const int total = start[V], j0 = blockIdx.x * piece, j1 = min(j0 + piece, total);
+__global__ __launch_bounds__(NT) void piece_kernel(const int *ids, const TI *d_o, const int *order, const int2 *runs,
+                                                   const int *total, float *part, int D, long long ld, int piece) {
+  __shared__ int tokens[MAX_PIECE];
+  const int j0 = blockIdx.x * piece, c = (blockIdx.y * NT + threadIdx.x) * 8;
+  const int j1 = min(j0 + piece, *total);
+  for (int j = j0 + threadIdx.x; j < j1; j += NT) tokens[j - j0] = order[j];
+  __syncthreads();
   if (j0 >= j1) return;
-  const int c = (blockIdx.y * NT + threadIdx.x) * 8;
-  const int a = ids[order[j0]], z = ids[order[j1 - 1]];
+  const int a = ids[tokens[0]], z = ids[tokens[j1 - j0 - 1]];
+  const int2 run[2] = {runs[a], runs[z]};
 #pragma unroll
   for (int slot = 0; slot < 2; ++slot) {
-    if (slot == 1 && z == a) break;
-    const int v = slot ? z : a, s = start[v], e = start[v + 1];
-    if (e - s <= piece || c >= D) continue;
+    const int s = run[slot].x, e = run[slot].y;
+    if ((slot == 1 && z == a) || e - s <= piece || c >= D) continue;
+    const int from = max(s, j0), many = min(e, j1) - from;
     float sum[1][8] = {};
-    add_tokens<TI, 1, 8>(d_o, order, max(s, j0), min(e, j1), ld, c, 0, D, sum);
+    add_tokens<TI, 1, 16>(d_o, [&](int j) { return tokens[from - j0 + j]; }, many, ld, c, 0, D, sum);
     store8(part + (2LL * blockIdx.x + slot) * D + c, D - c, sum[0]);
   }
 }
 
 // A row of the gradient by tpr lanes (a power of two up to a wave), CH chunks of eight columns each at a
-// time: a wave a row rather than a workgroup, since a row's time is that of start, order and tokens
-// one after the other.
+// time: a wave a row rather than a workgroup, since a row's time is that of its run, the run's tokens
+// and their rows, one after the other.
 template <typename TI, typename TO, int CH>
-__global__ __launch_bounds__(NT) void rows_kernel(const TI *d_o, const int *order, const int *start, const float *part,
+__global__ __launch_bounds__(NT) void rows_kernel(const TI *d_o, const int *order, const int2 *runs, const float *part,
                                                   TO *dtable, int V, int D, long long ld, int piece, int tpr,
                                                   float scale) {
   const int col = threadIdx.x & (tpr - 1), rows = NT / tpr, step = tpr * 8;
   const int v = blockIdx.x * rows + threadIdx.x / tpr;
   if (v >= V) return;
-  const int s = start ? start[v] : 0, e = start ? start[v + 1] : 0;
-  for (int c = col * 8; c < D; c += CH * step) {
+  const int2 run = runs ? runs[v] : make_int2(0, 0);
+  const int s = run.x, e = run.y;
+  for (int c = col * 8; c < D + col * 8; c += CH * step) {  // all of a row's lanes stay together
     float sum[CH][8] = {};
     if (e - s <= piece) {
-      add_tokens<TI, CH, CH >= 4 ? 2 : 4>(d_o, order, s, e, ld, c, step, D, sum);
+      for (int j = s; j < e; j += tpr) {
+        const int mine = order[min(j + col, e - 1)];
+        const int first = (threadIdx.x & 63) - col;
+        add_tokens<TI, CH, CH >= 4 ? 2 : 4>(d_o, [&](int i) { return __shfl(mine, first + i, 64); }, min(tpr, e - j), ld, c,
+                                            step, D, sum);
+      }
     } else {
       // a run that begins inside its first piece is that piece's second slot
       const int p0 = s / piece, p1 = (e - 1) / piece;
@@ -219,8 +246,8 @@ int threads_per_row(int D, int most) {
   return t;
 }
 
-// Tokens of a piece: about a quarter of the square root of their number, so that neither a piece nor the list
-// of pieces of one id is long (16384 tokens in pieces of 128 and 32: 73 and 9 us).
+// Tokens of a piece: about a quarter of the square root of their number, 4096 at most (of 2^28), so that neither a
+// piece nor the list of pieces of one id is long.
 int piece_of(long long n) {
   int p = 32;
   while (16LL * p * p < n) p *= 2;
@@ -228,13 +255,14 @@ int piece_of(long long n) {
 }
 
 struct EmbedWs {
-  size_t order, start, part, bytes;
+  size_t order, runs, total, part, bytes;
 };
 EmbedWs embed_ws(long long n, int V, int D) {
   EmbedWs w;
   w.order = 0;
-  w.start = rec_align((size_t)n * 4);
-  w.part = w.start + rec_align(((size_t)V + 1) * 4);
+  w.runs = rec_align((size_t)n * 4);
+  w.total = w.runs + rec_align((size_t)V * 8);
+  w.part = w.total + 256;
   w.bytes = w.part + rec_align((size_t)rec_cdiv(n, piece_of(n)) * 2 * D * 4);
   return w;
 }
@@ -302,25 +330,26 @@ extern "C" ret_status_t embedding_bwd(const int *ids, const void *d_o, void *dta
   }
   hipStream_t st = (hipStream_t)hip_stream;
   char *ws = (char *)workspace;
-  int *order = n ? (int *)(ws + w.order) : nullptr, *start = n ? (int *)(ws + w.start) : nullptr;
+  int *order = n ? (int *)(ws + w.order) : nullptr, *total = n ? (int *)(ws + w.total) : nullptr;
+  int2 *runs = n ? (int2 *)(ws + w.runs) : nullptr;
   float *part = n ? (float *)(ws + w.part) : nullptr;
   const int piece = piece_of(n), tpr = threads_per_row(D, 64);
   if (n > 0) {
-    const int range = (int)std::min<long long>(MAX_RANGE, std::max<long long>(1, rec_cdiv(V, 256)));
-    int bits = 0;
-    while (1 << bits < range) ++bits;
-    hipLaunchKernelGGL(sort_kernel, dim3((unsigned)rec_cdiv(V, range)), dim3(SORT_NT), 0, st, ids, order, start, (int)n,
-                       V, range, bits);
+    int shift = 8, bits = 0;  // 256 workgroups, or more where they would own more ids than they can count
+    while (V > MAX_RANGE << shift) ++shift;
+    while (1LL << (shift + bits) < V) ++bits;
+    hipLaunchKernelGGL(sort_kernel, dim3(1u << shift), dim3(SORT_NT), 0, st, ids, order, runs, total, (int)n, V, shift,
+                       bits);
   }
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     using TI = std::remove_pointer_t<decltype(ti)>;
     using TO = std::remove_pointer_t<decltype(to)>;
     if (n > piece)
       hipLaunchKernelGGL((piece_kernel<TI>), dim3((unsigned)rec_cdiv(n, piece), (unsigned)rec_cdiv(D, NT * 8)), dim3(NT),
-                         0, st, ids, (const TI *)d_o, order, start, part, V, D, o_ld, piece);
+                         0, st, ids, (const TI *)d_o, order, runs, total, part, D, o_ld, piece);
     auto rows = [&](auto chunks) {
       hipLaunchKernelGGL((rows_kernel<TI, TO, decltype(chunks)::value>), dim3((unsigned)rec_cdiv(V, NT / tpr)), dim3(NT), 0,
-                         st, (const TI *)d_o, order, start, part, (TO *)dtable, V, D, o_ld, piece, tpr, scale);
+                         st, (const TI *)d_o, order, runs, part, (TO *)dtable, V, D, o_ld, piece, tpr, scale);
     };
     if (D <= 512)
       rows(std::integral_constant<int, 1>{});

@@ -349,12 +349,19 @@ extern "C" ret_status_t group_norm_gate(const void *x, const void *gate, const f
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     return with_width(W, [&](auto tpr, auto chunks) {
-      constexpr int RT = decltype(chunks)::value == 1 ? 4 : 1;
-      hipLaunchKernelGGL((norm_fwd_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>,
-                                          decltype(tpr)::value, decltype(chunks)::value, RT>),
-                         dim3((unsigned)rec_cdiv(rec_cdiv(tokens, RT) * H, NT / decltype(tpr)::value)), dim3(NT), 0,
-                         (hipStream_t)hip_stream, a);
-      return hipGetLastError();
+      constexpr int T = decltype(tpr)::value, C = decltype(chunks)::value;
+      auto launch = [&](auto rt) {
+        constexpr int RT = decltype(rt)::value;
+        hipLaunchKernelGGL(
+            (norm_fwd_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>, T, C, RT>),
+            dim3((unsigned)rec_cdiv(rec_cdiv(tokens, RT) * H, NT / T)), dim3(NT), 0, (hipStream_t)hip_stream, a);
+        return hipGetLastError();
+      };
+      // four tokens a group of lanes where that leaves every CU eight workgroups: 131072 rows of 512 bf16
+      // values 130 -> 108 us, 5000 rows of 100 fp32 values 5.7 -> 10 us
+      if constexpr (C == 1)
+        if (rec_cdiv(tokens * H, 4 * (NT / T)) >= 2048) return launch(std::integral_constant<int, 4>{});
+      return launch(std::integral_constant<int, 1>{});
     });
   }));
 }

@@ -26,27 +26,36 @@ __device__ __forceinline__ Words4 raw8(const uint16_t *p, int n) {
 template <int M, int RW>
 __global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint16_t *w, int tokens, int N, int K,
                                                    long long x_ld, Finish f) {
-  constexpr int C = M * RW;
+  constexpr int C = M * RW, UNROLL = M <= 2 ? 4 : M <= 8 ? 2 : 1;
   static_assert(C <= 64 && (C & (C - 1)) == 0, "sums of a wave");
   const int lane = threadIdx.x & 63;
   const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * RW;
   if (n0 >= N) return;
   float acc[C] = {};  // [RW][M]
-#pragma unroll 2
-  for (int k = lane * 8; k < K; k += 512) {
+  auto add = [&](const Words4 (&wv)[RW], const Words4 &xv, int m) {
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[r * M + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wv[r].w[i]),
+                                                         __builtin_bit_cast(bf16x2, xv.w[i]), acc[r * M + m], false);
+  };
+  const int whole = K / 512 * 512;
+#pragma unroll UNROLL
+  for (int k = lane * 8; k < whole; k += 512) {
+    Words4 wv[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) wv[r] = *(const Words4 *)(w + (long long)min(n0 + r, N - 1) * K + k);
+#pragma unroll
+    for (int m = 0; m < M; ++m) add(wv, *(const Words4 *)(x + min(m, tokens - 1) * x_ld + k), m);
+  }
+  if (whole < K) {
+    const int k = whole + lane * 8;
     Words4 wv[RW];
 #pragma unroll
     for (int r = 0; r < RW; ++r) wv[r] = raw8(w + (long long)min(n0 + r, N - 1) * K + k, K - k);
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const Words4 xv = raw8(x + min(m, tokens - 1) * x_ld + k, K - k);
-#pragma unroll
-      for (int r = 0; r < RW; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[r * M + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wv[r].w[i]),
-                                                           __builtin_bit_cast(bf16x2, xv.w[i]), acc[r * M + m], false);
-    }
+    for (int m = 0; m < M; ++m) add(wv, raw8(x + min(m, tokens - 1) * x_ld + k, K - k), m);
   }
   int n = C;
 #pragma unroll
