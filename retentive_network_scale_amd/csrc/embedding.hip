@@ -213,13 +213,13 @@ __global__ __launch_bounds__(NT) void rows_kernel(const TI *d_o, const int *orde
       for (int j = s; j < e; j += tpr) {
         const int mine = order[min(j + col, e - 1)];
         const int first = (threadIdx.x & 63) - col;
-        add_tokens<TI, CH, CH >= 4 ? 2 : 4>(d_o, [&](int i) { return __shfl(mine, first + i, 64); }, min(tpr, e - j), ld, c,
+        add_tokens<TI, CH, 4>(d_o, [&](int i) { return __shfl(mine, first + i, 64); }, min(tpr, e - j), ld, c,
                                             step, D, sum);
       }
     } else {
       // a run that begins inside its first piece is that piece's second slot
       const int p0 = s / piece, p1 = (e - 1) / piece;
-#pragma unroll 4
+#pragma unroll 2
       for (int p = p0; p <= p1; ++p) {
         const float *src = part + (2LL * p + (p == p0 && s % piece != 0)) * D + c;
         float r[CH][8];

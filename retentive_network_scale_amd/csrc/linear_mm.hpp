@@ -10,9 +10,10 @@
 // Where there are too few tiles for the chip, k is cut, the parts' sums go to the workspace in
 // fp32, and a second launch joins them in order and finishes.
 //
-// M 16384, features 2048 -> 4096 (275 GFLOP): 228 us without and 248 us with bias and gelu, whose 18
-// operations an element follow the last matrix step with nothing to hide behind; dx 243 us, dw 272 us and 13 us
-// to join two parts.  The largest library product reaches 1385 TFLOP/s here, so 199 us would be the floor.
+// M 16384, features 2048 -> 4096 (275 GFLOP): 215 us without and 237 us with gelu, whose 18 operations an
+// element follow the last matrix step with nothing to hide behind; dx 211 us, dw 260 us and 17 us to join two
+// parts.  The largest library product reaches 1385 TFLOP/s here, so 199 us would be the floor.  What is left is the
+// wait at a tile's middle: with one workgroup a CU, whose 128 KB of LDS hold two tiles, all waves stand there.
 #pragma once
 
 #include "linear.hpp"
@@ -31,7 +32,9 @@ typedef __attribute__((address_space(3))) void lds_void;
 //     the next 32: a wave load takes 8 whole lines of 128 bytes (tiles of 32 k fetched every line
 //     twice and were bound by it: 128 x 128 tiles took 0.29 us a step of 32 k).  Chunk c (16 bytes) of
 //     a half's row r is at c ^ (r / 2 & 3): the 8 rows that a read takes together meet no bank twice.
-//   else: [64][R], chunk c of row k at c ^ 2 (k & 3), for reads that transpose
+//   else: [64][R], chunk c of row k at c ^ turn(k), for reads that transpose.  In rows of 256 columns the
+//     rows k + 8 .. are turned further than k ..: 32 lanes take them together (dx 234 -> 215 us; 128 columns
+//     were slower with it, 296 -> 321 us, and 64 have no chunks for it).
 template <int R, bool KROWS, int NT, bool DMA>
 struct Operand {
   static constexpr int SIZE = R * BK, NJ = SIZE * 2 / 1024 / (NT / 64);  // elements; wave loads of a wave
@@ -48,6 +51,7 @@ struct Operand {
   }
   // The wave, as a scalar.
   static __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+  static __device__ __forceinline__ int turn(int k) { return 2 * (R >= 256 ? (k & 3) | (k >> 1 & 4) : k & 3); }
   // What chunk j of this thread holds: a row and one of its 16-byte chunks (KROWS: of k, else of columns).
   static __device__ __forceinline__ void place(int j, int &row, int &c) {
     const int piece = wave() * NJ + j, lane = threadIdx.x & 63;
@@ -58,7 +62,7 @@ struct Operand {
     } else {
       const int off = piece * 1024 + lane * 16;
       row = off / (R * 2);
-      c = off % (R * 2) / 16 ^ 2 * (row & 3);
+      c = off % (R * 2) / 16 ^ turn(row);
     }
   }
   // The tile at k0 on its way to `lds` (DMA) or to registers; k from `kend` on is zero.
@@ -113,7 +117,7 @@ struct Operand {
     } else {
       // within 16 lanes, lane r receives element r % 4 of the pieces that lanes 4 j + r / 4 address
       const int row = h * 32 + 8 * g + (l16 >> 2), c = (r0 >> 3) + ((l16 & 3) >> 1);
-      const uint16_t *p = lds + row * R + ((c ^ 2 * (row & 3)) << 3) + 4 * (l16 & 1);
+      const uint16_t *p = lds + row * R + ((c ^ turn(row)) << 3) + 4 * (l16 & 1);
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p + 4 * R));
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -187,14 +191,21 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
       for (int j = 0; j < FN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fq[h][j], fp[h][i], acc[i][j], 0, 0, 0);
   };
-  // the reads go out between the first matrix instructions
-  auto interleave = [] {
-    constexpr int READS = (PK ? FM : 2 * FM) + (QK ? FN : 2 * FN);
+  // the reads, and then the loads, go out between the matrix instructions: loads issued in a row keep a wave from
+  // its matrix instructions (fwd 221 -> 215 us)
+  auto interleave = [](auto loads) {
+    constexpr int READS = (PK ? FM : 2 * FM) + (QK ? FN : 2 * FN), REST = FM * FN - READS;
 #pragma unroll
     for (int r = 0; r < READS; ++r) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // and a matrix instruction
     }
+    if constexpr (decltype(loads)::value)
+#pragma unroll
+      for (int r = 0; r < LOADS; ++r) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a load from memory
+        __builtin_amdgcn_sched_group_barrier(0x008, REST / LOADS > 1 ? REST / LOADS : 1, 0);
+      }
   };
   if constexpr (DMA) {
     // tiles behind the last are fetched as zeros, so that all steps are alike
@@ -207,14 +218,15 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
     for (int i = 0; i < tiles_k; ++i) {
       read(slot, 1);
       multiply(0);
-      interleave();
+      interleave(std::false_type{});
       wait_loads<(NB - 2) * LOADS>();
       meet();
-      fetch(i + NB, slot);
+      const int free = slot;
       slot = slot + 1 == NB ? 0 : slot + 1;
       read(slot, 0);
+      fetch(i + NB, free);
       multiply(1);
-      interleave();
+      interleave(std::true_type{});
     }
   } else {
     if (tiles_k > 0) fetch(0, 0);
@@ -297,9 +309,7 @@ hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   a.kpart = p.kpart;
   a.part = p.parts > 1 ? (float *)ws : nullptr;
   const bool dma = chunked(a.p, a.ldp, PK ? a.K : a.M) && chunked(a.q, a.ldq, QK ? a.K : a.N);
-  // of 256 x 256, a wave takes 64 x 128, or, where Q's operands cost two reads each, 128 x 64: 227 and 232 us
-  // forward, 252 and 243 us for dx (M 16384, features 2048 and 4096)
-  hipError_t e = p.tile == 256   ? launch_tile<256, 256, QK ? 4 : 2, QK ? 2 : 4, PK, QK>(a, p.parts, dma, st)
+  hipError_t e = p.tile == 256   ? launch_tile<256, 256, 2, 4, PK, QK>(a, p.parts, dma, st)
                  : p.tile == 128 ? launch_tile<128, 128, 2, 2, PK, QK>(a, p.parts, dma, st)
                                  : launch_tile<64, 64, 2, 2, PK, QK>(a, p.parts, dma, st);
   if (e != hipSuccess || p.parts == 1) return e;
