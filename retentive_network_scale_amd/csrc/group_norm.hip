@@ -67,30 +67,12 @@ __device__ __forceinline__ float normalise(float (&x)[C][8], int col, int W, flo
   return 1.0f / sqrtf(row_sum<TPR>(q) / (float)W + eps);
 }
 
-// A group of lanes takes RT tokens of one head, their loads all under way from the start, and the head's weight
-// and bias once for all of them.
-template <typename TI, typename TO, int TPR, int C, int RT>
+// The forward kernel, for the head blockIdx.y: tokens blockIdx.x * RB + row, then parts * RB further on, whose
+// loads are under way while one is computed.
+template <typename TI, typename TO, int TPR, int C>
 __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs a) {
-  const int col = threadIdx.x & (TPR - 1);
-  // (tokens, head); the launch's threads fit 32 bits, so the groups do
-  const unsigned group = blockIdx.x * (NT / TPR) + threadIdx.x / TPR, tokens = (unsigned)a.B * a.L;
-  const unsigned run = group / (unsigned)a.H, h = group - run * a.H;
-  if (run * RT >= tokens) return;
-  Raw8<TI> xr[RT][C], gr[RT][C];
-  bool live[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const unsigned tok = run * RT + j, b = tok / (unsigned)a.L, t = tok - b * a.L;
-    live[j] = tok < tokens && (!a.lengths || (int)t < a.lengths[b]);
-    const TI *xp = (const TI *)a.x + (long long)b * a.x_sb + h * a.x_sh + t * a.x_sl;
-    const TI *gp = (const TI *)a.gate + tok * a.gate_ld + (long long)h * a.W;
-#pragma unroll
-    for (int k = 0; k < C; ++k) {
-      const int c = (k * TPR + col) * 8, n = live[j] ? a.W - c : 0;
-      xr[j][k].load(xp + c, n);
-      if (a.gate) gr[j][k].load(gp + c, n);
-    }
-  }
+  constexpr int RB = NT / TPR;
+  const int col = threadIdx.x & (TPR - 1), h = blockIdx.y;
   float w[C][8], bias[C][8];
 #pragma unroll
   for (int k = 0; k < C; ++k) {
@@ -98,25 +80,44 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs a) {
     if (a.weight) load8(a.weight + (long long)h * a.W + c, a.W - c, w[k]);
     if (a.bias) load8(a.bias + (long long)h * a.W + c, a.W - c, bias[k]);
   }
+  const unsigned tokens = (unsigned)a.B * a.L, step = a.parts * RB;
+  Raw8<TI> xr[C], gr[C];
+  bool live = false;
+  auto fetch = [&](unsigned tok) {
+    const unsigned b = tok / (unsigned)a.L, t = tok - b * a.L;
+    live = tok < tokens && (!a.lengths || (int)t < a.lengths[b]);
+    const TI *xp = (const TI *)a.x + (long long)b * a.x_sb + h * a.x_sh + t * a.x_sl;
+    const TI *gp = (const TI *)a.gate + tok * a.gate_ld + (long long)h * a.W;
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    if (!live[j]) continue;
-    float x[C][8];
+    for (int k = 0; k < C; ++k) {
+      const int c = (k * TPR + col) * 8, n = live ? a.W - c : 0;
+      xr[k].load(xp + c, n);
+      if (a.gate) gr[k].load(gp + c, n);
+    }
+  };
+  unsigned tok = blockIdx.x * RB + threadIdx.x / TPR;
+  fetch(tok);
+  for (; tok < tokens; tok += step) {
+    const bool now = live;
+    float x[C][8], g[C][8];
 #pragma unroll
-    for (int k = 0; k < C; ++k) xr[j][k].get(x[k]);
+    for (int k = 0; k < C; ++k) {
+      xr[k].get(x[k]);
+      if (a.gate) gr[k].get(g[k]);
+    }
+    fetch(tok + step);
+    if (!now) continue;
     const float r = normalise<TPR, C>(x, col, a.W, a.eps);
-    TO *out = (TO *)a.out + (long long)(run * RT + j) * a.H * a.W + (long long)h * a.W;
+    TO *out = (TO *)a.out + (long long)tok * a.H * a.W + (long long)h * a.W;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8;
-      float g[8];
-      if (a.gate) gr[j][k].get(g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float n = x[k][i] * r;
         if (a.weight) n *= w[k][i];
         if (a.bias) n += bias[k][i];
-        x[k][i] = a.gate ? n * act_of(g[i], a.silu) : act_of(n, a.silu);
+        x[k][i] = a.gate ? n * act_of(g[k][i], a.silu) : act_of(n, a.silu);
       }
       store8(out + c, a.W - c, x[k]);
     }
@@ -268,10 +269,9 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int 
   }
 }
 
-// Workgroups of a head in the gradients: about eight of 512 threads for each of the 256 CUs together,
-// and no more than there are tokens for.
-int parts_of(long long tokens, int H, int tpr) {
-  const long long most = rec_cdiv(tokens, BWD_NT / tpr), want = std::max<long long>(1, 2048 / H);
+// Workgroups of a head: 4096 threads for each of the 256 CUs together, and no more than there are tokens for.
+int parts_of(long long tokens, int H, int tpr, int threads) {
+  const long long most = rec_cdiv(tokens, threads / tpr), want = std::max<long long>(1, 2048 * BWD_NT / threads / H);
   return (int)std::max<long long>(1, std::min(most, want));
 }
 
@@ -347,28 +347,20 @@ extern "C" ret_status_t group_norm_gate(const void *x, const void *gate, const f
                          {"lengths", lengths, (size_t)B * 4}};
   const RecSpan outs[] = {{"out", out, (size_t)tokens * width * oe}};
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
+  a.parts = parts_of(tokens, H, tpr_of(W), NT);
   return rec_status(with_types(in_dtype, out_dtype, [&](auto ti, auto to) {
     return with_width(W, [&](auto tpr, auto chunks) {
-      constexpr int T = decltype(tpr)::value, C = decltype(chunks)::value;
-      auto launch = [&](auto rt) {
-        constexpr int RT = decltype(rt)::value;
-        hipLaunchKernelGGL(
-            (norm_fwd_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>, T, C, RT>),
-            dim3((unsigned)rec_cdiv(rec_cdiv(tokens, RT) * H, NT / T)), dim3(NT), 0, (hipStream_t)hip_stream, a);
-        return hipGetLastError();
-      };
-      // four tokens a group of lanes where that leaves every CU eight workgroups: 131072 rows of 512 bf16
-      // values 130 -> 108 us, 5000 rows of 100 fp32 values 5.7 -> 10 us
-      if constexpr (C == 1)
-        if (rec_cdiv(tokens * H, 4 * (NT / T)) >= 2048) return launch(std::integral_constant<int, 4>{});
-      return launch(std::integral_constant<int, 1>{});
+      hipLaunchKernelGGL((norm_fwd_kernel<std::remove_pointer_t<decltype(ti)>, std::remove_pointer_t<decltype(to)>,
+                                          decltype(tpr)::value, decltype(chunks)::value>),
+                         dim3((unsigned)a.parts, (unsigned)H), dim3(NT), 0, (hipStream_t)hip_stream, a);
+      return hipGetLastError();
     });
   }));
 }
 
 extern "C" size_t group_norm_gate_bwd_workspace_bytes(int B, int H, int L, int W) {
   if (check_sizes(B, H, L, W) != RET_OK || L == 0) return 0;
-  return rec_align((size_t)parts_of((long long)B * L, H, tpr_of(W)) * 2 * H * W * 4);
+  return rec_align((size_t)parts_of((long long)B * L, H, tpr_of(W), BWD_NT) * 2 * H * W * 4);
 }
 
 extern "C" ret_status_t group_norm_gate_bwd(const void *x, const void *gate, const float *weight, const float *bias,
@@ -392,7 +384,7 @@ extern "C" ret_status_t group_norm_gate_bwd(const void *x, const void *gate, con
       !rec_aligned(bias, 4) || !rec_aligned(dx, oe) || !rec_aligned(dgate, oe) || !rec_aligned(dweight, 4) ||
       !rec_aligned(dbias, 4) || !rec_aligned(lengths, 4))
     return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  a.parts = parts_of(tokens, H, tpr_of(W));
+  a.parts = parts_of(tokens, H, tpr_of(W), BWD_NT);
   const size_t need = sums && L > 0 ? (size_t)a.parts * 2 * width * 4 : 0;
   if (need && (!workspace || workspace_bytes < need))
     return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed", need);

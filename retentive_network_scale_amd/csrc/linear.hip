@@ -10,72 +10,73 @@ namespace {
 // --------------------------------------------------------------------------- few tokens
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 
-// Eight bf16 elements as they are, the first n of them (any alignment).
-__device__ __forceinline__ Words4 raw8(const uint16_t *p, int n) {
-  Words4 v = {{0u, 0u, 0u, 0u}};
-  if (n >= 8) return *(const Words4 *)p;
+// Adds the lanes' N values over lanes: each step halves the number of values a lane holds, as long as
+// there is more than one.
+template <int N, int OFF, int C>
+__device__ __forceinline__ void fold(float (&v)[C], int lane) {
+  if constexpr (OFF > 0) {
+    if constexpr (N > 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) v.w[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
-  return v;
+      for (int i = 0; i < N / 2; ++i) {
+        const float mine = lane & OFF ? v[i + N / 2] : v[i], other = lane & OFF ? v[i] : v[i + N / 2];
+        v[i] = mine + __shfl_xor(other, OFF, 64);
+      }
+      fold<N / 2, OFF / 2>(v, lane);
+    } else {
+      v[0] += __shfl_xor(v[0], OFF, 64);
+      fold<1, OFF / 2>(v, lane);
+    }
+  }
 }
 
-// A wave takes RW rows of w, which it reads at full width, a lane 8 k of each 512; M tokens at most.  The
-// lanes' RW M sums are added so that each step halves their number: value i ends in lane i 64 / (RW M).
-// Bound by the launch and the way from memory: one token, N 4096, K 2048 (16.8 MB).
+// A workgroup takes RW rows of w, its four waves take turns along k, 512 at a time, a lane 8 of them; M tokens at
+// most.  w is read once at full width, x comes from the caches.  Each wave's RW M sums end in as many lanes,
+// and the waves' are added in LDS.  Bound by the launch and the way from memory for one token (N 4096, K 2048,
+// 16.8 MB: 3.4 us) and by the caches' way for x with more of them.
 template <int M, int RW>
 __global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint16_t *w, int tokens, int N, int K,
                                                    long long x_ld, Finish f) {
-  constexpr int C = M * RW, UNROLL = M <= 2 ? 4 : M <= 8 ? 2 : 1;
+  constexpr int C = M * RW;
   static_assert(C <= 64 && (C & (C - 1)) == 0, "sums of a wave");
-  const int lane = threadIdx.x & 63;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * RW;
-  if (n0 >= N) return;
+  __shared__ float red[4][C];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = blockIdx.x * RW;
   float acc[C] = {};  // [RW][M]
-  auto add = [&](const Words4 (&wv)[RW], const Words4 &xv, int m) {
+  auto add = [&](const Raw8<uint16_t> (&wv)[RW], const Raw8<uint16_t> &xv, int m) {
 #pragma unroll
     for (int r = 0; r < RW; ++r)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        acc[r * M + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wv[r].w[i]),
-                                                         __builtin_bit_cast(bf16x2, xv.w[i]), acc[r * M + m], false);
+        acc[r * M + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, wv[r].w[0].w[i]),
+                                                         __builtin_bit_cast(bf16x2, xv.w[0].w[i]), acc[r * M + m], false);
   };
   const int whole = K / 512 * 512;
-#pragma unroll UNROLL
-  for (int k = lane * 8; k < whole; k += 512) {
-    Words4 wv[RW];
+  for (int k = wave * 512 + lane * 8; k < whole; k += 2048) {
+    Raw8<uint16_t> wv[RW], xv;
 #pragma unroll
-    for (int r = 0; r < RW; ++r) wv[r] = *(const Words4 *)(w + (long long)min(n0 + r, N - 1) * K + k);
+    for (int r = 0; r < RW; ++r) wv[r].load(w + (long long)min(n0 + r, N - 1) * K + k, 8);
 #pragma unroll
-    for (int m = 0; m < M; ++m) add(wv, *(const Words4 *)(x + min(m, tokens - 1) * x_ld + k), m);
-  }
-  if (whole < K) {
-    const int k = whole + lane * 8;
-    Words4 wv[RW];
-#pragma unroll
-    for (int r = 0; r < RW; ++r) wv[r] = raw8(w + (long long)min(n0 + r, N - 1) * K + k, K - k);
-#pragma unroll
-    for (int m = 0; m < M; ++m) add(wv, raw8(x + min(m, tokens - 1) * x_ld + k, K - k), m);
-  }
-  int n = C;
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    if (n > 1) {
-      n /= 2;
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i)
-        if (i < n) {
-          const bool up = lane & off;
-          const float mine = up ? acc[i + n] : acc[i], other = up ? acc[i] : acc[i + n];
-          acc[i] = mine + __shfl_xor(other, off, 64);
-        }
-    } else {
-      acc[0] += __shfl_xor(acc[0], off, 64);
+    for (int m = 0; m < M; ++m) {
+      xv.load(x + min(m, tokens - 1) * x_ld + k, 8);
+      add(wv, xv, m);
     }
   }
-  const int value = lane / (64 / C), m = value % M, col = n0 + value / M;
-  if (lane % (64 / C) == 0 && m < tokens && col < N) {
-    float v = acc[0];
+  if (whole < K && wave == (whole / 512 & 3)) {
+    const int k = whole + lane * 8;
+    Raw8<uint16_t> wv[RW], xv;
+#pragma unroll
+    for (int r = 0; r < RW; ++r) wv[r].load(w + (long long)min(n0 + r, N - 1) * K + k, K - k);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      xv.load(x + min(m, tokens - 1) * x_ld + k, K - k);
+      add(wv, xv, m);
+    }
+  }
+  fold<C, 32>(acc, lane);
+  if (lane % (64 / C) == 0) red[wave][lane / (64 / C)] = acc[0];
+  __syncthreads();
+  const int value = threadIdx.x, m = value % M, col = n0 + value / M;
+  if (value < C && m < tokens && col < N) {
+    float v = red[0][value] + red[1][value] + red[2][value] + red[3][value];
     const long long at = (long long)m * N + col;
     if (f.bias) v += bf2f(f.bias[col]);
     if (f.pre) f.pre[at] = f2bf(v);
@@ -140,12 +141,14 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float *part, int 
 }
 
 // ------------------------------------------------------------------------------- host
-constexpr long long FEW = 16;  // tokens that rows_kernel serves
+// Whether rows_kernel serves a call.  It and the tiles take, in us, for 8 tokens 5.8 and 8.8 (N 4096, K 2048), for
+// 16 tokens 6.5 and 9.2 (1000, 1000), 8.6 and 8.8 (4096, 2048), 46 and 21 (32000, 2048).
+bool few(long long M, long long N, long long K) { return M <= 8 || (M <= 16 && N * K <= 1 << 23); }
 
 template <int M, int RW>
 hipError_t launch_rows(const void *x, const void *w, int tokens, int N, int K, long long x_ld, const Finish &f,
                        hipStream_t st) {
-  hipLaunchKernelGGL((rows_kernel<M, RW>), dim3((unsigned)rec_cdiv(N, 4 * RW)), dim3(256), 0, st, (const uint16_t *)x,
+  hipLaunchKernelGGL((rows_kernel<M, RW>), dim3((unsigned)rec_cdiv(N, RW)), dim3(256), 0, st, (const uint16_t *)x,
                      (const uint16_t *)w, tokens, N, K, x_ld, f);
   return hipGetLastError();
 }
@@ -180,7 +183,7 @@ BwdWs bwd_ws(long long M, int N, int K) {
 }  // namespace
 
 extern "C" size_t linear_workspace_bytes(long long M, int N, int K) {
-  if (check_sizes(M, N, K) != RET_OK || M <= FEW) return 0;
+  if (check_sizes(M, N, K) != RET_OK || few(M, N, K)) return 0;
   return mm_plan(M, N, K).bytes;
 }
 
@@ -214,12 +217,12 @@ extern "C" ret_status_t linear(const void *x, const void *w, const void *bias, c
   f.bias = (const uint16_t *)bias, f.residual = residual, f.out = out, f.pre = (uint16_t *)pre;
   f.act = act, f.res_bf16 = residual_dtype == RET_BF16, f.out_bf16 = out_dtype == RET_BF16;
   hipStream_t st = (hipStream_t)hip_stream;
-  if (M <= FEW) {
+  if (few(M, N, K)) {
     const int m = (int)M;
-    return rec_status(m == 1   ? launch_rows<1, 2>(x, w, m, N, K, x_ld, f, st)
-                      : m == 2 ? launch_rows<2, 2>(x, w, m, N, K, x_ld, f, st)
-                      : m <= 4 ? launch_rows<4, 2>(x, w, m, N, K, x_ld, f, st)
-                      : m <= 8 ? launch_rows<8, 2>(x, w, m, N, K, x_ld, f, st)
+    return rec_status(m == 1   ? launch_rows<1, 4>(x, w, m, N, K, x_ld, f, st)
+                      : m == 2 ? launch_rows<2, 4>(x, w, m, N, K, x_ld, f, st)
+                      : m <= 4 ? launch_rows<4, 4>(x, w, m, N, K, x_ld, f, st)
+                      : m <= 8 ? launch_rows<8, 4>(x, w, m, N, K, x_ld, f, st)
                                : launch_rows<16, 4>(x, w, m, N, K, x_ld, f, st));
   }
   MmArgs a = {};

@@ -139,7 +139,7 @@ inline MmPlan mm_plan(long long M, long long N, long long K) {
       if (real != parts) continue;
       const double fullest = (double)rec_cdiv(tiles * parts, 256);
       double t = each * std::max(k.alone, fullest * k.each) + k.end;
-      if (parts > 1) t += 2.5 + (double)M * N * (8 * parts + 2) / 4.5e6;
+      if (parts > 1) t += 5.0 + (double)M * N * (8 * parts + 2) / 4.5e6;
       if (t < least) {
         least = t;
         best.tile = k.tile;
