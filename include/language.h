@@ -35,6 +35,7 @@ extern "C" {
 #define LANGUAGE_MAX_NORM_WIDTH 2048      /* W of the norm */
 #define LANGUAGE_MAX_FEATURES (1 << 22)   /* N and K of linear */
 #define LANGUAGE_MAX_BEAMS 64             /* W and K of beam_select, W of beam_reorder */
+#define LANGUAGE_MAX_BEAM_ROWS (1 << 23)  /* B * W of beam_select */
 #define LANGUAGE_MAX_BEAM_LISTS 2048      /* W * ceil(V / 2048) of beam_select */
 #define LANGUAGE_MAX_REORDERED 64         /* tensors of one beam_reorder */
 #define LANGUAGE_MAX_REORDER_BATCH 65535  /* B of beam_reorder */

@@ -417,7 +417,7 @@ SelectWs select_ws(long long rows, int V, int K) {
 ret_status_t check_sizes(int B, int W, int V, int K) {
   if (B < 0 || W <= 0 || V <= 0 || K <= 0) return rec_fail(RET_ERR_INVALID_ARG, "sizes must be positive");
   if ((long long)W * V < K) return rec_fail(RET_ERR_INVALID_ARG, "K above W V");
-  if (W > LANGUAGE_MAX_BEAMS || K > LANGUAGE_MAX_BEAMS || V > LANGUAGE_MAX_VOCAB || (long long)B * W > (1LL << 24) ||
+  if (W > LANGUAGE_MAX_BEAMS || K > LANGUAGE_MAX_BEAMS || V > LANGUAGE_MAX_VOCAB || (long long)B * W > LANGUAGE_MAX_BEAM_ROWS ||
       W * rec_cdiv(V, NT * 8) > LANGUAGE_MAX_BEAM_LISTS)
     return rec_fail(RET_ERR_UNSUPPORTED, "B, W, V or K too large");
   return RET_OK;

@@ -296,8 +296,6 @@ ret_status_t check_sizes(int B, int H, int L, int W) {
   if (W > LANGUAGE_MAX_NORM_WIDTH || width > LANGUAGE_MAX_CHANNELS || H > 65535 || tokens > LANGUAGE_MAX_TOKENS ||
       (double)tokens * width > (double)LANGUAGE_MAX_ELEMENTS)
     return rec_fail(RET_ERR_UNSUPPORTED, "B, H, L or W too large");
-  if (!rec_grid_ok((double)rec_cdiv(tokens * H, NT / tpr_of(W)), NT))
-    return rec_fail(RET_ERR_UNSUPPORTED, "too many rows for one launch");
   return RET_OK;
 }
 

@@ -68,16 +68,35 @@ struct Finish {
   int act, res_bf16, out_bf16;
 };
 
-// z's elements n .. n + 7 of row m (of N a row), as far as there are any: bias, activation, residual.
-__device__ __forceinline__ void finish8(const Finish &f, long long m, int n, int N, float (&z)[8]) {
-  const long long at = m * N + n;
-  const int left = N - n;
-  float r[8];
-  if (f.bias) {
-    load8(f.bias + n, left, r);
+// Eight elements of the residual on their way, of either type.
+struct Residual8 {
+  Raw8<uint16_t> h;
+  Raw8<float> s;
+  __device__ __forceinline__ void load(const Finish &f, long long at, int left) {
+    if (!f.residual) return;
+    if (f.res_bf16)
+      h.load((const uint16_t *)f.residual + at, left);
+    else
+      s.load((const float *)f.residual + at, left);
+  }
+  __device__ __forceinline__ void add(const Finish &f, float (&z)[8]) const {
+    if (!f.residual) return;
+    float r[8];
+    if (f.res_bf16)
+      h.get(r);
+    else
+      s.get(r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += r[i];
   }
+};
+
+// Eight of z's elements, `left` of which exist, at `at` of [M][N]: bias (zero where there is none), activation,
+// residual.
+__device__ __forceinline__ void finish8(const Finish &f, long long at, int left, const float (&bias)[8],
+                                        const Residual8 &res, float (&z)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] += bias[i];
   if (f.pre) store8(f.pre + at, left, z);
   if (f.act == LINEAR_ACT_GELU) {
 #pragma unroll
@@ -86,14 +105,7 @@ __device__ __forceinline__ void finish8(const Finish &f, long long m, int n, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= sigmoid(z[i]);
   }
-  if (f.residual) {
-    if (f.res_bf16)
-      load8((const uint16_t *)f.residual + at, left, r);
-    else
-      load8((const float *)f.residual + at, left, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += r[i];
-  }
+  res.add(f, z);
   if (f.out_bf16)
     store8((uint16_t *)f.out + at, left, z);
   else
@@ -112,7 +124,7 @@ struct MmArgs {
 };
 
 struct MmPlan {
-  int tile;  // rows and columns of a tile: 64, 128 or 256
+  int rows, cols;  // of a tile: 64 x 64, 64 x 128, 128 x 128 or 256 x 256
   int parts;
   long long kpart;
   size_t bytes;  // of the parts' sums
@@ -126,23 +138,24 @@ struct MmPlan {
 // 12, 21 and 45; four parts for M 16, N 2048, K 4096: 18.8 -> 10.7 us.
 inline MmPlan mm_plan(long long M, long long N, long long K) {
   struct {
-    int tile;
+    int rows, cols;
     double alone, each, end;
-  } const kinds[] = {{64, 0.27, 0.23, 0.7}, {128, 0.50, 0.53, 1.5}, {256, 1.25, 1.70, 3.0}};
+  } const kinds[] = {{64, 64, 0.27, 0.23, 0.7}, {64, 128, 0.38, 0.35, 1.0}, {128, 128, 0.50, 0.53, 1.5}, {256, 256, 1.25, 1.70, 3.0}};
   const long long steps = std::max<long long>(1, rec_cdiv(K, BK));
   MmPlan best = {};
-  double least = 1e30;
+  double least = 1e300;
   for (const auto &k : kinds) {
-    const long long tiles = std::max<long long>(1, rec_cdiv(M, k.tile) * rec_cdiv(N, k.tile));
+    const long long tiles = std::max<long long>(1, rec_cdiv(M, k.rows) * rec_cdiv(N, k.cols));
     for (long long parts = 1; parts <= 32 && (parts == 1 || 2 * parts <= steps); parts *= 2) {
       const long long each = rec_cdiv(steps, parts), real = rec_cdiv(steps, each);
-      if (real != parts) continue;
+      if (real != parts || !rec_grid_ok((double)tiles, 512)) continue;
       const double fullest = (double)rec_cdiv(tiles * parts, 256);
       double t = each * std::max(k.alone, fullest * k.each) + k.end;
       if (parts > 1) t += 5.0 + (double)M * N * (8 * parts + 2) / 4.5e6;
       if (t < least) {
         least = t;
-        best.tile = k.tile;
+        best.rows = k.rows;
+        best.cols = k.cols;
         best.parts = (int)parts;
         best.kpart = each * BK;
       }

@@ -247,24 +247,37 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
   // at a time, they become runs of eight neighbours, which are finished and stored together.
   wait_loads<0>();
   meet();
-  constexpr int TN = BN / WN, PITCH = TN + 4, ROWS = 512 / TN;  // ROWS rows in a pass of 64 lanes
+  // The bias is read once and the residual 16 rows ahead.
+  constexpr int TN = BN / WN, PITCH = TN + 4, ROWS = 512 / TN, PASSES = 16 / ROWS;  // ROWS rows in a pass of 64 lanes
   static_assert(NT / 64 * 16 * PITCH * 4 <= (int)sizeof(lds) && ROWS <= 16, "the waves' patches");
   float *patch = (float *)lds + wave * 16 * PITCH;
+  const int c = lane % (TN / 8) * 8, r0 = lane / (TN / 8), n = n0 + wn + c;
+  float bias[8] = {};
+  if (a.f.bias && !a.part) load8(a.f.bias + n, a.N - n, bias);
+  Residual8 res[2][PASSES];
+  auto row = [&](int i, int q) { return m0 + wm + i * 16 + q * ROWS + r0; };
+  auto ahead = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < PASSES; ++q)
+      if (!a.part) res[i & 1][q].load(a.f, row(i, q) * a.N + n, row(i, q) < a.M ? a.N - n : 0);
+  };
+  ahead(0);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
+    if (i + 1 < FM) ahead(i + 1);
 #pragma unroll
     for (int j = 0; j < FN; ++j) *(f32x4 *)(patch + l16 * PITCH + j * 16 + 4 * g) = acc[i][j];
-#pragma unroll 1
-    for (int r = lane / (TN / 8); r < 16; r += ROWS) {
-      const int c = lane % (TN / 8) * 8, n = n0 + wn + c;
-      const long long m = m0 + wm + i * 16 + r;
+#pragma unroll
+    for (int q = 0; q < PASSES; ++q) {
+      const int r = q * ROWS + r0;
       const f32x4 lo = *(const f32x4 *)(patch + r * PITCH + c), hi = *(const f32x4 *)(patch + r * PITCH + c + 4);
       float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      const long long m = row(i, q);
       if (m < a.M && n < a.N) {
         if (a.part)
           store8(a.part + ((long long)blockIdx.y * a.M + m) * a.N + n, a.N - n, z);
         else
-          finish8(a.f, m, n, a.N, z);
+          finish8(a.f, m * a.N + n, a.N - n, bias, res[i & 1][q], z);
       }
     }
   }
@@ -277,6 +290,8 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, int par
   if (e >= M * runs) return;
   const long long m = e / runs;
   const int n = (int)(e - m * runs) * 8;
+  Residual8 res;
+  res.load(f, m * N + n, N - n);
   float z[8] = {};
 #pragma unroll 4
   for (int p = 0; p < parts; ++p) {
@@ -285,14 +300,16 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, int par
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += v[i];
   }
-  finish8(f, m, n, N, z);
+  float bias[8] = {};
+  if (f.bias) load8(f.bias + n, N - n, bias);
+  finish8(f, m * N + n, N - n, bias, res, z);
 }
 
-template <int BM, int BN, int WM, int WN, bool PK, bool QK>
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK>
 hipError_t launch_tile(const MmArgs &a, int parts, bool dma, hipStream_t st) {
   const dim3 grid((unsigned)(rec_cdiv(a.M, BM) * rec_cdiv(a.N, BN)), (unsigned)parts);
   if (dma)
-    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, 2, PK, QK, true>), grid, dim3(WM * WN * 64), 0, st, a);
+    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, NB, PK, QK, true>), grid, dim3(WM * WN * 64), 0, st, a);
   else
     hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, 2, PK, QK, false>), grid, dim3(WM * WN * 64), 0, st, a);
   return hipGetLastError();
@@ -309,9 +326,10 @@ hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   a.kpart = p.kpart;
   a.part = p.parts > 1 ? (float *)ws : nullptr;
   const bool dma = chunked(a.p, a.ldp, PK ? a.K : a.M) && chunked(a.q, a.ldq, QK ? a.K : a.N);
-  hipError_t e = p.tile == 256   ? launch_tile<256, 256, 2, 4, PK, QK>(a, p.parts, dma, st)
-                 : p.tile == 128 ? launch_tile<128, 128, 2, 2, PK, QK>(a, p.parts, dma, st)
-                                 : launch_tile<64, 64, 2, 2, PK, QK>(a, p.parts, dma, st);
+  hipError_t e = p.rows == 256   ? launch_tile<256, 256, 2, 4, 2, PK, QK>(a, p.parts, dma, st)
+                 : p.rows == 128 ? launch_tile<128, 128, 2, 2, 2, PK, QK>(a, p.parts, dma, st)
+                 : p.cols == 128 ? launch_tile<64, 128, 2, 2, 3, PK, QK>(a, p.parts, dma, st)
+                                 : launch_tile<64, 64, 2, 2, 2, PK, QK>(a, p.parts, dma, st);
   if (e != hipSuccess || p.parts == 1) return e;
   const long long runs = a.M * ((a.N + 7) / 8);
   hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)rec_cdiv(runs, 256)), dim3(256), 0, st, a.part, p.parts, a.M, a.N,
