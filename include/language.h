@@ -32,7 +32,7 @@ extern "C" {
 #define LANGUAGE_MAX_VOCAB (1 << 24)      /* V */
 #define LANGUAGE_MAX_CHANNELS (1 << 20)   /* D of the embedding, H * W of the norm */
 #define LANGUAGE_MAX_ELEMENTS (1LL << 37) /* n * D, V * D, B * L * H * W of one call */
-#define LANGUAGE_MAX_NORM_WIDTH 2048      /* W of the norm */
+#define LANGUAGE_MAX_NORM_WIDTH RETENTION_MAX_DV /* W of the norm */
 #define LANGUAGE_MAX_FEATURES (1 << 22)   /* N and K of linear */
 #define LANGUAGE_MAX_BEAMS 64             /* W and K of beam_select, W of beam_reorder */
 #define LANGUAGE_MAX_BEAM_ROWS (1 << 23)  /* B * W of beam_select */
@@ -137,6 +137,7 @@ ret_status_t linear_bwd(const void *x, const void *w, const void *d_o, const voi
  *   scores : [B, W] fp32      ended : bytes [B, W] or NULL: a beam with a byte other than
  *            zero offers token eos at its own score and nothing else
  *   tokens, parents : int32 [B, K]     out_scores : fp32 [B, K]
+ *   workspace : beam_select_workspace_bytes() bytes (NULL where that is 0)
  * Scores are compared in 64 bits.  A continuation without a finite score (a logit of -inf,
  * the other tokens of an ended beam; all of a beam whose score is not finite, or whose
  * logits hold a NaN or +inf or nothing above -inf) counts as -inf: it is taken after all

@@ -25,6 +25,8 @@ namespace {
 constexpr int NT = 256;
 constexpr int MAXK = LANGUAGE_MAX_BEAMS;
 typedef unsigned long long u64;
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 struct Cand {
   float value;
@@ -192,42 +194,47 @@ struct Key {
   }
 };
 
-constexpr int MAX_LISTS = LANGUAGE_MAX_BEAM_LISTS;
-constexpr int CAP2 = MAXK * MAXK;
+// What a workgroup of NTH threads needs to choose a request's K (KM at most) of its lists' candidates.
+template <int NTH, int LISTS, int KM>
+struct Join {
+  double lse[MAXK];
+  int kind[MAXK];  // 0: an ordinary beam, 1: ended, 2: nothing to offer
+  u64 head_score[LISTS];
+  uint32_t head_index[LISTS];
+  u64 list_score[KM * KM];
+  uint32_t list_index[KM * KM];
+  Key bound;
+  int count;
+};
 
-__global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
-  __shared__ double lse[MAXK];
-  __shared__ int kind[MAXK];  // 0: an ordinary beam, 1: ended, 2: nothing to offer
-  __shared__ u64 head_score[MAX_LISTS];
-  __shared__ uint32_t head_index[MAX_LISTS];
-  __shared__ u64 list_score[CAP2];
-  __shared__ uint32_t list_index[CAP2];
-  __shared__ Key bound;
-  __shared__ int count;
-  const int tid = threadIdx.x;
-  const long long b = blockIdx.x;
-  const int lists = a.W * a.slices;
+// Request b, from its lists' sums ([lists]) and candidates ([lists][K]), in memory or in LDS.
+template <int NTH, int LISTS, int KM>
+__device__ __forceinline__ void join(const SelectArgs &a, long long b, const float2 *sums, const Cand *cands,
+                                     Join<NTH, LISTS, KM> &lds) {
+  constexpr int CAP2 = KM * KM;
+  const int tid = threadIdx.x, lists = a.W * a.slices;
+  if (tid == 0) lds.bound = {0, 0}, lds.count = 0;
   // few candidates are all on their way from the start
   constexpr int EACH = 4;
-  const bool ahead = lists * a.K <= EACH * NT;
+  const bool ahead = lists * a.K <= EACH * NTH;
   Cand own[EACH];
   if (ahead)
 #pragma unroll
     for (int u = 0; u < EACH; ++u)
-      if (u * NT + tid < lists * a.K) own[u] = a.cands[b * lists * a.K + u * NT + tid];
+      if (u * NTH + tid < lists * a.K) own[u] = cands[u * NTH + tid];
   // a beam's log-sum by a wave, its slices by the lanes
-  for (int w = tid >> 6; w < a.W; w += NT / 64) {
+  for (int w = tid >> 6; w < a.W; w += NTH / 64) {
     const long long row = b * a.W + w;
     const float own = a.scores[row];
     const bool end = a.ended && a.ended[row];
     float m = -INFINITY;
     double s = 0.0;
     if (!end && isfinite(own)) {
-      for (int i = tid & 63; i < a.slices; i += 64) m = fmaxf(m, a.sums[row * a.slices + i].x);
+      for (int i = tid & 63; i < a.slices; i += 64) m = fmaxf(m, sums[w * a.slices + i].x);
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
       for (int i = tid & 63; i < a.slices; i += 64) {
-        const float2 v = a.sums[row * a.slices + i];
+        const float2 v = sums[w * a.slices + i];
         // a slice of nothing but -inf adds its sum, 0 or NaN
         s += v.x == -INFINITY ? (double)v.y : (double)v.y * exp((double)v.x - (double)m);
       }
@@ -236,11 +243,10 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
     }
     if ((tid & 63) == 0) {
       const double l = (double)m + log(s);
-      lse[w] = l;
-      kind[w] = !isfinite(own) ? 2 : end ? 1 : isfinite(l) ? 0 : 2;
+      lds.lse[w] = l;
+      lds.kind[w] = !isfinite(own) ? 2 : end ? 1 : isfinite(l) ? 0 : 2;
     }
   }
-  if (tid == 0) bound = {0, 0}, count = 0;
   __syncthreads();
   // Candidate j of a list as a key; {0, 0}: none
   auto key_of_cand = [&](int list, int j, const Cand &c) -> Key {
@@ -248,71 +254,71 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
     const long long row = b * a.W + w;
     int v;
     double score;
-    if (kind[w] == 0) {
+    if (lds.kind[w] == 0) {
       if (c.index < 0) return {0, 0};
       v = c.index;
-      score = (double)a.scores[row] + ((double)c.value - lse[w]);
+      score = (double)a.scores[row] + ((double)c.value - lds.lse[w]);
     } else {
       // the tokens in their order, after the end token where the beam has ended: in the first list
       if (slice) return {0, 0};
-      const bool end = kind[w] == 1 && a.eos >= 0 && a.eos < a.V;
+      const bool end = lds.kind[w] == 1 && a.eos >= 0 && a.eos < a.V;
       v = !end ? j : j == 0 ? a.eos : j - 1 < a.eos ? j - 1 : j;
       if (v >= a.V) return {0, 0};
       score = end && j == 0 ? (double)a.scores[row] : -INFINITY;
     }
     return {ordered(score + 0.0), ~(uint32_t)(w * a.V + v)};
   };
-  auto key_at = [&](int list, int j) { return key_of_cand(list, j, a.cands[(b * lists + list) * a.K + j]); };
+  auto key_at = [&](int list, int j) { return key_of_cand(list, j, cands[list * a.K + j]); };
   Key mine[EACH];
   if (ahead) {
 #pragma unroll
     for (int u = 0; u < EACH; ++u) {
-      const int e = u * NT + tid, l = e / a.K, j = e - l * a.K;
+      const int e = u * NTH + tid, l = e / a.K, j = e - l * a.K;
       mine[u] = {0, 0};
       if (e < lists * a.K) {
         mine[u] = key_of_cand(l, j, own[u]);
-        if (j == 0) head_score[l] = mine[u].score, head_index[l] = mine[u].index;
+        if (j == 0) lds.head_score[l] = mine[u].score, lds.head_index[l] = mine[u].index;
       }
     }
   } else {
-    for (int l = tid; l < lists; l += NT) {
+    for (int l = tid; l < lists; l += NTH) {
       const Key k = key_at(l, 0);
-      head_score[l] = k.score;
-      head_index[l] = k.index;
+      lds.head_score[l] = k.score;
+      lds.head_index[l] = k.index;
     }
   }
   __syncthreads();
-  for (int l = tid; l < lists; l += NT) {
-    const Key k = {head_score[l], head_index[l]};
+  for (int l = tid; l < lists; l += NTH) {
+    const Key k = {lds.head_score[l], lds.head_index[l]};
     if (!k.score) continue;
     int r = 0;
-    for (int j = 0; j < lists; ++j) r += Key{head_score[j], head_index[j]}.above(k);
-    if (r == a.K - 1) bound = k;
+    for (int j = 0; j < lists; ++j) r += Key{lds.head_score[j], lds.head_index[j]}.above(k);
+    if (r == a.K - 1) lds.bound = k;
   }
   __syncthreads();
   // what reaches the bound: prefixes of at most K lists
   auto put = [&](const Key &k) {
-    const int to = atomicAdd(&count, 1);
-    if (to < CAP2) list_score[to] = k.score, list_index[to] = k.index;
+    const int to = atomicAdd(&lds.count, 1);
+    if (to < CAP2) lds.list_score[to] = k.score, lds.list_index[to] = k.index;
   };
   if (ahead) {
 #pragma unroll
     for (int u = 0; u < EACH; ++u)
-      if (mine[u].score && !bound.above(mine[u])) put(mine[u]);
+      if (mine[u].score && !lds.bound.above(mine[u])) put(mine[u]);
   } else {
-    for (int l = tid; l < lists; l += NT)
+    for (int l = tid; l < lists; l += NTH)
       for (int j = 0; j < a.K; ++j) {
         const Key k = key_at(l, j);
-        if (!k.score || bound.above(k)) break;
+        if (!k.score || lds.bound.above(k)) break;
         put(k);
       }
   }
   __syncthreads();
-  const int n = min(count, CAP2);
-  for (int e = tid; e < n; e += NT) {
-    const Key k = {list_score[e], list_index[e]};
+  const int n = min(lds.count, CAP2);
+  for (int e = tid; e < n; e += NTH) {
+    const Key k = {lds.list_score[e], lds.list_index[e]};
     int r = 0;
-    for (int j = 0; j < n; ++j) r += Key{list_score[j], list_index[j]}.above(k);
+    for (int j = 0; j < n; ++j) r += Key{lds.list_score[j], lds.list_index[j]}.above(k);
     if (r < a.K) {
       const uint32_t flat = ~k.index;
       const u64 o = k.score;
@@ -324,6 +330,100 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
   }
 }
 
+__global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
+  __shared__ Join<NT, LANGUAGE_MAX_BEAM_LISTS, MAXK> lds;
+  const long long b = blockIdx.x, lists = (long long)a.W * a.slices;
+  join(a, b, a.sums + b * lists, a.cands + b * lists * a.K, lds);
+}
+
+// Both steps in one launch, for requests of few slices and candidates: a wave takes a slice of 2048 elements of a
+// beam at a time, the workgroup's NTH / 64 waves take turns.
+constexpr int SLICE = 2048, FEW_LISTS = 32, FEW_K = 32;
+template <typename T, int NTH>
+__global__ __launch_bounds__(NTH) void request_kernel(SelectArgs a) {
+  constexpr int CAP = 64;  // elements gathered by a wave
+  __shared__ Join<NTH, FEW_LISTS, FEW_K> lds;
+  __shared__ float2 sums[FEW_LISTS];
+  __shared__ Cand cands[FEW_LISTS * FEW_K];
+  __shared__ u64 list[NTH / 64][CAP];
+  __shared__ int counts[NTH / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lists = a.W * a.slices;
+  const long long b = blockIdx.x;
+  for (int l = wave; l < lists; l += NTH / 64) {
+    const int w = l / a.slices, first = (l - w * a.slices) * SLICE;
+    const long long row = b * a.W + w;
+    if ((a.ended && a.ended[row]) || !isfinite(a.scores[row])) continue;
+    const T *src = (const T *)a.logits + row * a.ld;
+    float x[4][8];  // -inf behind the row's end
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int at = first + (c * 64 + lane) * 8, left = a.V - at;
+      load8(src + at, left, x[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[c][i] = i < left ? x[c][i] : -INFINITY;
+        top = fmaxf(top, x[c][i]);
+      }
+    }
+    const float least = value_of(kth_of_wave(ordered(top + 0.0f), a.K));
+    float m = top;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    if (lane == 0) counts[wave] = 0;
+    __builtin_amdgcn_wave_barrier();
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = first + (c * 64 + lane) * 8 + i;
+        if (x[c][i] >= least && at < a.V) {
+          const int to = atomicAdd(&counts[wave], 1);
+          if (to < CAP) list[wave][to] = key_of(x[c][i], at);
+        }
+        s += m == -INFINITY ? (x[c][i] == x[c][i] ? 0.0f : x[c][i]) : __builtin_amdgcn_exp2f((x[c][i] - m) * kLog2e);
+      }
+    s = wave_sum(s);
+    if (lane == 0) sums[l] = make_float2(m, s);
+    __builtin_amdgcn_wave_barrier();
+    const int n = *(volatile int *)&counts[wave];
+    Cand *out = cands + l * a.K;
+    if (n <= CAP) {
+      if (lane < n) {
+        const u64 k = list[wave][lane];
+        int r = 0;
+        for (int j = 0; j < n; ++j) r += list[wave][j] > k;
+        if (r < a.K) out[r] = {value_of((uint32_t)(k >> 32)), (int)~(uint32_t)k};
+      }
+      for (int e = n + lane; e < a.K; e += 64) out[e] = {0.0f, -1};
+    } else {  // rows of equal values: one after the other
+      u64 last = ~0ull;
+      for (int r = 0; r < a.K; ++r) {
+        u64 best = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int at = first + (c * 64 + lane) * 8 + i;
+            const u64 k = at < a.V ? key_of(x[c][i], at) : 0;
+            best = k < last && k > best ? k : best;
+          }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+          const u64 other = __shfl_xor(best, off, 64);
+          best = other > best ? other : best;
+        }
+        if (lane == 0) out[r] = best ? Cand{value_of((uint32_t)(best >> 32)), (int)~(uint32_t)best} : Cand{0.0f, -1};
+        last = best;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  join(a, b, sums, cands, lds);
+}
+
 // ----------------------------------------------------------------------------- reorder
 // MT tensors at most: of few all arguments are read at once, in one trip to the memory they lie in (two tensors
 // of 131 KB a beam: 8.8 us with arguments for 64, read one after the other).
@@ -331,7 +431,7 @@ template <int MT>
 struct ReorderArgs {
   void *states[MT];
   long long bytes[MT];
-  unsigned first[MT + 1];  // workgroups of a request in front of tensor i
+  unsigned first[MT + 1];  // workgroups of a request in front of tensor i; behind the last their number, then ~0
   const int *parents;
   int count, W;
 };
@@ -340,7 +440,7 @@ struct ReorderArgs {
 // writes, so the exchange needs no second buffer.  WM beams at most, T at a time.
 template <typename T, int WM>
 __device__ __forceinline__ void reorder_at(char *base, long long bytes, long long off, const int (&parent)[WM]) {
-  T v[WM];
+  T v[WM] = {};
 #pragma unroll
   for (int w = 0; w < WM; ++w)
     if (parent[w] != w) v[w] = *(const T *)(base + parent[w] * bytes + off);
@@ -351,7 +451,7 @@ __device__ __forceinline__ void reorder_at(char *base, long long bytes, long lon
 
 template <int WM, int MT>
 __global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs<MT> a) {
-  using Wide = std::conditional_t<(WM <= 16), uint4, std::conditional_t<(WM <= 32), uint2, uint32_t>>;
+  using Wide = std::conditional_t<(WM <= 16), u32x4, std::conditional_t<(WM <= 32), u32x2, uint32_t>>;
   const long long b = blockIdx.y;
   long long bytes = a.bytes[0];
   char *tensor = (char *)a.states[0];
@@ -359,12 +459,15 @@ __global__ __launch_bounds__(NT) void reorder_kernel(ReorderArgs<MT> a) {
   if constexpr (MT <= 4) {
 #pragma unroll
     for (int i = 1; i < MT; ++i)
-      if (i < a.count && blockIdx.x >= a.first[i])
+      if (blockIdx.x >= a.first[i])
         bytes = a.bytes[i], tensor = (char *)a.states[i], from = a.first[i], to = a.first[i + 1];
   } else {
+    // indexed where they lie: the argument itself would be copied to be indexed
+    const auto *lie = (const __attribute__((address_space(4))) ReorderArgs<MT> *)__builtin_amdgcn_kernarg_segment_ptr();
     int i = 0;
-    while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) ++i;
-    bytes = a.bytes[i], tensor = (char *)a.states[i], from = a.first[i], to = a.first[i + 1];
+#pragma unroll
+    for (int j = 1; j < MT; ++j) i += blockIdx.x >= a.first[j];
+    bytes = lie->bytes[i], tensor = (char *)lie->states[i], from = lie->first[i], to = lie->first[i + 1];
   }
   char *base = tensor + b * a.W * bytes;
   int parent[WM];
@@ -402,12 +505,17 @@ hipError_t launch_reorder(const ReorderArgs<MT> &a, dim3 grid, hipStream_t st) {
 // Elements of a row a thread keeps: 32 where that gives enough workgroups, else 8.
 int per_thread(long long rows, int V) { return rows * rec_cdiv(V, NT * 32) >= 256 ? 32 : 8; }
 
+// Whether one launch does: few slices and candidates a request.
+bool one_launch(long long W, int V, int K) { return W * rec_cdiv(V, SLICE) <= FEW_LISTS && K <= FEW_K; }
+
 struct SelectWs {
   int slices;
   size_t cands, bytes;
 };
-SelectWs select_ws(long long rows, int V, int K) {
-  SelectWs w;
+SelectWs select_ws(long long B, int W, int V, int K) {
+  SelectWs w = {};
+  if (one_launch(W, V, K)) return w;
+  const long long rows = B * W;
   w.slices = (int)rec_cdiv(V, NT * per_thread(rows, V));
   w.cands = rec_align((size_t)rows * w.slices * sizeof(float2));
   w.bytes = w.cands + rec_align((size_t)rows * w.slices * K * sizeof(Cand));
@@ -427,7 +535,7 @@ ret_status_t check_sizes(int B, int W, int V, int K) {
 
 extern "C" size_t beam_select_workspace_bytes(int B, int W, int V, int K) {
   if (check_sizes(B, W, V, K) != RET_OK || B == 0) return 0;
-  return select_ws((long long)B * W, V, K).bytes;
+  return select_ws(B, W, V, K).bytes;
 }
 
 extern "C" ret_status_t beam_select(const void *logits, const float *scores, const unsigned char *ended, int *tokens,
@@ -448,23 +556,40 @@ extern "C" ret_status_t beam_select(const void *logits, const float *scores, con
   if (!rec_aligned(logits, e) || !rec_aligned(scores, 4) || !rec_aligned(tokens, 4) || !rec_aligned(parents, 4) ||
       !rec_aligned(out_scores, 4))
     return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
-  const SelectWs w = select_ws(rows, V, K);
-  if (!workspace || workspace_bytes < w.bytes)
+  const SelectWs w = select_ws(B, W, V, K);
+  if (w.bytes && (!workspace || workspace_bytes < w.bytes))
     return rec_fail(RET_ERR_WORKSPACE, "workspace of %zu bytes needed", w.bytes);
   const RecSpan ins[] = {rec_rows("logits", logits, rows, logits_ld, V, e), {"scores", scores, (size_t)rows * 4},
                          {"ended", ended, (size_t)rows}};
   const RecSpan outs[] = {{"tokens", tokens, picked}, {"parents", parents, picked}, {"out_scores", out_scores, picked},
                           {"workspace", workspace, w.bytes}};
   if ((s = rec_check_overlap(ins, outs)) != RET_OK) return s;
-  if (!rec_aligned(workspace, 16)) return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (w.bytes && !rec_aligned(workspace, 16))
+    return rec_fail(RET_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   SelectArgs a = {};
   a.logits = logits, a.scores = scores, a.ended = ended, a.tokens = tokens, a.parents = parents;
   a.out_scores = out_scores, a.ld = logits_ld;
   a.B = B, a.W = W, a.V = V, a.K = K, a.eos = eos, a.slices = w.slices;
+  hipStream_t st = (hipStream_t)hip_stream;
+  if (one_launch(W, V, K)) {
+    a.slices = (int)rec_cdiv(V, SLICE);
+    const bool small = W * a.slices <= 4;
+    if (dtype == RET_BF16) {
+      if (small)
+        hipLaunchKernelGGL((request_kernel<uint16_t, 256>), dim3((unsigned)B), dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((request_kernel<uint16_t, 1024>), dim3((unsigned)B), dim3(1024), 0, st, a);
+    } else {
+      if (small)
+        hipLaunchKernelGGL((request_kernel<float, 256>), dim3((unsigned)B), dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((request_kernel<float, 1024>), dim3((unsigned)B), dim3(1024), 0, st, a);
+    }
+    return rec_status(hipGetLastError());
+  }
   a.sums = (float2 *)workspace;
   a.cands = (Cand *)((char *)workspace + w.cands);
   const dim3 grid((unsigned)w.slices, (unsigned)std::min<long long>(rows, 65535), (unsigned)rec_cdiv(rows, 65535));
-  hipStream_t st = (hipStream_t)hip_stream;
   const bool many = per_thread(rows, V) == 32;
   if (dtype == RET_BF16) {
     if (many)
@@ -512,12 +637,13 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
     a.first[n + 1] = blocks;
   }
   if (a.count == 0) return rec_status(hipSuccess);
+  for (int i = a.count + 1; i <= LANGUAGE_MAX_REORDERED; ++i) a.first[i] = ~0u;
   if (!rec_grid_ok((double)blocks * B, NT)) return rec_fail(RET_ERR_UNSUPPORTED, "too many workgroups for one launch");
   const dim3 grid(blocks, (unsigned)B);
   hipStream_t st = (hipStream_t)hip_stream;
   if (a.count > 4) return rec_status(launch_reorder(a, grid, st));
   ReorderArgs<4> few = {};
-  for (int i = 0; i < a.count; ++i) few.states[i] = a.states[i], few.bytes[i] = a.bytes[i], few.first[i + 1] = a.first[i + 1];
+  for (int i = 0; i < 4; ++i) few.states[i] = a.states[i], few.bytes[i] = a.bytes[i], few.first[i + 1] = a.first[i + 1];
   few.parents = parents, few.count = a.count, few.W = W;
   return rec_status(launch_reorder(few, grid, st));
 }

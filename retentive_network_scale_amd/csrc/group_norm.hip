@@ -285,8 +285,7 @@ hipError_t with_width(int W, F f) {
   if (W <= 128) NORM_AT(16, 1);
   if (W <= 256) NORM_AT(32, 1);
   if (W <= 512) NORM_AT(64, 1);
-  if (W <= 1024) NORM_AT(64, 2);
-  NORM_AT(64, 4);
+  NORM_AT(64, 2);
 #undef NORM_AT
 }
 

@@ -11,60 +11,6 @@ namespace ret {
 struct __attribute__((packed, aligned(2))) Words4 {
   uint32_t w[4];
 };
-__device__ __forceinline__ void load8(const uint16_t *p, float (&r)[8]) {
-  const Words4 v = *(const Words4 *)p;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[2 * i] = __uint_as_float(v.w[i] << 16);
-    r[2 * i + 1] = __uint_as_float(v.w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float *p, float (&r)[8]) {
-  const Words4 a = *(const Words4 *)p, b = *(const Words4 *)(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = __uint_as_float(a.w[i]);
-    r[4 + i] = __uint_as_float(b.w[i]);
-  }
-}
-__device__ __forceinline__ void store8(uint16_t *p, const float (&r)[8]) {
-  Words4 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v.w[i] = pack_bf2(r[2 * i], r[2 * i + 1]);
-  *(Words4 *)p = v;
-}
-__device__ __forceinline__ void store8(float *p, const float (&r)[8]) {
-  Words4 a, b;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a.w[i] = __float_as_uint(r[i]);
-    b.w[i] = __float_as_uint(r[4 + i]);
-  }
-  *(Words4 *)p = a;
-  *(Words4 *)(p + 4) = b;
-}
-
-// The first n of eight elements (n <= 0: none, read as zero).
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, float (&r)[8]) {
-  if (n >= 8) {
-    load8(p, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = i < n ? load_elem(p, i, sizeof(T) == 2) : 0.0f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *p, int n, const float (&r)[8]) {
-  if (n >= 8) {
-    store8(p, r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) store_elem(p, i, r[i], sizeof(T) == 2);
-  }
-}
-
 // Eight elements as they come from memory, for loads that are to be under way while others are used.
 template <typename T>
 struct Raw8 {
@@ -96,6 +42,45 @@ struct Raw8 {
     }
   }
 };
+
+// Eight elements, the first n of them (n <= 0: none; the others are zero).
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int n, float (&r)[8]) {
+  Raw8<T> v;
+  v.load(p, n);
+  v.get(r);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&r)[8]) {
+  load8(p, 8, r);
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float (&r)[8]) {
+  Words4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.w[i] = pack_bf2(r[2 * i], r[2 * i + 1]);
+  *(Words4 *)p = v;
+}
+__device__ __forceinline__ void store8(float *p, const float (&r)[8]) {
+  Words4 a, b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a.w[i] = __float_as_uint(r[i]);
+    b.w[i] = __float_as_uint(r[4 + i]);
+  }
+  *(Words4 *)p = a;
+  *(Words4 *)(p + 4) = b;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int n, const float (&r)[8]) {
+  if (n >= 8) {
+    store8(p, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) store_elem(p, i, r[i], sizeof(T) == 2);
+  }
+}
 
 // Calls f with a null pointer of the element type that each dtype stands for.
 template <typename F>

@@ -195,7 +195,8 @@ def beam_select(logits, scores, K, ended=None, eos=0, workspace=None, stream=Non
     if ended is not None and (not isinstance(ended, torch.Tensor) or ended.dtype not in (torch.bool, torch.uint8)):
         raise TypeError("ended must be a bool tensor")
     out = BeamSelection(call.empty((b, K), _I32), call.empty((b, K), _I32), call.empty((b, K), _F32))
-    ws, wp, wb = call.workspace(workspace, beam_select_workspace_bytes(b, w, v, K))
+    need = beam_select_workspace_bytes(b, w, v, K)
+    ws, wp, wb = call.workspace(workspace, need) if need else (None, None, 0)
     call.run(lib().beam_select, lp, _dense(scores, "scores", (b, w), _F32, ix), _dense(ended, "ended", (b, w), None, ix),
              *(t.data_ptr() for t in out), b, w, v, K, ld, int(eos), _dtc(logits.dtype), wp, wb)
     return out

@@ -79,7 +79,8 @@ def _ids(kind, n, V, seed):
 @pytest.mark.parametrize("kind,n,V,D", [
     ("words", 1, 1, 1), ("words", 1, 600, 3), ("words", 63, 7, 8), ("words", 64, 300, 40), ("words", 65, 3, 100),
     ("one", 33, 5, 16), ("one", 1000, 2, 24), ("holes", 500, 40, 33), ("outside", 70, 20, 16), ("words", 1025, 4, 2050),
-    ("words", 3000, 1000, 20), ("holes", 4100, 513, 9), ("one", 2049, 700, 65)])
+    ("words", 3000, 1000, 20), ("holes", 4100, 513, 9), ("one", 2049, 700, 65), ("words", 2500, 9, 700), ("one", 1500, 3, 1030),
+    ("words", 1200, 2000, 4100)])
 @pytest.mark.parametrize("dt,od", [(BF, F32), (F32, F32), (BF, BF)])
 def test_embedding_gradient(kind, n, V, D, dt, od):
     ids, d_o = _ids(kind, n, V, 3), _r(4, n, D, dt=dt)
@@ -107,7 +108,7 @@ def test_embedding_without_tokens():
 
 
 # -------------------------------------------------------------------------------------- norm
-WIDTHS = [1, 2, 7, 8, 63, 64, 65, 100, 128, 129, 256, 257, 512, 513, 1000, 1024, 1025, 2048]
+WIDTHS = [1, 2, 7, 8, 63, 64, 65, 100, 128, 129, 256, 257, 512, 513, 1000, 1023, 1024]
 
 
 def _norm_case(B, H, L, W, dt, seed, gate=True, weight=True, bias=True):
@@ -319,6 +320,15 @@ def test_linear_large_tiles():
         _check_linear_bwd(v, d, pre, "gelu")
 
 
+@pytest.mark.parametrize("M,N,K", [(777, 1302, 200), (520, 700, 1000), (1100, 2100, 72), (2304, 2050, 64), (300, 4000, 71),
+                                   (2200, 2050, 77), (4096, 4100, 9), (1000, 33, 3001)])
+def test_linear_between_the_tiles(M, N, K):
+    """Sizes at which one kind of tile gives way to the next, aligned and not."""
+    v = _linear_case(M, N, K, 135, True, True)
+    d, pre = _check_linear(v, "silu")
+    _check_linear_bwd(v, d, pre, "silu")
+
+
 def test_linear_in_place_and_leading_axes():
     v = _linear_case(6, 24, 16, 140, True, True)
     d = {k: _dev(t) for k, t in v.items()}
@@ -397,7 +407,7 @@ def _check_select(z, cum, K, ended=None, eos=0):
     return got
 
 
-SELECT = [(1, 1, 1, 1), (1, 1, 5, 5), (3, 2, 3, 6), (2, 4, 100, 8), (1, 1, 2048, 64), (2, 3, 2049, 7), (1, 2, 8193, 16),
+SELECT = [(2, 16, 4096, 32), (3, 17, 2049, 9), (2, 1, 65536, 32), (2, 2, 40000, 33), (1, 1, 1, 1), (1, 1, 5, 5), (3, 2, 3, 6), (2, 4, 100, 8), (1, 1, 2048, 64), (2, 3, 2049, 7), (1, 2, 8193, 16),
           (4, 5, 1000, 10), (5, 64, 40, 64), (1, 1, 20000, 4), (70, 4, 300, 4), (300, 2, 64, 3), (1, 3, 33, 64)]
 
 
@@ -410,7 +420,7 @@ def test_select_shapes(B, W, V, K, dt):
 
 def test_select_all_tied():
     """Equal logits, equal beams: the lowest indices, whatever the slices are."""
-    for V, K in ((10, 7), (5000, 64), (30000, 20)):
+    for V, K in ((10, 7), (5000, 64), (30000, 20), (2000, 32), (30000, 64)):
         z, cum = torch.zeros(2, 3, V), torch.full((2, 3), -1.5)
         got = rn.beam_select(z.to(DEV), cum.to(DEV), K)
         assert torch.equal(got.tokens.cpu(), (torch.arange(K) % V).to(I32).expand(2, K))

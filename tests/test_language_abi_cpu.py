@@ -85,7 +85,7 @@ def _norm_bwd(**kw):
     (dict(outd=9), INVALID), (dict(x=None), INVALID), (dict(sb=10), INVALID), (dict(sh=63), INVALID), (dict(sl=63), INVALID),
     (dict(sl=-64), INVALID), (dict(gld=191), INVALID), (dict(x=P(1, 1)), INVALID), (dict(gate=P(2, 1)), INVALID),
     (dict(w=P(3, 2)), INVALID), (dict(b=P(4, 1)), INVALID), (dict(lengths=P(11, 2)), INVALID),
-    (dict(W=2049, sl=2049, sh=20490, sb=61470, gld=3 * 2049), UNSUPPORTED), (dict(sl=1 << 32), UNSUPPORTED),
+    (dict(W=1025, sl=1025, sh=10250, sb=30750, gld=3 * 1025), UNSUPPORTED), (dict(sl=1 << 32), UNSUPPORTED),
     (dict(sb=1 << 40), UNSUPPORTED), (dict(gld=1 << 32), UNSUPPORTED), (dict(B=1 << 20, L=1 << 10), UNSUPPORTED),
     (dict(H=1 << 16, W=8, gld=1 << 19, sh=80, sb=80 << 16, sl=8), UNSUPPORTED),
     (dict(B=1 << 18, L=1 << 8, H=64, W=64, gld=64 * 64), UNSUPPORTED),
@@ -174,9 +174,10 @@ def _select(**kw):
     (dict(tok=P(4, 1)), INVALID), (dict(K=65), UNSUPPORTED), (dict(W=65), UNSUPPORTED),
     (dict(W=64, V=1 << 24, ld=1 << 24), UNSUPPORTED), (dict(W=64, V=65537, ld=65537), UNSUPPORTED),
     (dict(V=(1 << 24) + 1, ld=1 << 25), UNSUPPORTED),
-    (dict(B=1 << 23), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(wb=16), WORKSPACE), (dict(ws=P(7, 8)), INVALID),
-    (dict(tok=P(1)), INVALID), (dict(out=P(2)), INVALID), (dict(par=P(4)), INVALID), (dict(ws=P(6)), INVALID),
-    (dict(ws=P(1)), INVALID), (dict(tok=P(3)), INVALID),
+    (dict(B=1 << 23), UNSUPPORTED), (dict(V=20000, ld=20000, ws=None), WORKSPACE), (dict(V=20000, ld=20000, wb=16), WORKSPACE),
+    (dict(V=20000, ld=20000, ws=P(7, 8)), INVALID), (dict(K=33, ws=None), WORKSPACE),
+    (dict(tok=P(1)), INVALID), (dict(out=P(2)), INVALID), (dict(par=P(4)), INVALID), (dict(V=20000, ld=20000, ws=P(6)), INVALID),
+    (dict(V=20000, ld=20000, ws=P(1)), INVALID), (dict(tok=P(3)), INVALID),
 ])
 def test_select_refuses(kw, code):
     assert _select(**kw) == code
@@ -186,7 +187,7 @@ def test_select_refuses(kw, code):
 def test_select_without_requests():
     assert _select(B=0, z=None, ws=None, wb=0) == 0
     q = rn.lib().beam_select_workspace_bytes
-    assert q(0, 4, 100, 8) == 0 == q(2, 65, 100, 8) and q(2, 4, 100, 8) > 0
+    assert q(0, 4, 100, 8) == 0 == q(2, 65, 100, 8) and q(2, 4, 20000, 8) > 0
 
 
 def _reorder(states=((21, 4096), (22, 4096)), parents=P(30), B=2, W=4, count=None, null=False):
