@@ -6,7 +6,8 @@
 //   dw       P = dz, Q = x         both with k across their rows
 // Tiles of 64 k reach LDS by DMA, two in turn, so that one is filled while the other is multiplied, and the
 // operands of the next matrix step are read from LDS while the present one's are multiplied.
-// Operands whose rows are not 16-byte aligned take the same way through registers.
+// Operands whose rows are not 16-byte aligned take the same way through registers (M 64, N 4096, K 2048 11.7 us,
+// K 2047 19.0; M 300, N 1001, K 999 12.0 against 7.9 for 1000 and 1000).
 // Where there are too few tiles for the chip, k is cut, the parts' sums go to the workspace in
 // fp32, and a second launch joins them in order and finishes.
 //
@@ -35,14 +36,19 @@ typedef __attribute__((address_space(3))) void lds_void;
 //   else: [64][R], chunk c of row k at c ^ turn(k), for reads that transpose.  In rows of 256 columns the
 //     rows k + 8 .. are turned further than k ..: 32 lanes take them together (dx 234 -> 215 us; 128 columns
 //     were slower with it, 296 -> 321 us, and 64 have no chunks for it).
-template <int R, bool KROWS, int NT, bool DMA>
+//
+// DMA: 16-byte chunks straight to LDS.  WIDE: the same chunks at any address through registers, DEPTH tiles under
+// way (M 300, N 1001, K 999 with a branch around each row's end and one tile: 21.8 us, without and with four: 12.0).
+// SINGLE: element by element, for rows of fewer than 8.
+enum Way { DMA, WIDE, SINGLE };
+template <int R, bool KROWS, int NT, Way WAY, int DEPTH>
 struct Operand {
   static constexpr int SIZE = R * BK, NJ = SIZE * 2 / 1024 / (NT / 64);  // elements; wave loads of a wave
   static_assert(NJ >= 1 && SIZE * 2 % (1024 * (NT / 64)) == 0, "whole wave loads");
   const uint16_t *base;  // of the tile's rows (KROWS) or columns
   long long ld;
   int width;  // rows of the operand from the tile on, R at most
-  u32x4 reg[DMA ? 1 : NJ];
+  u32x4 reg[DEPTH][NJ];
 
   __device__ __forceinline__ void start(const uint16_t *p, long long ld_, long long rows, long long r0) {
     base = KROWS ? p + r0 * ld_ : p + r0;
@@ -65,11 +71,11 @@ struct Operand {
       c = off % (R * 2) / 16 ^ turn(row);
     }
   }
-  // The tile at k0 on its way to `lds` (DMA) or to registers; k from `kend` on is zero.
-  __device__ __forceinline__ void fetch(uint16_t *lds, long long k0, long long kend) {
-    if constexpr (DMA) {
+  // The tile at k0 on its way to `lds` (DMA) or to reg[d]; k from `kend` on is zero.
+  __device__ __forceinline__ void fetch(uint16_t *lds, int d, long long k0, long long kend) {
+    const int left = kend - k0 < BK ? (int)(kend - k0) : BK;
+    if constexpr (WAY == DMA) {
       // rows are whole 16-byte chunks; what lies behind the range reads as zero
-      const int left = kend - k0 < BK ? (int)(kend - k0) : BK;
       const uint16_t *b = KROWS ? base + k0 : base + k0 * ld;
       const long long last = left <= 0 ? 0 : KROWS ? (long long)(width - 1) * ld + left : (long long)(left - 1) * ld + width;
       const __amdgpu_buffer_rsrc_t rs =
@@ -82,33 +88,53 @@ struct Operand {
         if (KROWS && c * 8 >= left) off = (int)0x80000000u;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(lds + (wave() * NJ + j) * 512), 16, off, 0, 0, 0);
       }
+    } else if constexpr (WAY == WIDE) {
+      // Every lane loads, with no branch, which would hold up the loads under way: rows behind the last are the
+      // last once more, and a row's last chunk ends with the row.
+      const char *b = (const char *)(KROWS ? base + k0 - 8 : base + k0 * ld - 8);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        int row, c;
+        place(j, row, c);
+        row = min(row, (KROWS ? width : left) - 1);
+        const uint32_t off = (uint32_t)row * (uint32_t)ld + min(c * 8, (KROWS ? left : width) - 8) + 8;
+        const Words4 w = *(const Words4 *)(b + (size_t)off * 2);
+        reg[d][j] = u32x4{w.w[0], w.w[1], w.w[2], w.w[3]};
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         int row, c;
         place(j, row, c);
-        const long long k = k0 + (KROWS ? c * 8 : row);
-        const int r = KROWS ? row : c * 8;
-        const uint16_t *src = KROWS ? base + r * ld + k : base + k * ld + r;
-        int n = 0;  // elements of the chunk that exist
-        if (KROWS ? r < width : k < kend) n = (int)(KROWS ? (kend - k < 8 ? kend - k : 8) : (width - r < 8 ? width - r : 8));
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (n >= 8) {
-          const Words4 w = *(const Words4 *)src;
-          v = u32x4{w.w[0], w.w[1], w.w[2], w.w[3]};
-        } else {
+        const uint16_t *src = KROWS ? base + row * ld + k0 + c * 8 : base + (k0 + row) * ld + c * 8;
+        const int n = row < (KROWS ? width : left) ? (KROWS ? left : width) - c * 8 : 0;
+        reg[d][j] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < n) v[i / 2] |= (uint32_t)src[i] << (i % 2 * 16);
-        }
-        reg[j] = v;
+        for (int i = 0; i < 8; ++i)
+          if (i < n) reg[d][j][i / 2] |= (uint32_t)src[i] << (i % 2 * 16);
       }
     }
   }
-  __device__ __forceinline__ void commit(uint16_t *lds) {
-    if constexpr (!DMA)
+  // The tile of `left` k in reg[d] to LDS.
+  __device__ __forceinline__ void commit(uint16_t *lds, int d, int left) {
+    if constexpr (WAY != DMA) {
+      const bool cut = WAY == WIDE && (left < BK || (!KROWS && width < R));
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) *(u32x4 *)(lds + (wave() * NJ + j) * 512 + (threadIdx.x & 63) * 8) = reg[j];
+      for (int j = 0; j < NJ; ++j) {
+        u32x4 v = reg[d][j];
+        if (cut) {
+          int row, c;
+          place(j, row, c);
+          const int s = 16 * (c * 8 - min(c * 8, (KROWS ? left : width) - 8));  // bits that the chunk was read early
+          uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+          lo = s == 0 ? lo : s < 64 ? lo >> s | hi << (64 - s) : s < 128 ? hi >> (s - 64) : 0;
+          hi = s < 64 ? hi >> s : 0;
+          if (!KROWS && row >= left) lo = hi = 0;
+          v = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        }
+        *(u32x4 *)(lds + (wave() * NJ + j) * 512 + (threadIdx.x & 63) * 8) = v;
+      }
+    }
   }
   // Matrix operand of half h: lane (l16, g) holds k = 32 h + 8 g .. + 7 of row r0 + l16.
   static __device__ __forceinline__ bf16x8 read(const uint16_t *lds, int r0, int h, int l16, int g) {
@@ -140,11 +166,13 @@ __device__ __forceinline__ void meet() {
 // BM x BN of out by WM x WN waves, with a ring of NB tiles in LDS.  A wave multiplies the operands of a half
 // tile while it reads those of the next half.  The barrier in the middle of a tile tells that all
 // have read it, so that tile i + NB takes its place, and that tile i + 1 has come.
-template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, bool DMA>
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY>
 __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
   constexpr int NT = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
-  using OpP = Operand<BM, PK, NT, DMA>;
-  using OpQ = Operand<BN, QK, NT, DMA>;
+  // WIDE's tiles under way: as many as there are registers for beside the sums
+  constexpr int DEPTH = WAY != WIDE ? 1 : BM * BN <= 4096 ? 4 : BM * BN <= 16384 ? 2 : 1;
+  using OpP = Operand<BM, PK, NT, WAY, DEPTH>;
+  using OpQ = Operand<BN, QK, NT, WAY, DEPTH>;
   constexpr int SIZE = OpP::SIZE + OpQ::SIZE, LOADS = OpP::NJ + OpQ::NJ;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[NB * SIZE];
   const int lane = threadIdx.x & 63, wave = OpP::wave(), l16 = lane & 15, g = lane >> 4;
@@ -174,9 +202,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   bf16x8 fp[2][FM], fq[2][FN];
-  auto fetch = [&](int i, int slot) {
-    P.fetch(lds + slot * SIZE, kb + (long long)i * BK, ke);
-    Q.fetch(lds + slot * SIZE + OpP::SIZE, kb + (long long)i * BK, ke);
+  auto fetch = [&](int i, int slot) {  // a place in LDS, or in registers
+    P.fetch(lds + slot * SIZE, slot, kb + (long long)i * BK, ke);
+    Q.fetch(lds + slot * SIZE + OpP::SIZE, slot, kb + (long long)i * BK, ke);
   };
   auto read = [&](int slot, int h) {
 #pragma unroll
@@ -207,7 +235,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
         __builtin_amdgcn_sched_group_barrier(0x008, REST / LOADS > 1 ? REST / LOADS : 1, 0);
       }
   };
-  if constexpr (DMA) {
+  if constexpr (WAY == DMA) {
     // tiles behind the last are fetched as zeros, so that all steps are alike
 #pragma unroll
     for (int i = 0; i < NB; ++i) fetch(i, i);
@@ -228,18 +256,26 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
       multiply(1);
       interleave(std::true_type{});
     }
-  } else {
-    if (tiles_k > 0) fetch(0, 0);
-    for (int i = 0; i < tiles_k; ++i) {
-      uint16_t *cur = lds + (i & 1) * SIZE;
-      P.commit(cur);
-      Q.commit(cur + OpP::SIZE);
-      __syncthreads();  // this tile is there, and all have left the other place
-      if (i + 1 < tiles_k) fetch(i + 1, 0);
+  } else if (tiles_k > 0) {
+    // steps behind the last tile have it once more, as zeros: all are alike, with no branch around a load
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        read(i & 1, h);
-        multiply(h);
+    for (int d = 0; d < DEPTH; ++d) fetch(min(d, tiles_k - 1), d);
+    for (int i0 = 0; i0 < tiles_k; i0 += DEPTH) {
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) {
+        const int i = i0 + d, slot = DEPTH > 1 ? d & 1 : i & 1;
+        const long long rest = ke - kb - (long long)i * BK;
+        const int left = rest < BK ? (rest > 0 ? (int)rest : 0) : BK;
+        P.commit(lds + slot * SIZE, d, left);
+        Q.commit(lds + slot * SIZE + OpP::SIZE, d, left);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // for LDS only: the next tiles stay under way
+        meet();                              // this tile is there, and all have left the other place
+        fetch(min(i + DEPTH, tiles_k - 1), d);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          read(slot, h);
+          multiply(h);
+        }
       }
     }
   }
@@ -305,14 +341,20 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, int par
   finish8(f, m * N + n, N - n, bias, res, z);
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK>
-hipError_t launch_tile(const MmArgs &a, int parts, bool dma, hipStream_t st) {
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY>
+hipError_t launch_tile(const MmArgs &a, int parts, hipStream_t st) {
   const dim3 grid((unsigned)(rec_cdiv(a.M, BM) * rec_cdiv(a.N, BN)), (unsigned)parts);
-  if (dma)
-    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, NB, PK, QK, true>), grid, dim3(WM * WN * 64), 0, st, a);
-  else
-    hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, 2, PK, QK, false>), grid, dim3(WM * WN * 64), 0, st, a);
+  hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, NB, PK, QK, WAY>), grid, dim3(WM * WN * 64), 0, st, a);
   return hipGetLastError();
+}
+
+template <bool PK, bool QK, Way WAY>
+hipError_t launch(const MmArgs &a, const MmPlan &p, hipStream_t st) {
+  constexpr int NB = WAY == DMA ? 3 : 2;
+  if (p.rows == 256) return launch_tile<256, 256, 2, 4, 2, PK, QK, WAY>(a, p.parts, st);
+  if (p.rows == 128) return launch_tile<128, 128, 2, 2, 2, PK, QK, WAY>(a, p.parts, st);
+  if (p.cols == 128) return launch_tile<64, 128, 2, 2, NB, PK, QK, WAY>(a, p.parts, st);
+  return launch_tile<64, 64, 2, 2, 2, PK, QK, WAY>(a, p.parts, st);
 }
 
 // Rows of `width` elements whose 16-byte chunks are whole and aligned, within a buffer's reach.
@@ -325,11 +367,12 @@ hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   const MmPlan p = mm_plan(a.M, a.N, a.K);
   a.kpart = p.kpart;
   a.part = p.parts > 1 ? (float *)ws : nullptr;
-  const bool dma = chunked(a.p, a.ldp, PK ? a.K : a.M) && chunked(a.q, a.ldq, QK ? a.K : a.N);
-  hipError_t e = p.rows == 256   ? launch_tile<256, 256, 2, 4, 2, PK, QK>(a, p.parts, dma, st)
-                 : p.rows == 128 ? launch_tile<128, 128, 2, 2, 2, PK, QK>(a, p.parts, dma, st)
-                 : p.cols == 128 ? launch_tile<64, 128, 2, 2, 3, PK, QK>(a, p.parts, dma, st)
-                                 : launch_tile<64, 64, 2, 2, 2, PK, QK>(a, p.parts, dma, st);
+  const long long wp = PK ? a.K : a.M, wq = QK ? a.K : a.N;
+  const Way way = chunked(a.p, a.ldp, wp) && chunked(a.q, a.ldq, wq) ? DMA : wp >= 8 && wq >= 8 ? WIDE : SINGLE;
+  // SINGLE in one size: 128 x 128 of the largest output still are a grid
+  const hipError_t e = way == DMA    ? launch<PK, QK, DMA>(a, p, st)
+                       : way == WIDE ? launch<PK, QK, WIDE>(a, p, st)
+                                     : launch_tile<128, 128, 2, 2, 2, PK, QK, SINGLE>(a, p.parts, st);
   if (e != hipSuccess || p.parts == 1) return e;
   const long long runs = a.M * ((a.N + 7) / 8);
   hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)rec_cdiv(runs, 256)), dim3(256), 0, st, a.part, p.parts, a.M, a.N,
