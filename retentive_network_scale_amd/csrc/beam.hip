@@ -10,8 +10,10 @@
 // from the lanes' best as such whole numbers, which at most K lanes reach.
 // The second launch, a workgroup a request, joins the slices' sums to the beams' log-sums and does the
 // same with the lists' heads and the lists.
-// Bound by the vector unit's work on an element (exponential, two comparisons): ranking all 256 lanes' best by
-// counting took three times as long (64 requests, 8 beams, 32000 bf16 logits: 29 us).
+// 64 requests, 8 beams, 32000 bf16 logits (33 MB): 14 us, 2.3 TB/s, and 8 for the second launch, a chain of four
+// dependent loads and barriers.  The first is bound by the chain of a slice: load, bound, gather, rank, each waiting
+// for the one before; ranking all 256 lanes' best by counting took 29 us.
+// A request of few slices takes one launch, whose waves keep a slice each and whose workgroup joins them.
 #include <math.h>
 
 #include <algorithm>
@@ -337,7 +339,8 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
 }
 
 // Both steps in one launch, for requests of few slices and candidates: a wave takes a slice of 2048 elements of a
-// beam at a time, the workgroup's NTH / 64 waves take turns.
+// beam at a time, the workgroup's NTH / 64 waves take turns.  One beam of 32000 fp32 logits: 10.5 us, and 5.3 + 4.8
+// in two launches, which cost a call 5 us more (15.7 against 10.9).
 constexpr int SLICE = 2048, FEW_LISTS = 32, FEW_K = 32;
 template <typename T, int NTH>
 __global__ __launch_bounds__(NTH) void request_kernel(SelectArgs a) {
@@ -573,7 +576,8 @@ extern "C" ret_status_t beam_select(const void *logits, const float *scores, con
   hipStream_t st = (hipStream_t)hip_stream;
   if (one_launch(W, V, K)) {
     a.slices = (int)rec_cdiv(V, SLICE);
-    const bool small = W * a.slices <= 4;
+    // four waves also where 16 would not fit a grid
+    const bool small = W * a.slices <= 4 || !rec_grid_ok((double)B, 1024);
     if (dtype == RET_BF16) {
       if (small)
         hipLaunchKernelGGL((request_kernel<uint16_t, 256>), dim3((unsigned)B), dim3(256), 0, st, a);

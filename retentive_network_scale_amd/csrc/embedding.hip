@@ -1,6 +1,7 @@
 // Scaled embedding and its gradient by sorted tokens (language.h).
 //
-// The lookup streams: eight elements a thread, each moved once.
+// The lookup streams: eight elements a thread, each moved once.  Bound by bytes written: 16384 tokens of 2048
+// bf16 channels (67 MB, from 5000 distinct rows) take 24 us, 64 tokens 2.6.
 //
 // The gradient of a row is a sum over the tokens that name it, in their order.  Three launches:
 //   1. Sort.  The tokens are ordered by (id modulo the number of workgroups, id, token).  Each workgroup
@@ -11,6 +12,8 @@
 //      order is cut into pieces of `piece` tokens, and runs longer than one are summed piece by piece.
 //   3. Rows.  Every row of the table's gradient is written once: the sum of a short run's tokens or of
 //      a long run's pieces, or zero.
+// 16384 tokens of 2048 bf16 channels, V 32000: 14, 10.5 and 46 us.  The last writes 131 MB and reads 67 and is bound by
+// bytes (4.3 TB/s with the pieces'); the first by its chain: ids, counts, their running sum, ids again.
 #include <algorithm>
 #include <type_traits>
 

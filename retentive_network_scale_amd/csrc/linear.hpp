@@ -134,8 +134,9 @@ struct MmPlan {
 // one workgroup and `each` for every workgroup of the fullest CU (measured with 16 tokens, and with
 // 1024 tiles, K 2048: a 128 x 128 tile fetches twice the bytes of a 256 x 256 one for its work, and a 64 x 64
 // one four times); `end` is its way from sums to output.  Parts of k cost their sums' way to memory and back
-// and a launch.  At M 16384, N 4096, K 2048 the larger two take 215 and 248 us, at M 1024 the three 31, 25 and 47, at M 200
-// 12, 21 and 45; four parts for M 16, N 2048, K 4096: 18.8 -> 10.7 us.
+// and a launch, 5 us.  At M 16384, N 4096, K 2048 tiles of 256 x 256 take 215 us and of 128 x 128 248; at M 1024 64 x 64,
+// 128 x 128 and 256 x 256 31, 25 and 47, at M 200 12, 21 and 45; M 777, N 2304, K 1000 with 64 x 128 12.1, with
+// the better of its neighbours 13.3; four parts for M 16, N 2048, K 4096: 18.8 -> 10.7 us.
 inline MmPlan mm_plan(long long M, long long N, long long K) {
   struct {
     int rows, cols;
