@@ -86,6 +86,103 @@ __global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint
   }
 }
 
+// ------------------------------------------------------------------- a batch of single tokens
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+// A workgroup takes 16 rows of w and all tokens, 16 FM at most; its eight waves take turns along k, 64 at a time,
+// and their sums meet in LDS: one launch, where tiles need parts of k and a second one.  Operands go straight from
+// memory to the matrix cores' registers, four steps ahead.  Bound by the rate at which a CU takes 16 rows' lines in
+// a load, 0.88 us for 16 rows of 1000 k (45 GB/s a CU); 32 tokens, N 4096, K 2048: 8.1 us.
+template <int FM>
+__global__ __launch_bounds__(512) void batch_kernel(const uint16_t *x, const uint16_t *w, int tokens, int N, int K,
+                                                    long long x_ld, Finish f) {
+  constexpr int WAVES = 8, AHEAD = 4, PITCH = 16 + 4, THREADS = 16 * FM * 2;  // of eight sums each
+  __shared__ __attribute__((aligned(16))) float red[WAVES][16 * FM][PITCH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const uint16_t *rows[FM + 1];  // rows behind the last are the last once more
+#pragma unroll
+  for (int i = 0; i < FM; ++i) rows[i] = x + min(i * 16 + l16, tokens - 1) * x_ld + g * 8;
+  rows[FM] = w + (long long)min(n0 + l16, N - 1) * K + g * 8;
+  f32x4 acc[FM] = {};
+  struct Chunk {
+    Words4 r[FM + 1][2];
+  };
+  auto load = [&](Chunk &c, int k) {
+#pragma unroll
+    for (int i = 0; i < FM + 1; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) c.r[i][h] = *(const Words4 *)(rows[i] + k + h * 32);
+  };
+  auto multiply = [&](const Chunk &c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, c.r[FM][h]),
+                                                         __builtin_bit_cast(bf16x8, c.r[i][h]), acc[i], 0, 0, 0);
+  };
+  // what the sums need at the end, on its way early
+  const int t = threadIdx.x, m = t / 2, col = t % 2 * 8, left = t < THREADS && m < tokens ? N - n0 - col : 0;
+  const long long at = (long long)m * N + n0 + col;
+  float bias[8] = {};
+  if (f.bias) load8(f.bias + n0 + col, left, bias);
+  Residual8 res;
+  res.load(f, at, left);
+
+  const int whole = K / 64, mine = whole > wave ? (whole - wave + WAVES - 1) / WAVES : 0;
+  const int groups = mine / AHEAD, rest = mine % AHEAD;
+  auto k_of = [&](int c) { return (wave + c * WAVES) * 64; };
+  if (groups > 0) {
+    Chunk now[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) load(now[u], k_of(u));
+    for (int i = 1; i < groups; ++i) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        multiply(now[u]);
+        load(now[u], k_of(i * AHEAD + u));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) multiply(now[u]);
+  }
+  if (rest > 0) {
+    Chunk now[AHEAD - 1];
+#pragma unroll
+    for (int u = 0; u < AHEAD - 1; ++u)
+      if (u < rest) load(now[u], k_of(groups * AHEAD + u));
+#pragma unroll
+    for (int u = 0; u < AHEAD - 1; ++u)
+      if (u < rest) multiply(now[u]);
+  }
+  if (whole * 64 < K && wave == whole % WAVES) {
+    Chunk end;
+#pragma unroll
+    for (int i = 0; i < FM + 1; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        Raw8<uint16_t> r;
+        r.load(rows[i] + whole * 64 + h * 32, K - whole * 64 - g * 8 - h * 32);
+        end.r[i][h] = r.w[0];
+      }
+    multiply(end);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) *(f32x4 *)&red[wave][i * 16 + l16][4 * g] = acc[i];
+  __syncthreads();
+  if (left <= 0) return;
+  float z[8] = {};
+#pragma unroll
+  for (int v = 0; v < WAVES; ++v) {
+    const f32x4 lo = *(const f32x4 *)&red[v][m][col], hi = *(const f32x4 *)&red[v][m][col + 4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] += lo[i], z[i + 4] += hi[i];
+  }
+  finish8(f, at, left, bias, res, z);
+}
+
 // ----------------------------------------------------------------- dz and the bias's gradient
 // Columns blockIdx.y * 512 + 8 lane .., rows blockIdx.x * 4 + wave, then parts * 4 further on.
 // dz [M][ldz] (columns behind N zero) and one partial row of sums a workgroup; either may be NULL.
@@ -142,14 +239,31 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float *part, int 
 }
 
 // ------------------------------------------------------------------------------- host
-// Whether rows_kernel serves a call.  It and the tiles take, in us, for 8 tokens 5.8 and 8.8 (N 4096, K 2048), for
-// 16 tokens 6.5 and 9.2 (1000, 1000), 8.6 and 8.8 (4096, 2048), 46 and 21 (32000, 2048).
-bool few(long long M, long long N, long long K) { return M <= 8 || (M <= 16 && N * K <= 1 << 23); }
+// Whether rows_kernel serves a call.  It and the tiles take, in us, for 8 tokens 5.8 and 8.8 (N 4096, K 2048); it and
+// batch_kernel for 16 tokens 7.5 and 9.8 (2048, 4096), where that has half the CUs, but 8.9 and 6.3 (4096, 2048) and 6.5
+// and 4.1 (1000, 1000).
+bool few(long long M, long long N, long long K) { return M <= 8 || (M <= 16 && K >= 2 * N && N * K <= 1 << 23); }
 
 template <int M, int RW>
 hipError_t launch_rows(const void *x, const void *w, int tokens, int N, int K, long long x_ld, const Finish &f,
                        hipStream_t st) {
   hipLaunchKernelGGL((rows_kernel<M, RW>), dim3((unsigned)rec_cdiv(N, RW)), dim3(256), 0, st, (const uint16_t *)x,
+                     (const uint16_t *)w, tokens, N, K, x_ld, f);
+  return hipGetLastError();
+}
+
+// Whether batch_kernel does, among the others: its time as measured (in us, without the launch) against the tiles'
+// estimate.  For 32 tokens it and the tiles take 8.1 and 10.6 (N 4096, K 2048), 4.6 and 7.1 (1000, 1000), 13.2 and 9.6
+// (2048, 4096), 48 and 22 (32000, 2048).
+bool batch(long long M, long long N, long long K) {
+  const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  return M <= 64 && 0.88e-3 * K * (fm + 1) * rec_cdiv(rec_cdiv(N, 16), 256) < mm_plan(M, N, K).us;
+}
+
+template <int FM>
+hipError_t launch_batch(const void *x, const void *w, int tokens, int N, int K, long long x_ld, const Finish &f,
+                        hipStream_t st) {
+  hipLaunchKernelGGL(batch_kernel<FM>, dim3((unsigned)rec_cdiv(N, 16)), dim3(512), 0, st, (const uint16_t *)x,
                      (const uint16_t *)w, tokens, N, K, x_ld, f);
   return hipGetLastError();
 }
@@ -184,7 +298,7 @@ BwdWs bwd_ws(long long M, int N, int K) {
 }  // namespace
 
 extern "C" size_t linear_workspace_bytes(long long M, int N, int K) {
-  if (check_sizes(M, N, K) != RET_OK || few(M, N, K)) return 0;
+  if (check_sizes(M, N, K) != RET_OK || few(M, N, K) || batch(M, N, K)) return 0;
   return mm_plan(M, N, K).bytes;
 }
 
@@ -225,6 +339,12 @@ extern "C" ret_status_t linear(const void *x, const void *w, const void *bias, c
                       : m <= 4 ? launch_rows<4, 4>(x, w, m, N, K, x_ld, f, st)
                       : m <= 8 ? launch_rows<8, 4>(x, w, m, N, K, x_ld, f, st)
                                : launch_rows<16, 4>(x, w, m, N, K, x_ld, f, st));
+  }
+  if (batch(M, N, K)) {
+    const int m = (int)M;
+    return rec_status(m <= 16   ? launch_batch<1>(x, w, m, N, K, x_ld, f, st)
+                      : m <= 32 ? launch_batch<2>(x, w, m, N, K, x_ld, f, st)
+                                : launch_batch<4>(x, w, m, N, K, x_ld, f, st));
   }
   MmArgs a = {};
   a.p = (const uint16_t *)x, a.q = (const uint16_t *)w, a.ldp = x_ld, a.ldq = K;

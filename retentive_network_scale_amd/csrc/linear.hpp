@@ -128,6 +128,7 @@ struct MmPlan {
   int parts;
   long long kpart;
   size_t bytes;  // of the parts' sums
+  double us;     // the estimate
 };
 
 // Tile and parts of k by an estimate of the time, in us.  A step (64 k) of a tile takes `alone` where a CU has
@@ -162,6 +163,7 @@ inline MmPlan mm_plan(long long M, long long N, long long K) {
       }
     }
   }
+  best.us = least;
   best.bytes = best.parts > 1 ? rec_align((size_t)best.parts * M * N * 4) : 0;
   return best;
 }

@@ -4,7 +4,7 @@
 //   forward  P = x,  Q = w         both with k along their rows
 //   dx       P = dz, Q = w         w's rows run along n: its tiles are read transposed from LDS
 //   dw       P = dz, Q = x         both with k across their rows
-// Tiles of 64 k reach LDS by DMA, two in turn, so that one is filled while the other is multiplied, and the
+// Tiles of 64 k reach LDS by DMA, two to four in turn, so that one is filled while another is multiplied, and the
 // operands of the next matrix step are read from LDS while the present one's are multiplied.
 // Operands whose rows are not 16-byte aligned take the same way through registers (M 64, N 4096, K 2048 11.7 us,
 // K 2047 19.0; M 300, N 1001, K 999 12.0 against 7.9 for 1000 and 1000).
@@ -350,11 +350,13 @@ hipError_t launch_tile(const MmArgs &a, int parts, hipStream_t st) {
 
 template <bool PK, bool QK, Way WAY>
 hipError_t launch(const MmArgs &a, const MmPlan &p, hipStream_t st) {
-  constexpr int NB = WAY == DMA ? 3 : 2;
+  // Tiles in LDS.  The smallest tiles are for calls of one workgroup a CU, whose w comes from memory: four of them
+  // (M 32, N 8192, K 2048: 18.2 -> 11.8 us).  128 x 128 with four: 27.4 -> 26.6 us (M 777, N 4096) but 33 -> 50 (N 8192).
+  constexpr int NB = WAY == DMA ? 3 : 2, NB64 = WAY == DMA ? 4 : 2;
   if (p.rows == 256) return launch_tile<256, 256, 2, 4, 2, PK, QK, WAY>(a, p.parts, st);
   if (p.rows == 128) return launch_tile<128, 128, 2, 2, 2, PK, QK, WAY>(a, p.parts, st);
   if (p.cols == 128) return launch_tile<64, 128, 2, 2, NB, PK, QK, WAY>(a, p.parts, st);
-  return launch_tile<64, 64, 2, 2, 2, PK, QK, WAY>(a, p.parts, st);
+  return launch_tile<64, 64, 2, 2, NB64, PK, QK, WAY>(a, p.parts, st);
 }
 
 // Rows of `width` elements whose 16-byte chunks are whole and aligned, within a buffer's reach.

@@ -369,6 +369,34 @@ def test_linear_infinities_and_nan_stay_in_their_rows():
         assert torch.equal(got[ok], want[ok])
 
 
+@pytest.mark.parametrize("M", [9, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("N,K", [(1, 1), (15, 63), (17, 64), (300, 65), (48, 700), (130, 2047), (2100, 1000)])
+def test_linear_a_batch_of_tokens(M, N, K):
+    """Up to 64 tokens: rows of w and of x behind the last, chunks of k that not every wave has, and a part of one."""
+    v = _linear_case(M, N, K, 160, True, True, F32 if M % 2 else BF, extra=M % 3)
+    d, _ = _check_linear(v, "gelu" if M % 2 else "silu", out_dtype=F32 if M % 2 else BF)
+    x = torch.cat([d["x"].new_zeros(1), d["x"].reshape(-1)])[1:].reshape(M, K) if M % 3 == 0 else d["x"]
+    want = rn.linear(d["x"], d["w"], d["b"], residual=d["r"], out_dtype=d["r"].dtype)
+    assert torch.equal(rn.linear(x, d["w"], d["b"], residual=d["r"], out=d["r"]), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 2100, 4200), (12, 2300, 4160), (20, 8200, 500), (60, 4200, 130)])
+def test_linear_a_batch_of_tokens_in_turns(M, N, K):
+    """More chunks of k than a wave has under way at a time, and more workgroups than there are CUs."""
+    _check_linear(_linear_case(M, N, K, 165, True, True), "silu")
+
+
+@pytest.mark.parametrize("M", [12, 40])
+def test_linear_a_batch_keeps_nan_in_its_row(M):
+    v = _linear_case(M, 80, 200, 170)
+    d = {k: _dev(t) for k, t in v.items()}
+    want = rn.linear(d["x"], d["w"])
+    d["x"][M - 1, 199], d["w"][79, 3] = float("nan"), float("inf")
+    got = rn.linear(d["x"], d["w"])
+    assert torch.isnan(got[M - 1]).all() and not torch.isfinite(got[:, 79]).any()
+    assert torch.equal(got[:M - 1, :79], want[:M - 1, :79])
+
+
 def test_activations_far_out():
     """gelu and silu of pre-activations from -40 to 40 and at infinity, through a product with the identity."""
     z = torch.cat([torch.linspace(-40, 40, 801), torch.tensor([float("inf"), 1e-30, -1e-30, 0.0])]).to(BF)
