@@ -139,7 +139,7 @@ def linear(x, w, bias=None, activation=None, residual=None, out_dtype=None, out=
         pre_out = call.empty((*lead, n), _BF16)
     elif pre_out is False:
         pre_out = None
-    m = x.numel() // k
+    m = x.numel() // max(k, 1)
     need = linear_workspace_bytes(m, n, k)
     ws, wp, wb = call.workspace(workspace, need) if need else (None, None, 0)
     call.run(lib().linear, xp, _dense(w, "w", None, _BF16, ix), _dense(bias, "bias", (n,), _BF16, ix),
@@ -166,7 +166,7 @@ def linear_bwd(x, w, d_o, pre=None, activation=None, dx=True, dw=True, dbias=Fal
     lead, (n, k), ix = x.shape[:-1], w.shape, call.index
     xp, xld = _rows(x, "x", x.dim() - 1, (*lead, k), _BF16, ix, k)
     od = x.dtype if out_dtype is None else out_dtype
-    odc, act, m = _dtc(od), _act(activation), x.numel() // k
+    odc, act, m = _dtc(od), _act(activation), x.numel() // max(k, 1)
     gx = call.empty((*lead, k), od) if dx else None
     gw = call.empty((n, k), od) if dw else None
     gb = call.empty((n,), _F32) if dbias else None

@@ -58,8 +58,8 @@ def _rows(t, name, lead, shape, dtype, index, width):
         return t.data_ptr(), width
     strides = t.stride()
     ld = strides[lead - 1]
-    if (shape[lead - 1] > 1 and ld >= width and (lead == 1 or strides[0] == shape[1] * ld) and strides[-1] == 1
-            and (len(shape) == lead + 1 or strides[-2] == shape[-1])):
+    if (0 < lead < 3 and shape[lead - 1] > 1 and ld >= width and (lead == 1 or strides[0] == shape[1] * ld)
+            and strides[-1] == 1 and (len(shape) == lead + 1 or strides[-2] == shape[-1])):
         return t.data_ptr(), ld
     want, bad = 1, False  # axes of one element may have any stride
     for n, s in zip(reversed(shape[lead:]), reversed(strides[lead:])):

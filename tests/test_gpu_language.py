@@ -397,6 +397,26 @@ def test_linear_a_batch_keeps_nan_in_its_row(M):
     assert torch.equal(got[:M - 1, :79], want[:M - 1, :79])
 
 
+def test_rows_of_three_leading_axes():
+    """Three axes of rows at one stride are taken, in another order refused, also where a part of the strides fits."""
+    x, w, ids = _r(180, 3, 2, 2, 16, dt=BF).to(DEV), _r(181, 8, 16, dt=BF).to(DEV), torch.zeros(3, 2, 2, dtype=torch.int32, device=DEV)
+    wide = torch.cat([x, x], -1)[..., :16]
+    assert torch.equal(rn.linear(wide, w), rn.linear(x, w)) and torch.equal(rn.embedding_bwd(ids, wide, 4), rn.embedding_bwd(ids, x, 4))
+    for axes in ((1, 0), (0, 2), (1, 2)):
+        t, i = x.transpose(*axes), ids.transpose(*axes).contiguous()
+        with pytest.raises(ValueError, match="one stride"):
+            rn.linear(t, w)
+        with pytest.raises(ValueError, match="one stride"):
+            rn.linear_bwd(t, w, rn.linear(t.contiguous(), w))
+        with pytest.raises(ValueError, match="one stride"):
+            rn.embedding_bwd(i, t, 4)
+    assert torch.equal(rn.linear(x[0, 0, 0], w), rn.linear(x, w)[0, 0, 0])
+    with pytest.raises(ValueError, match="one stride"):
+        rn.linear(x[0, 0, 0, ::8], w[:, :2].contiguous())
+    with pytest.raises(rn.RetentionError, match="sizes must be positive"):
+        rn.linear(x[..., :0].contiguous(), w[:, :0].contiguous())
+
+
 def test_activations_far_out():
     """gelu and silu of pre-activations from -40 to 40 and at infinity, through a product with the identity."""
     z = torch.cat([torch.linspace(-40, 40, 801), torch.tensor([float("inf"), 1e-30, -1e-30, 0.0])]).to(BF)
