@@ -97,8 +97,9 @@ struct Operand {
         int row, c;
         place(j, row, c);
         row = min(row, (KROWS ? width : left) - 1);
-        const uint32_t off = (uint32_t)row * (uint32_t)ld + min(c * 8, (KROWS ? left : width) - 8) + 8;
-        const Words4 w = *(const Words4 *)(b + (size_t)off * 2);
+        // a row's offset in 64 bits: rows are up to 2^31 elements apart
+        const uint64_t off = (uint64_t)(uint32_t)row * (uint32_t)ld + (uint32_t)(min(c * 8, (KROWS ? left : width) - 8) + 8);
+        const Words4 w = *(const Words4 *)(b + off * 2);
         reg[d][j] = u32x4{w.w[0], w.w[1], w.w[2], w.w[3]};
       }
     } else {
