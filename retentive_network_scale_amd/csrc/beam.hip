@@ -188,23 +188,30 @@ __global__ __launch_bounds__(NT) void slice_kernel(SelectArgs a) {
   if (tid == 0) a.sums[row * a.slices + slice] = make_float2(m, s);
 }
 
+// A candidate of a request: its score, and what decides between equal ones, the lower beam, then the larger logit, then
+// the lower token.  Far from zero many logits have one score (all of a beam's at the type's lowest value), so the
+// logit has to be compared itself: a slice's list is in this order only then.
 struct Key {
-  u64 score;
-  uint32_t index;  // ~ flat index
+  u64 score, tie;
+  static constexpr uint32_t LAST = LANGUAGE_MAX_VOCAB - 1;
+  static __device__ __forceinline__ u64 tie_of(int w, float value, int v) {
+    return (u64)(MAXK - 1 - w) << 56 | (u64)ordered(value) << 24 | (LAST - v);
+  }
+  __device__ __forceinline__ int beam() const { return MAXK - 1 - (int)(tie >> 56); }
+  __device__ __forceinline__ int token() const { return (int)(LAST - ((uint32_t)tie & LAST)); }
   __device__ __forceinline__ bool above(const Key &o) const {
-    return score > o.score || (score == o.score && index > o.index);
+    return score > o.score || (score == o.score && tie > o.tie);
   }
 };
+static_assert((Key::LAST & LANGUAGE_MAX_VOCAB) == 0 && LANGUAGE_MAX_VOCAB == 1 << 24, "a token in 24 bits");
 
 // What a workgroup of NTH threads needs to choose a request's K (KM at most) of its lists' candidates.
 template <int NTH, int LISTS, int KM>
 struct Join {
   double lse[MAXK];
   int kind[MAXK];  // 0: an ordinary beam, 1: ended, 2: nothing to offer
-  u64 head_score[LISTS];
-  uint32_t head_index[LISTS];
-  u64 list_score[KM * KM];
-  uint32_t list_index[KM * KM];
+  Key head[LISTS];
+  Key list[KM * KM];
   Key bound;
   int count;
 };
@@ -255,10 +262,12 @@ __device__ __forceinline__ void join(const SelectArgs &a, long long b, const flo
     const int w = list / a.slices, slice = list - w * a.slices;
     const long long row = b * a.W + w;
     int v;
+    float value = 0.0f;
     double score;
     if (lds.kind[w] == 0) {
       if (c.index < 0) return {0, 0};
       v = c.index;
+      value = c.value;
       score = (double)a.scores[row] + ((double)c.value - lds.lse[w]);
     } else {
       // the tokens in their order, after the end token where the beam has ended: in the first list
@@ -268,7 +277,7 @@ __device__ __forceinline__ void join(const SelectArgs &a, long long b, const flo
       if (v >= a.V) return {0, 0};
       score = end && j == 0 ? (double)a.scores[row] : -INFINITY;
     }
-    return {ordered(score + 0.0), ~(uint32_t)(w * a.V + v)};
+    return {ordered(score + 0.0), Key::tie_of(w, value, v)};
   };
   auto key_at = [&](int list, int j) { return key_of_cand(list, j, cands[list * a.K + j]); };
   Key mine[EACH];
@@ -279,29 +288,25 @@ __device__ __forceinline__ void join(const SelectArgs &a, long long b, const flo
       mine[u] = {0, 0};
       if (e < lists * a.K) {
         mine[u] = key_of_cand(l, j, own[u]);
-        if (j == 0) lds.head_score[l] = mine[u].score, lds.head_index[l] = mine[u].index;
+        if (j == 0) lds.head[l] = mine[u];
       }
     }
   } else {
-    for (int l = tid; l < lists; l += NTH) {
-      const Key k = key_at(l, 0);
-      lds.head_score[l] = k.score;
-      lds.head_index[l] = k.index;
-    }
+    for (int l = tid; l < lists; l += NTH) lds.head[l] = key_at(l, 0);
   }
   __syncthreads();
   for (int l = tid; l < lists; l += NTH) {
-    const Key k = {lds.head_score[l], lds.head_index[l]};
+    const Key k = lds.head[l];
     if (!k.score) continue;
     int r = 0;
-    for (int j = 0; j < lists; ++j) r += Key{lds.head_score[j], lds.head_index[j]}.above(k);
+    for (int j = 0; j < lists; ++j) r += lds.head[j].above(k);
     if (r == a.K - 1) lds.bound = k;
   }
   __syncthreads();
   // what reaches the bound: prefixes of at most K lists
   auto put = [&](const Key &k) {
     const int to = atomicAdd(&lds.count, 1);
-    if (to < CAP2) lds.list_score[to] = k.score, lds.list_index[to] = k.index;
+    if (to < CAP2) lds.list[to] = k;
   };
   if (ahead) {
 #pragma unroll
@@ -318,22 +323,22 @@ __device__ __forceinline__ void join(const SelectArgs &a, long long b, const flo
   __syncthreads();
   const int n = min(lds.count, CAP2);
   for (int e = tid; e < n; e += NTH) {
-    const Key k = {lds.list_score[e], lds.list_index[e]};
+    const Key k = lds.list[e];
     int r = 0;
-    for (int j = 0; j < n; ++j) r += Key{lds.list_score[j], lds.list_index[j]}.above(k);
+    for (int j = 0; j < n; ++j) r += lds.list[j].above(k);
     if (r < a.K) {
-      const uint32_t flat = ~k.index;
       const u64 o = k.score;
-      a.tokens[b * a.K + r] = (int)(flat % (uint32_t)a.V);
-      a.parents[b * a.K + r] = (int)(flat / (uint32_t)a.V);
+      a.tokens[b * a.K + r] = k.token();
+      a.parents[b * a.K + r] = k.beam();
       a.out_scores[b * a.K + r] =
           (float)__longlong_as_double((long long)(o ^ (o >> 63 ? 0x8000000000000000ull : ~0ull)));
     }
   }
 }
 
+template <int LISTS, int KM>
 __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
-  __shared__ Join<NT, LANGUAGE_MAX_BEAM_LISTS, MAXK> lds;
+  __shared__ Join<NT, LISTS, KM> lds;
   const long long b = blockIdx.x, lists = (long long)a.W * a.slices;
   join(a, b, a.sums + b * lists, a.cands + b * lists * a.K, lds);
 }
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(NT) void join_kernel(SelectArgs a) {
 // Both steps in one launch, for requests of few slices and candidates: a wave takes a slice of 2048 elements of a
 // beam at a time, the workgroup's NTH / 64 waves take turns.  One beam of 32000 fp32 logits: 10.5 us, and 5.3 + 4.8
 // in two launches, which cost a call 5 us more (15.7 against 10.9).
-constexpr int SLICE = 2048, FEW_LISTS = 32, FEW_K = 32;
+constexpr int SLICE = 2048, FEW_LISTS = 32, JOIN_LISTS = 512, FEW_K = 32;
 template <typename T, int NTH>
 __global__ __launch_bounds__(NTH) void request_kernel(SelectArgs a) {
   constexpr int CAP = 64;  // elements gathered by a wave
@@ -606,7 +611,11 @@ extern "C" ret_status_t beam_select(const void *logits, const float *scores, con
     else
       hipLaunchKernelGGL((slice_kernel<float, 8>), grid, dim3(NT), 0, st, a);
   }
-  hipLaunchKernelGGL(join_kernel, dim3((unsigned)B), dim3(NT), 0, st, a);
+  // LDS for the lists and K that there are: 25 KB or 98
+  if (W * w.slices <= JOIN_LISTS && K <= FEW_K)
+    hipLaunchKernelGGL((join_kernel<JOIN_LISTS, FEW_K>), dim3((unsigned)B), dim3(NT), 0, st, a);
+  else
+    hipLaunchKernelGGL((join_kernel<LANGUAGE_MAX_BEAM_LISTS, MAXK>), dim3((unsigned)B), dim3(NT), 0, st, a);
   return rec_status(hipGetLastError());
 }
 

@@ -1,5 +1,7 @@
 """GPU tests of the operators around the layers (include/language.h) at the edges of what their calls take:
-row strides beyond 32 bits within a tile."""
+row strides beyond 32 bits within a tile, beams whose scores are so far out that their tokens' scores meet."""
+import math
+
 import pytest
 import torch
 
@@ -32,3 +34,42 @@ def test_linear_rows_far_apart(M, N, K, ld):
     assert torch.equal(rn.linear(far, w, b), rn.linear(rows, w, b))
     far_g, g = (rn.linear_bwd(x, w, d_o, dbias=True) for x in (far, rows))
     assert all(torch.equal(s, t) for s, t in zip(far_g, g))
+
+
+# ------------------------------------------------------------------------------------- beams
+def _select_ref(z, cum, K):
+    """(tokens, parents), every continuation sorted by score, then beam, then logit, then token."""
+    B, W, V = z.shape
+    got = []
+    for b in range(B):
+        every = []
+        for w in range(W):
+            top = z[b, w].double().max().item()
+            lse = top + math.log(torch.exp(z[b, w].double() - top).sum().item())
+            every += [(-(cum[b, w].item() + (x - lse)), w, -x, v) for v, x in enumerate(z[b, w].tolist())]
+        got.append([(v, w) for _, w, _, v in sorted(every)[:K]])
+    got = torch.tensor(got, dtype=I32)
+    return got[..., 0], got[..., 1]
+
+
+@pytest.mark.parametrize("score", [torch.finfo(F32).min, -1e30, -1e15])
+@pytest.mark.parametrize("W,V,K", [(1, 100, 4), (3, 5, 12), (2, 9000, 20), (1, 70000, 9), (4, 30000, 40), (2, 300, 64)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_select_closed_beams(W, V, K, dt, score):
+    """Beams that are closed by a score far out, where the scores of all their tokens are one: a beam's tokens
+    come by logit, equal beams by index; and behind an open beam's tokens."""
+    z, cum = (2.5 * _r(10, 2, W, V)).to(dt), torch.full((2, W), score)
+    cum[1, 0] = -1.0
+    got = rn.beam_select(z.to(DEV), cum.to(DEV), K)
+    tokens, parents = _select_ref(z, cum, K)
+    assert torch.equal(got.tokens.cpu(), tokens) and torch.equal(got.parents.cpu(), parents)
+    want = cum.gather(1, parents.long())
+    assert ((got.scores.cpu() - want).abs() <= 30 + 2.0 ** -24 * want.abs()).all()
+
+
+def test_select_logits_closer_than_scores():
+    """Logits that differ by less than a score can tell are still in their own order."""
+    z = torch.full((1, 1, 4000), -10.0)
+    z[0, 0, 7], z[0, 0, 3], z[0, 0, 3999] = 1e-20, 0.0, 2e-20
+    got = rn.beam_select(z.to(DEV), torch.zeros(1, 1, device=DEV), 3)
+    assert got.tokens.cpu().tolist() == [[3999, 7, 3]]
