@@ -138,10 +138,12 @@ ret_status_t linear_bwd(const void *x, const void *w, const void *d_o, const voi
  *            zero offers token eos at its own score and nothing else
  *   tokens, parents : int32 [B, K]     out_scores : fp32 [B, K]
  *   workspace : beam_select_workspace_bytes() bytes (NULL where that is 0)
- * Scores are compared in 64 bits.  A continuation without a finite score (a logit of -inf,
- * the other tokens of an ended beam; all of a beam whose score is not finite, or whose
- * logits hold a NaN or +inf or nothing above -inf) counts as -inf: it is taken after all
- * others, by index.  K is at most W V.
+ * Scores, score + (logit - s), are compared in 64 bits.  s is the row's largest logit +
+ * log(1 + sum of e^-d) over the others, each d below it; an exponential in this sum is good to
+ * (16 + 3 d) 2^-24 of itself, the logarithm and what follows are in 64 bits.
+ * A continuation without a finite score (a logit of -inf, the other tokens of an ended beam;
+ * all of a beam whose score is not finite, or whose logits hold a NaN or +inf or nothing above
+ * -inf) counts as -inf: it is taken after all others, by index.  K is at most W V.
  */
 size_t beam_select_workspace_bytes(int B, int W, int V, int K);
 ret_status_t beam_select(const void *logits, const float *scores, const unsigned char *ended,

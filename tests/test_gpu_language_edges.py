@@ -73,3 +73,32 @@ def test_select_logits_closer_than_scores():
     z[0, 0, 7], z[0, 0, 3], z[0, 0, 3999] = 1e-20, 0.0, 2e-20
     got = rn.beam_select(z.to(DEV), torch.zeros(1, 1, device=DEV), 3)
     assert got.tokens.cpu().tolist() == [[3999, 7, 3]]
+
+
+@pytest.mark.parametrize("V,B", [(50, 1), (9000, 1), (70000, 1), (9000, 100), (40000, 60)])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("top", [0.0, 19.5])
+def test_select_confident_beams(V, B, dt, top):
+    """Beams of one score whose rows hold almost everything in one token: they differ by what is left, far below
+    2^-24.  Of the remainder's terms, e^-d, each is off by at most (16 + 3 d) 2^-24, and so is the score."""
+    W, K = 8, 8
+    left = 17.0 + torch.randperm(W, generator=_gen(20)).double() / 4  # -log of what is left, in steps that both types hold
+    z = torch.full((B, W, V), -math.inf)
+    at = torch.randint(0, V - 1, (B, W, 1), generator=_gen(21))
+    z.scatter_(2, at, top)
+    z.scatter_(2, at + 1, (top - left.float())[None, :, None].expand(B, W, 1).clone())
+    z = z.to(dt)
+    got = rn.beam_select(z.to(DEV), torch.zeros(B, W, device=DEV), K)
+    gap = (top - z.gather(2, at + 1).double())[..., 0]
+    order = gap.argsort(-1, descending=True)
+    want = -torch.log1p(torch.exp(-gap)).gather(1, order)
+    assert len(set(gap[0].tolist())) == W
+    assert torch.equal(got.parents.cpu().long(), order) and torch.equal(got.tokens.cpu().long(), at[..., 0].gather(1, order))
+    assert ((got.scores.cpu().double() - want).abs() <= (17 + 3 * gap.gather(1, order)) * 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.parametrize("V", [1, 8, 3000, 70000])
+def test_select_log_sum_of_equal_logits(V):
+    """A row of one value is counted: its log-sum is log V, whatever the slices are, and the score is rounded once."""
+    got = rn.beam_select(torch.full((1, 2, V), 3.25, device=DEV), torch.zeros(1, 2, device=DEV), 1)
+    assert abs(got.scores.item() + math.log(V)) <= 2.0 ** -24 * math.log(V) + 1e-15
