@@ -170,9 +170,20 @@ __global__ __launch_bounds__(BWD_NT) void norm_bwd_kernel(NormArgs a) {
       if (a.gate) gr[k].get(g[k]);
     }
     fetch(tok + step);
+    TO *dgate = (TO *)a.dgate + (long long)tok * a.H * a.W + (long long)h * a.W;
+    TO *dx = (TO *)a.dx + (((long long)b * a.H + h) * a.L + t) * a.W;
+    if (!now) {  // zero whatever weight and bias are
+      const float zero[8] = {};
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int c = (k * TPR + col) * 8;
+        if (a.gate) store8(dgate + c, a.W - c, zero);
+        store8(dx + c, a.W - c, zero);
+      }
+      continue;
+    }
     const float r = normalise<TPR, C>(x, col, a.W, a.eps);
     float s1 = 0.0f, s2 = 0.0f;
-    TO *dgate = (TO *)a.dgate + (long long)tok * a.H * a.W + (long long)h * a.W;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8;
@@ -206,12 +217,11 @@ __global__ __launch_bounds__(BWD_NT) void norm_bwd_kernel(NormArgs a) {
     }
     s1 = row_sum<TPR>(s1) / (float)a.W;
     s2 = row_sum<TPR>(s2) / (float)a.W;
-    TO *dx = (TO *)a.dx + (((long long)b * a.H + h) * a.L + t) * a.W;
 #pragma unroll
     for (int k = 0; k < C; ++k) {
       const int c = (k * TPR + col) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[k][i] = now ? r * (d[k][i] - s1 - x[k][i] * s2) : 0.0f;
+      for (int i = 0; i < 8; ++i) d[k][i] = r * (d[k][i] - s1 - x[k][i] * s2);
       store8(dx + c, a.W - c, d[k]);
     }
   }

@@ -1,5 +1,6 @@
 """GPU tests of the operators around the layers (include/language.h) at the edges of what their calls take:
-row strides beyond 32 bits within a tile, beams whose scores are so far out that their tokens' scores meet."""
+row strides beyond 32 bits within a tile, beams whose scores are so far out that their tokens'
+scores meet, parameters that are not finite beside rows that do not count."""
 import math
 
 import pytest
@@ -18,6 +19,24 @@ def _gen(seed):
 
 def _r(seed, *shape, dt=F32):
     return torch.randn(*shape, generator=_gen(seed)).to(dt)
+
+
+# -------------------------------------------------------------------------------------- norm
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+def test_norm_rows_behind_an_end_have_no_gradient(gate, value):
+    """Whatever weight and bias hold; sums over no token at all are zero."""
+    B, H, L, W = 3, 2, 7, 40
+    x, d_o = _r(30, B, H, L, W).to(DEV), _r(31, B, L, H * W).to(DEV)
+    g = _r(32, B, L, H * W).to(DEV) if gate else None
+    w, b = torch.ones(H * W, device=DEV), torch.zeros(H * W, device=DEV)
+    w[50], b[3] = value, value
+    for lengths in ([2, 0, 7], [0, 0, 0]):
+        got = rn.group_norm_gate_bwd(x, d_o, g, w, b, lengths=torch.tensor(lengths, dtype=I32, device=DEV))
+        dead = torch.arange(L)[None] >= torch.tensor(lengths)[:, None]
+        assert (got.dx.transpose(1, 2).cpu()[dead] == 0).all()
+        assert not gate or (got.dgate.cpu()[dead] == 0).all()
+    assert (got.dweight == 0).all() and (got.dbias == 0).all()
 
 
 # ------------------------------------------------------------------------------------ linear
