@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const uint16_t *x, const uint
     const long long at = (long long)m * N + col;
     if (f.bias) v += bf2f(f.bias[col]);
     if (f.pre) f.pre[at] = f2bf(v);
-    v = act_value(v, f.act);
+    v = act_value(v, f.act, f.out_bf16);
     if (f.residual) v += load_elem(f.residual, at, f.res_bf16);
     store_elem(f.out, at, v, f.out_bf16);
   }

@@ -9,12 +9,14 @@
 
 namespace ret {
 
-
 constexpr int BK = 64;  // k of a tile
 
 // ------------------------------------------------------------------------ activations
-// Phi(-a) for a >= 0 as 2^p(a), p a polynomial fitted to log2 Phi(-a) on 0..6 (a minimax fit of degree 7
-// made for this file; 5.7e-6 of the value at most, evaluated in fp32); behind 6 it stays at 1e-9.
+// gelu(z) = z Phi(z) = max(z, 0) - |z| Phi(-|z|), so that small results keep their relative accuracy, in two forms.
+//
+// For results that leave in bf16: Phi(-a), a >= 0, as 2^p(a), p a polynomial fitted to log2 Phi(-a) on 0..6 (a minimax
+// fit of degree 7 made for this file; 5.7e-6 of the value at most, evaluated in fp32).  Behind 6 it falls faster
+// than Phi does, to zero at 14: good to 4e-4 of the value at 7, 6e-3 at 8, where that is 6e-16.
 __device__ __forceinline__ float normal_tail(float a) {
   float p = -1.834846444e-06f;
   p = fmaf(p, a, 6.159897748e-05f);
@@ -26,15 +28,29 @@ __device__ __forceinline__ float normal_tail(float a) {
   p = fmaf(p, a, -9.999952912e-01f);
   return __builtin_amdgcn_exp2f(p);
 }
-// z Phi(z) = max(z, 0) - |z| Phi(-|z|), so that small results keep their relative accuracy.
-__device__ __forceinline__ float gelu(float z) {
-  const float a = fminf(fabsf(z), 6.0f);
+__device__ __forceinline__ float gelu_bf16(float z) {
+  const float a = fminf(fabsf(z), 14.0f);
   return fmaf(0.5f, fabsf(z), 0.5f * z) - a * normal_tail(a);
 }
-// Phi(z) + z phi(z), for the gradients, whose sums (dbias) stay in fp32: p is of degree 10 here, fitted for
-// the absolute error, 3.2e-8 at most.
+// For results that leave in fp32: Phi(-a) = e^(-a a / 2) m(a), m a polynomial in 1 / (1 + 0.35 a) (of degree 7, fitted
+// here for the relative error on 0..14, 5.2 half steps of fp32).  (10 + 2 a a) half steps of the value in all, most of
+// them the exponential's argument's, until it leaves fp32's range behind 13.  23 issue slots against 17.
+__device__ __forceinline__ float gelu_f32(float z) {
+  const float a = fminf(fabsf(z), 14.0f), t = __builtin_amdgcn_rcpf(fmaf(0.35f, a, 1.0f));
+  float m = 4.8942431807518005e-02f;
+  m = fmaf(m, t, -2.0211923122406006e-01f);
+  m = fmaf(m, t, 2.4064074456691742e-01f);
+  m = fmaf(m, t, -1.7023373395204544e-02f);
+  m = fmaf(m, t, 1.5596145391464233e-01f);
+  m = fmaf(m, t, 1.3335511088371277e-01f);
+  m = fmaf(m, t, 1.4027033746242523e-01f);
+  m = fmaf(m, t, -2.7315489205648191e-05f);
+  return fmaf(0.5f, fabsf(z), 0.5f * z) - a * (__builtin_amdgcn_exp2f(a * (-0.5f * kLog2e) * a) * m);
+}
+// Phi(z) + z phi(z), for the gradients, whose sums (dbias) stay in fp32: p is of degree 10 here, fitted on 0..6 for
+// the absolute error, 3.2e-8 at most; behind 6 it falls as the other does.
 __device__ __forceinline__ float gelu_slope(float z) {
-  const float a = fminf(fabsf(z), 6.0f);
+  const float a = fminf(fabsf(z), 14.0f);
   float p = -2.643092323e-08f;
   p = fmaf(p, a, 8.022586258e-07f);
   p = fmaf(p, a, -1.040739517e-05f);
@@ -50,8 +66,9 @@ __device__ __forceinline__ float gelu_slope(float z) {
   const float phi = 0.3989422804f * __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
   return fmaf(z, phi, z >= 0.0f ? 1.0f - t : t);
 }
-__device__ __forceinline__ float act_value(float z, int act) {
-  return act == LINEAR_ACT_GELU ? gelu(z) : act == LINEAR_ACT_SILU ? z * sigmoid(z) : z;
+__device__ __forceinline__ float act_value(float z, int act, bool out_bf16) {
+  if (act == LINEAR_ACT_GELU) return out_bf16 ? gelu_bf16(z) : gelu_f32(z);
+  return act == LINEAR_ACT_SILU ? z * sigmoid(z) : z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
   if (act == LINEAR_ACT_GELU) return gelu_slope(z);
@@ -66,6 +83,7 @@ struct Finish {
   void *out;
   uint16_t *pre;
   int act, res_bf16, out_bf16;
+  __host__ __device__ bool fine() const { return act == LINEAR_ACT_GELU && !out_bf16; }
 };
 
 // Eight elements of the residual on their way, of either type.
@@ -92,24 +110,35 @@ struct Residual8 {
 };
 
 // Eight of z's elements, `left` of which exist, at `at` of [M][N]: bias (zero where there is none), activation,
-// residual.
+// residual.  FINE: the activation is gelu for fp32.
+template <bool FINE>
 __device__ __forceinline__ void finish8(const Finish &f, long long at, int left, const float (&bias)[8],
                                         const Residual8 &res, float (&z)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] += bias[i];
   if (f.pre) store8(f.pre + at, left, z);
-  if (f.act == LINEAR_ACT_GELU) {
+  if constexpr (FINE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = gelu(z[i]);
+    for (int i = 0; i < 8; ++i) z[i] = gelu_f32(z[i]);
+  } else if (f.act == LINEAR_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = gelu_bf16(z[i]);
   } else if (f.act == LINEAR_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= sigmoid(z[i]);
   }
   res.add(f, z);
-  if (f.out_bf16)
+  if (!FINE && f.out_bf16)
     store8((uint16_t *)f.out + at, left, z);
   else
     store8((float *)f.out + at, left, z);
+}
+__device__ __forceinline__ void finish8(const Finish &f, long long at, int left, const float (&bias)[8],
+                                        const Residual8 &res, float (&z)[8]) {
+  if (f.fine())
+    finish8<true>(f, at, left, bias, res, z);
+  else
+    finish8<false>(f, at, left, bias, res, z);
 }
 
 struct MmArgs {
@@ -171,6 +200,7 @@ inline MmPlan mm_plan(long long M, long long N, long long K) {
 // The products on `ws`, mm_plan's bytes: forward (both operands with k along their rows), dx (P with k
 // along, Q across) and dw (both across).
 hipError_t mm_forward(MmArgs a, void *ws, hipStream_t st);
+hipError_t mm_forward_fine(MmArgs a, void *ws, hipStream_t st);  // gelu for fp32
 hipError_t mm_dx(MmArgs a, void *ws, hipStream_t st);
 hipError_t mm_dw(MmArgs a, void *ws, hipStream_t st);
 

@@ -167,7 +167,9 @@ __device__ __forceinline__ void meet() {
 // BM x BN of out by WM x WN waves, with a ring of NB tiles in LDS.  A wave multiplies the operands of a half
 // tile while it reads those of the next half.  The barrier in the middle of a tile tells that all
 // have read it, so that tile i + NB takes its place, and that tile i + 1 has come.
-template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY>
+// FINE: finish8's.  A kernel of its own: with both kinds of gelu in one, the large product without any took 241 us
+// instead of 226, going round their code.
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY, bool FINE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
   constexpr int NT = WM * WN * 64, FM = BM / WM / 16, FN = BN / WN / 16;
   // WIDE's tiles under way: as many as there are registers for beside the sums
@@ -314,7 +316,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void mm_kernel(MmArgs a) {
         if (a.part)
           store8(a.part + ((long long)blockIdx.y * a.M + m) * a.N + n, a.N - n, z);
         else
-          finish8(a.f, m * a.N + n, a.N - n, bias, res[i & 1][q], z);
+          finish8<FINE>(a.f, m * a.N + n, a.N - n, bias, res[i & 1][q], z);
       }
     }
   }
@@ -342,22 +344,22 @@ __global__ __launch_bounds__(256) void mm_join_kernel(const float *part, int par
   finish8(f, m * N + n, N - n, bias, res, z);
 }
 
-template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY>
+template <int BM, int BN, int WM, int WN, int NB, bool PK, bool QK, Way WAY, bool FINE>
 hipError_t launch_tile(const MmArgs &a, int parts, hipStream_t st) {
   const dim3 grid((unsigned)(rec_cdiv(a.M, BM) * rec_cdiv(a.N, BN)), (unsigned)parts);
-  hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, NB, PK, QK, WAY>), grid, dim3(WM * WN * 64), 0, st, a);
+  hipLaunchKernelGGL((mm_kernel<BM, BN, WM, WN, NB, PK, QK, WAY, FINE>), grid, dim3(WM * WN * 64), 0, st, a);
   return hipGetLastError();
 }
 
-template <bool PK, bool QK, Way WAY>
+template <bool PK, bool QK, Way WAY, bool FINE>
 hipError_t launch(const MmArgs &a, const MmPlan &p, hipStream_t st) {
   // Tiles in LDS.  The smallest tiles are for calls of one workgroup a CU, whose w comes from memory: four of them
   // (M 32, N 8192, K 2048: 18.2 -> 11.8 us).  128 x 128 with four: 27.4 -> 26.6 us (M 777, N 4096) but 33 -> 50 (N 8192).
   constexpr int NB = WAY == DMA ? 3 : 2, NB64 = WAY == DMA ? 4 : 2;
-  if (p.rows == 256) return launch_tile<256, 256, 2, 4, 2, PK, QK, WAY>(a, p.parts, st);
-  if (p.rows == 128) return launch_tile<128, 128, 2, 2, 2, PK, QK, WAY>(a, p.parts, st);
-  if (p.cols == 128) return launch_tile<64, 128, 2, 2, NB, PK, QK, WAY>(a, p.parts, st);
-  return launch_tile<64, 64, 2, 2, NB64, PK, QK, WAY>(a, p.parts, st);
+  if (p.rows == 256) return launch_tile<256, 256, 2, 4, 2, PK, QK, WAY, FINE>(a, p.parts, st);
+  if (p.rows == 128) return launch_tile<128, 128, 2, 2, 2, PK, QK, WAY, FINE>(a, p.parts, st);
+  if (p.cols == 128) return launch_tile<64, 128, 2, 2, NB, PK, QK, WAY, FINE>(a, p.parts, st);
+  return launch_tile<64, 64, 2, 2, NB64, PK, QK, WAY, FINE>(a, p.parts, st);
 }
 
 // Rows of `width` elements whose 16-byte chunks are whole and aligned, within a buffer's reach.
@@ -365,7 +367,7 @@ bool chunked(const void *p, long long ld, long long width) {
   return rec_aligned(p, 16) && ld % 8 == 0 && width % 8 == 0 && ld <= (1 << 21);
 }
 
-template <bool PK, bool QK>
+template <bool PK, bool QK, bool FINE = false>
 hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   const MmPlan p = mm_plan(a.M, a.N, a.K);
   a.kpart = p.kpart;
@@ -373,9 +375,9 @@ hipError_t product(MmArgs a, void *ws, hipStream_t st) {
   const long long wp = PK ? a.K : a.M, wq = QK ? a.K : a.N;
   const Way way = chunked(a.p, a.ldp, wp) && chunked(a.q, a.ldq, wq) ? DMA : wp >= 8 && wq >= 8 ? WIDE : SINGLE;
   // SINGLE in one size: 128 x 128 of the largest output still are a grid
-  const hipError_t e = way == DMA    ? launch<PK, QK, DMA>(a, p, st)
-                       : way == WIDE ? launch<PK, QK, WIDE>(a, p, st)
-                                     : launch_tile<128, 128, 2, 2, 2, PK, QK, SINGLE>(a, p.parts, st);
+  const hipError_t e = way == DMA    ? launch<PK, QK, DMA, FINE>(a, p, st)
+                       : way == WIDE ? launch<PK, QK, WIDE, FINE>(a, p, st)
+                                     : launch_tile<128, 128, 2, 2, 2, PK, QK, SINGLE, FINE>(a, p.parts, st);
   if (e != hipSuccess || p.parts == 1) return e;
   const long long runs = a.M * ((a.N + 7) / 8);
   hipLaunchKernelGGL(mm_join_kernel, dim3((unsigned)rec_cdiv(runs, 256)), dim3(256), 0, st, a.part, p.parts, a.M, a.N,

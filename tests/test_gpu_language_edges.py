@@ -55,6 +55,40 @@ def test_linear_rows_far_apart(M, N, K, ld):
     assert all(torch.equal(s, t) for s, t in zip(far_g, g))
 
 
+def _gelu(z):
+    """z Phi(z) in 64 bits, with Phi's relative accuracy for far negative z."""
+    return z * torch.exp(torch.special.log_ndtr(z))
+
+
+@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("od", [BF, F32])
+def test_linear_gelu_of_far_values(M, od):
+    """Through a product with the identity, by each of the kernels: in fp32 to (10 + 2 z^2) half steps of the value
+    (and its rounding's one) where that is a normal number; in bf16 to half a step and 5.7e-6, behind -6 to 1e-13;
+    far out 0."""
+    z = torch.cat([torch.linspace(-13, 13, 997), torch.linspace(-40, 40, 401), torch.logspace(-30, 0, 301), -torch.logspace(-30, 0, 301)]).to(BF)
+    z = z[:z.numel() // M * M].reshape(M, -1)
+    N = z.shape[1]
+    got = rn.linear(z.to(DEV), torch.eye(N, dtype=BF, device=DEV), activation="gelu", out_dtype=od).cpu().double()
+    want = _gelu(z.double())
+    tol = 2.0 ** -24 * (11 + 2 * z.double() ** 2).clamp(max=400) * want.abs() if od == F32 else (2.0 ** -8 + 5.8e-6) * want.abs() + (z < -6) * 1e-13
+    assert ((got - want).abs() <= tol + 1.2e-38).all()
+    assert not got[z < -14].any()
+
+
+def test_linear_gelu_slope_of_far_values():
+    """The slope, by way of the bias's gradient, to 3.2e-8 and the roundings of z phi(z); far out 0 and 1."""
+    z = torch.linspace(-40, 40, 1601).to(BF)[None]
+    one = torch.ones(1, z.shape[1], dtype=BF, device=DEV)
+    w = torch.zeros(z.shape[1], 8, dtype=BF, device=DEV)
+    got = rn.linear_bwd(one[:, :8], w, one, pre=z.to(DEV), activation="gelu", dx=False, dw=False, dbias=True).dbias.cpu().double()
+    z = z[0].double()
+    phi = torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    want = torch.exp(torch.special.log_ndtr(z)) + z * phi
+    assert ((got - want).abs() <= 3.3e-8 + 2.0 ** -24 * ((4 + z * z) * z.abs() * phi + 2 * want.abs())).all()
+    assert not got[z < -20].any() and (got[z > 20] == 1).all()
+
+
 # ------------------------------------------------------------------------------------- beams
 def _select_ref(z, cum, K):
     """(tokens, parents), every continuation sorted by score, then beam, then logit, then token."""
