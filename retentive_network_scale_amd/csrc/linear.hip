@@ -93,7 +93,7 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 // A workgroup takes 16 rows of w and all tokens, 16 FM at most; its eight waves take turns along k, 64 at a time,
 // and their sums meet in LDS: one launch, where tiles need parts of k and a second one.  Operands go straight from
 // memory to the matrix cores' registers, four steps ahead.  Bound by the rate at which a CU takes 16 rows' lines in
-// a load, 0.88 us for 16 rows of 1000 k (45 GB/s a CU); 32 tokens, N 4096, K 2048: 8.1 us.
+// a load, 0.88 us for 16 rows of 1000 k (36 GB/s a CU); 32 tokens, N 4096, K 2048: 8.1 us.
 template <int FM>
 __global__ __launch_bounds__(512) void batch_kernel(const uint16_t *x, const uint16_t *w, int tokens, int N, int K,
                                                     long long x_ld, Finish f) {
@@ -186,6 +186,9 @@ __global__ __launch_bounds__(512) void batch_kernel(const uint16_t *x, const uin
 // ----------------------------------------------------------------- dz and the bias's gradient
 // Columns blockIdx.y * 512 + 8 lane .., rows blockIdx.x * 4 + wave, then parts * 4 further on.
 // dz [M][ldz] (columns behind N zero) and one partial row of sums a workgroup; either may be NULL.
+// dz is rounded to bf16, as an operand of two products on the bf16 matrix cores: the gradients are off by 2.35e-3
+// (relative, of normal values) where those of an unrounded dz, rounded at the end, are by 1.66e-3; two bf16 terms
+// would keep it at twice the products' work.  The bias's sums take it unrounded.
 // Bound by bytes: 403 MB in 75 us (M 16384, N 4096), the copy rate.
 __global__ __launch_bounds__(256) void dz_kernel(const uint16_t *d_o, const uint16_t *pre, uint16_t *dz, float *part,
                                                  long long M, int N, int ldz, int parts, int act) {
