@@ -244,8 +244,11 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(const float *part, int 
 // ------------------------------------------------------------------------------- host
 // Whether rows_kernel serves a call.  It and the tiles take, in us, for 8 tokens 5.8 and 8.8 (N 4096, K 2048); it and
 // batch_kernel for 16 tokens 7.5 and 9.8 (2048, 4096), where that has half the CUs, but 8.9 and 6.3 (4096, 2048) and 6.5
-// and 4.1 (1000, 1000).
-bool few(long long M, long long N, long long K) { return M <= 8 || (M <= 16 && K >= 2 * N && N * K <= 1 << 23); }
+// and 4.1 (1000, 1000).  Rows of odd length, of which a lane's 16 bytes begin at any two, cost it three times as much:
+// 16 tokens 28 us, the tiles 12 (2048, 4095).
+bool few(long long M, long long N, long long K) {
+  return M <= 8 || (M <= 16 && K >= 2 * N && N * K <= 1 << 23 && K % 2 == 0);
+}
 
 template <int M, int RW>
 hipError_t launch_rows(const void *x, const void *w, int tokens, int N, int K, long long x_ld, const Finish &f,
@@ -257,10 +260,14 @@ hipError_t launch_rows(const void *x, const void *w, int tokens, int N, int K, l
 
 // Whether batch_kernel does, among the others: its time as measured (in us, without the launch) against the tiles'
 // estimate.  For 32 tokens it and the tiles take 8.1 and 10.6 (N 4096, K 2048), 4.6 and 7.1 (1000, 1000), 13.2 and 9.6
-// (2048, 4096), 48 and 22 (32000, 2048).
+// (2048, 4096), 48 and 22 (32000, 2048).  With rows of odd length it takes three times as much and the tiles 1.5 times:
+// for 16 tokens 8.8 and 16.6 (4096, 1401) but 16.6 and 11.4 (4096, 2047), for 33 10.6 and 12.1 (1000, 999), for 64 14.1
+// and 12.4 (1000, 999) and 36 and 20 (4096, 2047); there rows that are the last once more cost little.
 bool batch(long long M, long long N, long long K) {
-  const int fm = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  return M <= 64 && 0.88e-3 * K * (fm + 1) * rec_cdiv(rec_cdiv(N, 16), 256) < mm_plan(M, N, K).us;
+  if (M > 64) return false;
+  const double each = 0.88e-3 * K * rec_cdiv(rec_cdiv(N, 16), 256);
+  if (K % 2) return each * (M / 16.0 + 1) < 2.75;
+  return each * ((M <= 16 ? 1 : M <= 32 ? 2 : 4) + 1) < mm_plan(M, N, K).us;
 }
 
 template <int FM>

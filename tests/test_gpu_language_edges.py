@@ -7,6 +7,8 @@ import pytest
 import torch
 
 import retentive_network_scale_amd as rn
+from tests import _language_ref as ref
+from tests._recurrent_ref import assert_near
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -53,6 +55,16 @@ def test_linear_rows_far_apart(M, N, K, ld):
     assert torch.equal(rn.linear(far, w, b), rn.linear(rows, w, b))
     far_g, g = (rn.linear_bwd(x, w, d_o, dbias=True) for x in (far, rows))
     assert all(torch.equal(s, t) for s, t in zip(far_g, g))
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 300, 1401), (16, 300, 2047), (33, 200, 999), (40, 200, 999), (64, 130, 699), (12, 100, 4095)])
+def test_linear_rows_of_odd_length(M, N, K):
+    """Few tokens on both sides of where rows of odd length go to the tiles."""
+    x, w, b = _r(5, M, K, dt=BF), (_r(6, N, K) * K ** -0.5).to(BF), _r(7, N, dt=BF)
+    out, pre = rn.linear(x.to(DEV), w.to(DEV), b.to(DEV), "silu", out_dtype=F32, pre_out=True)
+    o, om, z, zm = ref.linear(x, w, b, "silu", None)
+    assert_near(out, o, om, 2 * K + 160, "out")
+    assert_near(pre, z, zm, 2 * K + 2, "pre")
 
 
 def _gelu(z):
