@@ -480,7 +480,7 @@ struct ReorderArgs {
   long long bytes[MT];
   unsigned first[MT + 1];  // workgroups of a request in front of tensor i; behind the last their number, then ~0
   const int *parents;
-  int count, W;
+  int W;
 };
 
 // A thread holds the same few bytes of every beam of a request: it reads the parents' before it
@@ -667,7 +667,8 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
   if (!states || !bytes || !parents) return rec_fail(RET_ERR_INVALID_ARG, "NULL pointer");
   if (!rec_aligned(parents, 4)) return rec_fail(RET_ERR_INVALID_ARG, "a pointer is not aligned to its elements");
   ReorderArgs<LANGUAGE_MAX_REORDERED> a = {};
-  a.parents = parents, a.count = 0, a.W = W;
+  a.parents = parents, a.W = W;
+  int n = 0;  // tensors that hold anything
   const RecSpan par = {"parents", parents, (size_t)B * W * 4};
   RecSpan all[LANGUAGE_MAX_REORDERED];
   unsigned blocks = 0;
@@ -677,7 +678,6 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
       return rec_fail(RET_ERR_UNSUPPORTED, "a tensor is too large");
     if (bytes[i] == 0) continue;
     if (!states[i]) return rec_fail(RET_ERR_INVALID_ARG, "NULL tensor pointer");
-    const int n = a.count++;
     all[n] = {"a tensor", states[i], (size_t)bytes[i] * B * W};
     if (rec_overlap(all[n], par)) return rec_fail(RET_ERR_INVALID_ARG, "a tensor overlaps parents");
     for (int j = 0; j < n; ++j)
@@ -686,16 +686,16 @@ extern "C" ret_status_t beam_reorder(void *const *states, const long long *bytes
     a.bytes[n] = bytes[i];
     a.first[n] = blocks;
     blocks += (unsigned)std::min<long long>(4096, rec_cdiv(bytes[i], NT * 16));
-    a.first[n + 1] = blocks;
+    a.first[++n] = blocks;
   }
-  if (a.count == 0) return rec_status(hipSuccess);
-  for (int i = a.count + 1; i <= LANGUAGE_MAX_REORDERED; ++i) a.first[i] = ~0u;
+  if (n == 0) return rec_status(hipSuccess);
+  for (int i = n + 1; i <= LANGUAGE_MAX_REORDERED; ++i) a.first[i] = ~0u;
   if (!rec_grid_ok((double)blocks * B, NT)) return rec_fail(RET_ERR_UNSUPPORTED, "too many workgroups for one launch");
   const dim3 grid(blocks, (unsigned)B);
   hipStream_t st = (hipStream_t)hip_stream;
-  if (a.count > 4) return rec_status(launch_reorder(a, grid, st));
+  if (n > 4) return rec_status(launch_reorder(a, grid, st));
   ReorderArgs<4> few = {};
   for (int i = 0; i < 4; ++i) few.states[i] = a.states[i], few.bytes[i] = a.bytes[i], few.first[i + 1] = a.first[i + 1];
-  few.parents = parents, few.count = a.count, few.W = W;
+  few.parents = parents, few.W = W;
   return rec_status(launch_reorder(few, grid, st));
 }
