@@ -15,6 +15,9 @@
  *   - Outputs must not overlap inputs, the workspace or each other, except where
  *     a call says so.  Calls sharing a workspace must not overlap in time; two
  *     captured graphs that may run at once need two workspaces.
+ *   - A workspace query's size is for the sizes it was asked for, whatever the call's other
+ *     arguments are.  It does not grow with every size: a caller with calls of several sizes
+ *     takes the largest of their answers (a product of fewer rows may be cut into more parts).
  *   - A call without rows (n, M, B or L of 0 where the call allows it) launches
  *     nothing, or writes the zeros that an empty sum is.
  */
@@ -108,7 +111,6 @@ ret_status_t group_norm_gate_bwd(const void *x, const void *gate, const float *w
  *         are good to (10 + 2 z^2) and (8 + 2 |z|) 2^-24 of their value, gelu for a bf16 out to
  *         5.7e-6 (z >= -6; behind that it goes to zero and is off by less than 1e-13)
  *   workspace : linear_workspace_bytes() bytes (NULL where that is 0)
- * The query's size serves every call of the same M, N and K, whatever the others are.
  */
 enum { LINEAR_ACT_NONE = 0, LINEAR_ACT_GELU = 1, LINEAR_ACT_SILU = 2 };
 size_t linear_workspace_bytes(long long M, int N, int K);
