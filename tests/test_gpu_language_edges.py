@@ -1,6 +1,8 @@
-"""GPU tests of the operators around the layers (include/language.h) at the edges of what their calls take:
-row strides beyond 32 bits within a tile, beams whose scores are so far out that their tokens'
-scores meet, parameters that are not finite beside rows that do not count."""
+"""GPU tests of the operators around the layers (include/language.h) at the edges of what their calls take, and at the
+sizes that small calls do not reach: row strides beyond 32 bits within a tile, beams whose scores are so far out
+that their tokens' scores meet, rows that hold almost everything in one token, parameters that are not finite
+beside rows that do not count, activations far out, workgroups that take several tokens, full batches of a
+selection, a search whose beams end."""
 import math
 
 import pytest
@@ -9,6 +11,8 @@ import torch
 import retentive_network_scale_amd as rn
 from tests import _language_ref as ref
 from tests._recurrent_ref import assert_near
+from tests.test_gpu_language import _check_grads, _check_norm, _norm_case, _run_norm
+from tests.test_gpu_language_model import Search
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -39,6 +43,18 @@ def test_norm_rows_behind_an_end_have_no_gradient(gate, value):
         assert (got.dx.transpose(1, 2).cpu()[dead] == 0).all()
         assert not gate or (got.dgate.cpu()[dead] == 0).all()
     assert (got.dweight == 0).all() and (got.dbias == 0).all()
+
+
+@pytest.mark.parametrize("B,H,L,W", [(3, 64, 3500, 20), (2, 32, 2000, 100), (3, 64, 220, 512), (5, 128, 31, 700)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_norm_many_tokens_a_workgroup(B, H, L, W, dt):
+    """Workgroups that take several tokens, one after the other: with lengths, so that tokens that count follow
+    ones that do not, and sums over tokens that stay in registers."""
+    v = _norm_case(B, H, L, W, dt, 35)
+    for lengths in (None, [L] + [(i * 7 + 3) * L // 29 if i % 2 else 0 for i in range(1, B)]):
+        out, g = _run_norm(v, lengths=lengths, out=torch.zeros(B, L, H * W, dtype=dt, device=DEV))
+        _check_norm(v, True, 1e-5, lengths, out, "many")
+        _check_grads(v, True, 1e-5, lengths, g, "many")
 
 
 # ------------------------------------------------------------------------------------ linear
@@ -167,3 +183,86 @@ def test_select_log_sum_of_equal_logits(V):
     """A row of one value is counted: its log-sum is log V, whatever the slices are, and the score is rounded once."""
     got = rn.beam_select(torch.full((1, 2, V), 3.25, device=DEV), torch.zeros(1, 2, device=DEV), 1)
     assert abs(got.scores.item() + math.log(V)) <= 2.0 ** -24 * math.log(V) + 1e-15
+
+
+def _check_sorted(z, cum, K, ended=None, eos=0):
+    """Against a stable sort of all continuations in 64 bits, on the GPU."""
+    got = rn.beam_select(z, cum, K, ended=ended, eos=eos)
+    B, W, V = z.shape
+    p = z.double() - z.double().amax(-1, keepdim=True)
+    p = p - torch.log(torch.exp(p).sum(-1, keepdim=True))
+    if ended is not None:
+        only = torch.where(torch.arange(V, device=DEV) == eos, 0.0, -math.inf).double()
+        p = torch.where(ended[..., None], only, p)
+    p = (cum.double()[..., None] + p).reshape(B, -1)
+    best, at = p.sort(dim=-1, descending=True, stable=True)
+    flat = got.parents.long() * V + got.tokens.long()
+    # a score is off by the log-sum's exponentials, at most (16 + 3 d) 2^-24, here with d below 25: 5.5e-6.  Neighbours
+    # of different beams that are nearer than twice that may change places; every other row has one answer
+    near = 1.1e-5
+    gap = best[:, :K] - best[:, 1:K + 1]
+    told = ((gap < 1e-9) | (gap > near) | gap.isnan()).all(-1)
+    assert told.sum() >= 0.8 * B and torch.equal(flat[told], at[told, :K])
+    assert (p.gather(1, flat)[~told] - best[~told, :K]).abs().max() <= near if not told.all() else True
+    assert all(len(set(row)) == K for row in flat.tolist())
+    off = (got.scores.double() - best[:, :K]).abs()
+    assert ((got.scores == best[:, :K]) | (off <= (91 + best[:, :K].abs()) * ref.U) | (~told[:, None] & (off <= 2 * near))).all()
+
+
+@pytest.mark.parametrize("B,W,V,K", [(16, 8, 8200, 8), (16, 8, 8192, 5), (11, 16, 16385, 12), (70, 2, 40001, 4), (8, 16, 24576, 33),
+                                     (20, 8, 8207, 40)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_select_full_batches(B, W, V, K, dt):
+    """Rows enough for 32 elements a thread: whole slices, ragged last ones, of odd lengths and strides, ended beams."""
+    z = (2.5 * _r(40, B, W, V + 1)).to(dt)[..., 1:] if V % 2 else (2.5 * _r(40, B, W, V)).to(dt)
+    z = z._base.to(DEV).as_strided(z.shape, z.stride(), z.storage_offset()) if V % 2 else z.to(DEV)
+    cum = -5 * torch.rand(B, W, generator=_gen(41)).to(DEV)
+    ended = (torch.rand(B, W, generator=_gen(42)) < 0.2).to(DEV)
+    _check_sorted(z, cum, K)
+    _check_sorted(z, cum, K, ended, V - 1)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("V,K", [(16385, 12), (20000, 50)])
+def test_select_full_batches_of_equal_logits(V, K, dt):
+    """More elements at the bound than there is room for, in whole slices and in the last: the lowest indices."""
+    B, W = 16, 16
+    z = torch.zeros(B, W, V, dtype=dt, device=DEV)
+    cum = torch.full((B, W), -1.5, device=DEV)
+    cum[3, 2], cum[4] = -1.0, -torch.rand(W, generator=_gen(43)).to(DEV)
+    z[5, 0, V - 3:], z[6, 0, :V - 3] = 1.0, -math.inf  # the best in the last slice; little but -inf
+    z[7, 0, ::2] = -0.0
+    got = rn.beam_select(z, cum, K)
+    for b in range(B):
+        first = {3: 2, 4: cum[4].argmax().item()}.get(b, 0)
+        row = [(first, v) for v in range(K)]
+        if b in (5, 6):
+            row = [(0, V - 3), (0, V - 2), (0, V - 1)] + [(1, v) for v in range(K - 3)]
+        assert list(zip(got.parents[b].tolist(), got.tokens[b].tolist())) == row, b
+
+
+# --------------------------------------------------------------------------------- generation
+def test_beam_search_with_ends():
+    """A search whose beams end while others go on: its end token is one that a beam takes at its third step."""
+    first = Search(31, 3, 4)
+    first.eos = 0  # never the best of these rows' tokens by accident: checked below
+    first.w_out[0] = 0
+    for _ in range(3):
+        first.step()
+    eos = first.history[1, 2, 2].item()
+    assert not first.ended.any()
+    own, plain = Search(31, 3, 4), Search(31, 3, 4)
+    own.eos = plain.eos = eos
+    own.w_out[0] = plain.w_out[0] = 0
+    plain.layer = own.layer
+    some = 0
+    for step in range(10):
+        own.step()
+        plain.plain_step()
+        assert torch.equal(own.history, plain.history), step
+        same = [torch.equal(getattr(own, k), getattr(plain, k)) for k in ("state", "pos", "ended")]
+        assert all(same), (step, same)
+        torch.testing.assert_close(own.scores, plain.scores, rtol=2e-6, atol=2e-5)
+        plain.scores.copy_(own.scores)
+        some += bool(own.ended[1].any()) and not bool(own.ended.all())
+    assert some > 0
