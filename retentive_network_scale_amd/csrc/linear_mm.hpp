@@ -7,7 +7,7 @@
 // Tiles of 64 k reach LDS by DMA, two to four in turn, so that one is filled while another is multiplied, and the
 // operands of the next matrix step are read from LDS while the present one's are multiplied.
 // Operands whose rows are not 16-byte aligned take the same way through registers (M 64, N 4096, K 2048 11.7 us,
-// K 2047 19.0; M 300, N 1001, K 999 12.0 against 7.9 for 1000 and 1000).
+// K 2047 20.0; M 300, N 1001, K 999 12.7 against 7.9 for 1000 and 1000).
 // Where there are too few tiles for the chip, k is cut, the parts' sums go to the workspace in
 // fp32, and a second launch joins them in order and finishes.
 //
@@ -38,7 +38,7 @@ typedef __attribute__((address_space(3))) void lds_void;
 //     were slower with it, 296 -> 321 us, and 64 have no chunks for it).
 //
 // DMA: 16-byte chunks straight to LDS.  WIDE: the same chunks at any address through registers, DEPTH tiles under
-// way (M 300, N 1001, K 999 with a branch around each row's end and one tile: 21.8 us, without and with four: 12.0).
+// way (M 300, N 1001, K 999 with a branch around each row's end and one tile: 21.8 us, without and with four: 12.7).
 // SINGLE: element by element, for rows of fewer than 8.
 enum Way { DMA, WIDE, SINGLE };
 template <int R, bool KROWS, int NT, Way WAY, int DEPTH>
