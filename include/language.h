@@ -122,8 +122,8 @@ ret_status_t linear(const void *x, const void *w, const void *bias, const void *
 /*
  * Its gradients for d_o ([M, N] bf16, dense) and the forward call's pre:
  *   dz = d_o act'(pre)     dx = dz w     dw = dz^T x     dbias = sum_m dz
- * (the residual's gradient is d_o; gelu' is good to 3.2e-8, absolute).  dz is rounded to bf16 for the two products, as their
- * operands are bf16; dbias sums it unrounded.
+ * (the residual's gradient is d_o; gelu' is good to 3.2e-8, absolute).  dz is rounded to bf16
+ * for the two products, as their operands are bf16; dbias sums it unrounded.
  *   pre : [M, N] bf16 (not read without an activation)
  *   dx : [M, K], dw : [N, K] out_dtype      dbias : [N] fp32     each NULL where not wanted
  */

@@ -185,7 +185,7 @@ def beam_select(logits, scores, K, ended=None, eos=0, workspace=None, stream=Non
     logits [B, W, V] bf16 or fp32 (rows of a wider tensor are read in place), scores [B, W] fp32,
     ended [B, W] bool or None (a beam that has ended offers eos at its own score).  Returns a
     BeamSelection: tokens and parents int32 [B, K], scores fp32 [B, K], best first, ties to the
-    lowest beam and token."""
+    lowest beam, in it by logit and then to the lowest token."""
     call = _Call(logits, "logits", stream)
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
